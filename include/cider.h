@@ -65,7 +65,8 @@ typedef enum {
   CIDER_ERR_MISALIGNED = 2,
   CIDER_ERR_UNSUPPORTED_DEVICE = 3,
   CIDER_ERR_CUDA = 4,
-  CIDER_ERR_TIMEOUT = 5
+  CIDER_ERR_TIMEOUT = 5,
+  CIDER_ERR_INDEX = 6
 } cider_status_t;
 
 typedef enum { CIDER_PER_CHANNEL = 0, CIDER_PER_GROUP = 1 } cider_granularity_t;
@@ -239,6 +240,142 @@ cider_status_t cider_w4a8_linear_ex(const void* x, int x_dtype, int64_t M, int64
                                     const uint8_t* qw_packed, const float* sw, int granularity,
                                     int group_size, void* y, int y_dtype, void* stream);
 
+/* ------------------------------------------- quantized key/value cache
+ *
+ * A paged cache of attention keys and values in this library's symmetric
+ * INT8 / INT4 form, for serving the models whose linears run above, and the
+ * operators of one speculative decoding step over it: write (append), read
+ * back, attend, verify the drafted tokens, keep the accepted ones (compact).
+ * The Cider README has no counterpart.
+ *
+ * A row is one token's key (or value) of one key/value head, D = head_dim
+ * values.  Its scale is fp32 s = max|x| / 127 (bits 8) or max|x| / 7 (bits 4),
+ * IEEE divide, 1 for an all-zero row; its codes are rint(x / s), ties to even,
+ * the quotient in fp32.  The value it stands for is code * s.  Two INT4 codes
+ * share a byte as in the weights: element 2j in the low nibble.
+ *
+ * Layouts, dense, of one allocation for all layers:
+ *   k, v              int8 [layers, pages, heads, page_size, D], or
+ *                     uint8 [layers, pages, heads, page_size, D / 2]
+ *   k_scale, v_scale  fp32 [layers, pages, heads, page_size]
+ * A position p of request b lies in page table[b, p / page_size], row
+ * p % page_size; its slot is page * page_size + row.  Table entries past a
+ * request's last page are not read.  head_dim is 64 or 128, page_size 16, 32,
+ * 64 or 128, bits 8 or 4; the four pointers are aligned to 16 bytes.
+ *
+ * Checks on the host, in this order: an empty problem (no layers, pages,
+ * tokens or requests) returns CIDER_OK; null pointers, negative or unsupported
+ * sizes give CIDER_ERR_INVALID_ARGUMENT; alignment (16 bytes for 16-bit
+ * matrices and the cache, 8 for int64, 4 for int32 and fp32)
+ * CIDER_ERR_MISALIGNED; the device CIDER_ERR_UNSUPPORTED_DEVICE.  What only the
+ * device knows is checked by the kernels: a page, slot, offset, length, count
+ * or token outside of the call's sizes is skipped, never followed, and
+ * reported as CIDER_ERR_INDEX by cider_check_device_error. */
+typedef struct {
+  void* k;
+  float* k_scale;
+  void* v;
+  float* v_scale;
+  int64_t layers, pages;
+  int32_t heads, page_size, head_dim, bits;
+} cider_kv_cache_t;
+
+/* Quantizes keys and values and writes them into one layer of the cache.
+ *   k, v    [tokens, heads, D] of dtype (CIDER_F16 or CIDER_BF16); a token's
+ *           heads are dense, k_stride / v_stride elements lie between tokens
+ *           (multiples of 8, at least heads * D), so slices of one projection's
+ *           output serve as they are
+ *   slots   int64 [tokens]: page * page_size + row; negative: the token is not
+ *           written.  No two tokens share a slot.
+ * tokens * heads is below 2^31. */
+cider_status_t cider_kv_append(const cider_kv_cache_t* cache, int64_t layer, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, int dtype,
+                               const int64_t* slots, int64_t tokens, void* stream);
+
+/* Reads rows back: code * s in fp32, rounded once to dtype.
+ *   layer    the layer, or -1 for all
+ *   table    int32 [requests, table_width]
+ *   starts   int32 [requests]; offsets int32 [requests + 1], increasing from 0:
+ *            output token i with offsets[b] <= i < offsets[b + 1] is request
+ *            b's position starts[b] + i - offsets[b]
+ *   k, v     [tokens, heads, D] of dtype ([layers, tokens, heads, D] for layer
+ *            -1).  A token that belongs to no request, or whose page is out of
+ *            range, reads as zeros and is reported. */
+cider_status_t cider_kv_read(const cider_kv_cache_t* cache, int64_t layer, const int32_t* table,
+                             int64_t table_width, const int32_t* starts, const int32_t* offsets,
+                             int64_t requests, int64_t tokens, void* k, void* v, int dtype,
+                             void* stream);
+
+/* Moves rows within each request, in every layer: position starts[b] + path[b, i]
+ * to starts[b] + i for i < kept[b], all rows read before any is written (the
+ * accepted path of a verified tree moves up behind the context).
+ *   starts int32 [requests]; kept int32 [requests] (0: nothing moves);
+ *   path int32 [requests, path_width], path_width <= 64. */
+cider_status_t cider_kv_compact(const cider_kv_cache_t* cache, const int32_t* table,
+                                int64_t table_width, const int32_t* starts, const int32_t* path,
+                                int64_t path_width, const int32_t* kept, int64_t requests,
+                                void* stream);
+
+/* Attention of each request's last tokens over one layer of the cache, which
+ * holds their keys and values already.
+ *   q        [tokens, q_heads, D] of dtype, q_stride elements between tokens (a
+ *            multiple of 8, at least q_heads * D); q_heads is a multiple of the
+ *            cache's heads; query head h reads key/value head
+ *            h / (q_heads / heads)
+ *   lengths  int32 [requests]: positions in the cache, the new tokens included
+ *   offsets  int32 [requests + 1]: request b's new tokens are rows
+ *            offsets[b] .. offsets[b + 1]; they are its last positions.  At most
+ *            max_nodes (<= 64) of one request; none is allowed
+ *   tree     int64 [tokens]: bit j of token t's mask lets t see its request's
+ *            new token j; every token sees all positions before the new ones.
+ *            NULL: token t sees the new tokens 0 .. t (a chain, or one token)
+ *   scale    of q . k before the softmax (finite)
+ *   out      [tokens, q_heads, D] of dtype.  A token that sees no position gets
+ *            zeros; rows of a request whose offsets or length contradict the
+ *            call's sizes are not written.
+ * Products and sums are fp32; the weights of the values are rounded to fp16 with
+ * their sum taken before; the result is rounded once to dtype.  Scratch for the
+ * joined parts of long requests comes from the library's pool. */
+cider_status_t cider_tree_attention(const cider_kv_cache_t* cache, int64_t layer, const void* q,
+                                    int64_t q_stride, int dtype, int64_t tokens, int64_t q_heads,
+                                    const int32_t* table, int64_t table_width,
+                                    const int32_t* lengths, const int32_t* offsets,
+                                    int64_t requests, int64_t max_nodes, const int64_t* tree,
+                                    float scale, void* out, void* stream);
+
+/* Verifies drafted tokens against the target's probabilities.
+ *   logits   [nodes, vocab] of dtype, logits_stride elements between rows: the
+ *            target's logits at every node of every request's tree.  -inf is a
+ *            token that cannot be drawn
+ *   tokens   int32 [nodes]: a node's drafted token (node 0's is not read)
+ *   parents  int32 [nodes]: the node's parent, counted within its request;
+ *            parents come before their children (node 0's is not read)
+ *   offsets  int32 [requests + 1]: request b's nodes; node 0 is the last token
+ *            that is certain.  At most max_nodes (<= 64) of one request
+ *   uniforms fp32 [nodes] in [0, 1); noise fp32 [requests, vocab], exponential,
+ *            above 0
+ *   draft    fp32 [nodes, vocab] or NULL: row i is the distribution that node
+ *            i's children were drawn from, without replacement, in their order.
+ *            NULL: the drafts are certain (a drafter's best tokens)
+ *   temperature  fp32 [requests] or NULL (1); 0 or less takes the likeliest token
+ *   count    int32 [requests]: nodes on the accepted path, node 0 included
+ *            (0 for a request without nodes)
+ *   path     int32 [requests, max_nodes]: the accepted nodes, then -1
+ *   next     int32 [requests]: the token that follows the path (-1 without nodes)
+ * The current node's children are asked in increasing order.  With draft: the
+ * residual r starts as softmax(logits / temperature), Z = 1, Q = 1; a child with
+ * token x is accepted if u q(x) Z < r(x) Q; else r <- max(r / Z - q / Q, 0),
+ * Z <- sum r (both stay if that is 0), Q <- Q - q(x), q(x) <- 0.  Without: accepted
+ * if u Z < r(x); else Z <- Z - r(x), r(x) <- 0.  With no accepted child the next
+ * token is the lowest index of the largest r(x) / noise(x). */
+cider_status_t cider_verify_drafts(const void* logits, int64_t logits_stride, int dtype,
+                                   const int32_t* tokens, const int32_t* parents,
+                                   const int32_t* offsets, int64_t requests, int64_t nodes,
+                                   int64_t vocab, int64_t max_nodes, const float* uniforms,
+                                   const float* noise, const float* draft,
+                                   const float* temperature, int32_t* count, int32_t* path,
+                                   int32_t* next, void* stream);
+
 /* Size of the fixed scratch array used by cider_w8a8_linear_noalloc: 32 MiB
  * of device global memory per GPU on which the library has been used. */
 #define CIDER_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)
@@ -298,8 +435,10 @@ cider_status_t cider_trim_scratch_pool(int64_t keep_bytes, void* stream);
 /* Device-side error word shared by the library's kernels on the current
  * device.  Every wait inside a kernel is bounded; a wait that runs out sets
  * this word and the kernel returns early instead of hanging.  This call
- * synchronizes `stream`, reads and clears the word, and returns CIDER_OK or
- * CIDER_ERR_TIMEOUT (CIDER_ERR_CUDA if the synchronization itself fails). */
+ * synchronizes `stream`, reads and clears the word, and returns CIDER_OK,
+ * CIDER_ERR_TIMEOUT, or CIDER_ERR_INDEX when a kernel of the key/value cache or
+ * of the verification met a page, slot, offset, count or token outside of what
+ * it was given (CIDER_ERR_CUDA if the synchronization itself fails). */
 cider_status_t cider_check_device_error(void* stream);
 
 /* Test hook for the bounded-wait machinery: launches one CTA that waits on a

@@ -11,7 +11,9 @@ raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 import threading
 
 import torch
@@ -29,7 +31,8 @@ CIDER_F16 = 0
 CIDER_BF16 = 1
 _DTYPES = {torch.float16: CIDER_F16, torch.bfloat16: CIDER_BF16}
 STATUS_NAMES = {0: "CIDER_OK", 1: "CIDER_ERR_INVALID_ARGUMENT", 2: "CIDER_ERR_MISALIGNED",
-                3: "CIDER_ERR_UNSUPPORTED_DEVICE", 4: "CIDER_ERR_CUDA", 5: "CIDER_ERR_TIMEOUT"}
+                3: "CIDER_ERR_UNSUPPORTED_DEVICE", 4: "CIDER_ERR_CUDA", 5: "CIDER_ERR_TIMEOUT",
+                6: "CIDER_ERR_INDEX"}
 
 _lib = None
 _lock = threading.Lock()
@@ -72,6 +75,13 @@ def _declare(lib):
         "cider_debug_wait_timeout": ([i64, p], i32),
         "cider_debug_pair_schedule": ([i64, i64, i64, i32, i64, p, p, p], i32),
         "cider_debug_small_m_slices": ([i64, i64, i64, i32, i32, i32, p], i32),
+        "cider_kv_append": ([p, i64, p, i64, p, i64, i32, p, i64, p], i32),
+        "cider_kv_read": ([p, i64, p, i64, p, p, i64, i64, p, p, i32, p], i32),
+        "cider_kv_compact": ([p, p, i64, p, p, i64, p, i64, p], i32),
+        "cider_tree_attention": ([p, i64, p, i64, i32, i64, i64, p, i64, p, p, i64, i64, p,
+                                  ctypes.c_float, p, p], i32),
+        "cider_verify_drafts": ([p, i64, i32, p, p, p, i64, i64, i64, i64, p, p, p, p, p, p, p, p],
+                                i32),
         "cider_debug_small_m_launch": ([i64, i64, i64, i32, i32, i32, i32, p], i32),
     }
     for name, (args, res) in sig.items():
@@ -388,3 +398,187 @@ def cider_debug_small_m_slices(M: int, N: int, K: int, bits: int, group_size: in
            _load().cider_debug_small_m_slices(M, N, K, 1 if bits == 4 else 0, group_size,
                                               num_sms, ctypes.byref(out)))
     return int(out.value)
+
+
+# ------------------------------------------------- quantized key/value cache
+_CACHE = struct.Struct("@PPPPqqiiii")   # cider_kv_cache_t
+
+
+def cider_kv_cache(layers: int, pages: int, heads: int, head_dim: int, page_size: int = 64,
+                   bits: int = 8, device="cuda"):
+    """An empty paged cache: (k, k_scale, v, v_scale) with codes int8 [layers,
+    pages, heads, page_size, head_dim] (bits 8) or uint8 [..., head_dim / 2]
+    (bits 4) and scales fp32 [layers, pages, heads, page_size]."""
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    shape = (layers, pages, heads, page_size)
+    width, kind = (head_dim, torch.int8) if bits == 8 else (head_dim // 2, torch.uint8)
+    out = []
+    for _ in range(2):
+        out += [torch.zeros(shape + (width,), dtype=kind, device=device),
+                torch.ones(shape, dtype=torch.float32, device=device)]
+    return tuple(out)
+
+
+def _cache_args(cache):
+    """-> (cider_kv_cache_t as bytes, its device, heads, head_dim, layers)."""
+    k, ks, v, vs = cache
+    layers, pages, heads, page, width = k.shape
+    bits = 8 if k.dtype == torch.int8 else 4
+    if k.dtype not in (torch.int8, torch.uint8) or v.dtype != k.dtype:
+        raise TypeError("cache codes must be int8 or (packed INT4) uint8")
+    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError("cache scales must be float32")
+    if v.shape != k.shape or ks.shape != k.shape[:-1] or vs.shape != k.shape[:-1]:
+        raise ValueError("cache tensors do not match")
+    dim = width if bits == 8 else 2 * width
+    for t in (k, ks, v, vs):
+        if not t.is_cuda:
+            raise TypeError("cache must be CUDA tensors")
+        if not t.is_contiguous():
+            raise ValueError("cache must be contiguous")
+    return (_CACHE.pack(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), layers, pages,
+                        heads, page, dim, bits), k.device, heads, dim, layers)
+
+
+def _rows(t, name, heads, dim):
+    """dtype and token stride of a [tokens, heads, dim] tensor with dense heads."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the cache {heads} heads of {dim}")
+    n, h, d = t.shape
+    stride = t.stride()
+    if stride[2] != 1 or (h > 1 and stride[1] != d):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    return _DTYPES[t.dtype], stride[0] if n > 1 else h * d
+
+
+def _flat(t, dtype, name, *shape):
+    """A contiguous CUDA tensor of this type and shape (None: any size) -> its pointer."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def cider_kv_append(k, v, slots, cache, layer: int = 0) -> None:
+    """Quantize k, v [tokens, heads, D] (fp16 or bf16, any token stride) into
+    slots int64 [tokens] (page * page_size + row, negative: skip) of a layer."""
+    c, dev, heads, dim, _ = _cache_args(cache)
+    dt, ks = _rows(k, "k", heads, dim)
+    dv, vs = _rows(v, "v", heads, dim)
+    n = k.shape[0]
+    if dv != dt or v.shape[0] != n:
+        raise ValueError("k and v must have the same type and tokens")
+    sp = _flat(slots, torch.int64, "slots", n)
+    _check("cider_kv_append",
+           _load().cider_kv_append(c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n,
+                                   _raw_stream(dev)))
+
+
+def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float16, layer=None,
+                  out=None):
+    """-> (k, v) of `dtype` [tokens, heads, D] ([layers, tokens, heads, D] for
+    layer None): request b's positions starts[b], starts[b] + 1, ... for its
+    output rows offsets[b] .. offsets[b + 1]."""
+    c, dev, heads, dim, layers = _cache_args(cache)
+    n = starts.shape[0]
+    tp = _flat(table, torch.int32, "table", n, None)
+    sp = _flat(starts, torch.int32, "starts", n)
+    op = _flat(offsets, torch.int32, "offsets", n + 1)
+    shape = (tokens, heads, dim) if layer is not None else (layers, tokens, heads, dim)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be float16 or bfloat16")
+    if out is None:
+        # zeros where no request reads: nothing is launched for an empty problem
+        make = torch.empty if n and cache[0].shape[1] else torch.zeros
+        out = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
+    kp = _flat(out[0], dtype, "out[0]", *shape)
+    vp = _flat(out[1], dtype, "out[1]", *shape)
+    _check("cider_kv_read",
+           _load().cider_kv_read(c, -1 if layer is None else layer, tp, table.shape[1], sp, op, n,
+                                 tokens, kp, vp, _DTYPES[dtype], _raw_stream(dev)))
+    return out
+
+
+def cider_kv_compact(cache, table, starts, path, kept) -> None:
+    """In every layer, move request b's row at position starts[b] + path[b, i]
+    to starts[b] + i for i < kept[b]."""
+    c, dev, _, _, _ = _cache_args(cache)
+    n = starts.shape[0]
+    tp = _flat(table, torch.int32, "table", n, None)
+    sp = _flat(starts, torch.int32, "starts", n)
+    pp = _flat(path, torch.int32, "path", n, None)
+    kp = _flat(kept, torch.int32, "kept", n)
+    _check("cider_kv_compact",
+           _load().cider_kv_compact(c, tp, table.shape[1], sp, pp, path.shape[1], kp, n,
+                                    _raw_stream(dev)))
+
+
+def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree=None, scale=None,
+                         layer: int = 0, out=None):
+    """Attention of each request's last tokens q [tokens, q_heads, D] over its
+    cached positions (lengths int32 [requests], the new tokens included).
+    tree int64 [tokens]: which of its request's new tokens a token sees (None:
+    itself and the earlier ones).  -> out [tokens, q_heads, D] of q's type."""
+    c, dev, heads, dim, _ = _cache_args(cache)
+    dt, qs = _rows(q, "q", None, dim)
+    n, hq, _ = q.shape
+    b = lengths.shape[0]
+    tp = _flat(table, torch.int32, "table", b, None)
+    lp = _flat(lengths, torch.int32, "lengths", b)
+    op = _flat(offsets, torch.int32, "offsets", b + 1)
+    mp = _flat(tree, torch.int64, "tree", n) if tree is not None else None
+    if out is None:
+        out = torch.empty((n, hq, dim), dtype=q.dtype, device=dev)
+    yp = _flat(out, q.dtype, "out", n, hq, dim)
+    _check("cider_tree_attention",
+           _load().cider_tree_attention(c, layer, q.data_ptr(), qs, dt, n, hq, tp, table.shape[1],
+                                        lp, op, b, max_nodes, mp,
+                                        1.0 / math.sqrt(dim) if scale is None else scale, yp,
+                                        _raw_stream(dev)))
+    return out
+
+
+def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_nodes: int,
+                        draft_probs=None, temperature=None):
+    """Accept or reject each request's drafted tokens against the target's
+    logits [nodes, vocab] (fp16 or bf16, any row stride), with the given random
+    numbers.  -> (count int32 [requests], path int32 [requests, max_nodes],
+    next int32 [requests])."""
+    if not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in _DTYPES:
+        raise TypeError("logits must be float16 or bfloat16")
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [nodes, vocab] with contiguous rows")
+    n, vocab = logits.shape
+    b = offsets.shape[0] - 1
+    dev = logits.device
+    tp = _flat(tokens, torch.int32, "tokens", n)
+    pp = _flat(parents, torch.int32, "parents", n)
+    op = _flat(offsets, torch.int32, "offsets", None)
+    up = _flat(uniforms, torch.float32, "uniforms", n)
+    np_ = _flat(noise, torch.float32, "noise", b, vocab)
+    dp = _flat(draft_probs, torch.float32, "draft_probs", n, vocab) if draft_probs is not None else None
+    wp = _flat(temperature, torch.float32, "temperature", b) if temperature is not None else None
+    # one allocation: path, count, next
+    out = torch.empty((b * (max_nodes + 2),), dtype=torch.int32, device=dev)
+    path, count, nxt = out.split((b * max_nodes, b, b))
+    at = out.data_ptr()
+    _check("cider_verify_drafts",
+           _load().cider_verify_drafts(logits.data_ptr(), logits.stride(0) if n > 1 else vocab,
+                                       _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes,
+                                       up, np_, dp, wp, at + 4 * b * max_nodes,
+                                       at + 0, at + 4 * b * (max_nodes + 1), _raw_stream(dev)))
+    return count, path.view(b, max_nodes), nxt

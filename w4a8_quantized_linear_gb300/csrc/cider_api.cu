@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "cider.h"
+#include "cider_device.cuh"
 #include "cider_internal.h"
 
 namespace {
@@ -362,6 +363,7 @@ const char* cider_status_string(int status) {
     case CIDER_ERR_UNSUPPORTED_DEVICE: return "CIDER_ERR_UNSUPPORTED_DEVICE: current device is not sm_103";
     case CIDER_ERR_CUDA: return "CIDER_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     case CIDER_ERR_TIMEOUT: return "CIDER_ERR_TIMEOUT: a bounded wait inside a kernel gave up";
+    case CIDER_ERR_INDEX: return "CIDER_ERR_INDEX: a page, slot, offset or token on the device was out of range";
     default: return "unknown cider status";
   }
 }
@@ -625,7 +627,8 @@ cider_status_t cider_check_device_error(void* stream) {
       return cuda_status(cudaErrorUnknown);
     int v = 0;
     if (cider::read_and_clear_device_error(&v) != cudaSuccess) return cuda_status(cudaErrorUnknown);
-    return v ? CIDER_ERR_TIMEOUT : CIDER_OK;
+    if (v & cider::kDevErrTimeout) return CIDER_ERR_TIMEOUT;
+    return v ? CIDER_ERR_INDEX : CIDER_OK;
   });
 }
 

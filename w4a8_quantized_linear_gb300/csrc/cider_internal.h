@@ -138,6 +138,29 @@ cudaError_t device_error_word(int** ptr);
 constexpr uint64_t kKernelWaitTimeoutNs = 2000000000ull;
 cudaError_t launch_debug_wait_timeout(int64_t max_polls, cudaStream_t st);
 
+// kv_cache.cu, kv_attention.cu, verify.cu: the quantized key/value cache and
+// speculative decoding over it.  `err` is the device error word.
+struct KvCache;
+struct AttendArgs;
+cudaError_t launch_kv_append(const KvCache& c, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, bool bf16, const int64_t* slots, int64_t tokens,
+                             int* err, cudaStream_t st);
+cudaError_t launch_kv_read(const KvCache& c, int64_t layers, const int32_t* table,
+                           int64_t table_width, const int32_t* starts, const int32_t* offsets,
+                           int requests, int64_t tokens, void* k, void* v, bool bf16, int* err,
+                           int num_sms, cudaStream_t st);
+cudaError_t launch_kv_compact(const KvCache& c, int64_t layers, const int32_t* table,
+                              int64_t table_width, const int32_t* starts, const int32_t* path,
+                              int path_width, const int32_t* kept, int requests, int* err,
+                              cudaStream_t st);
+cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_verify(const void* logits, int64_t logits_stride, bool bf16,
+                          const int32_t* tokens, const int32_t* parents, const int32_t* offsets,
+                          int requests, int64_t nodes, int vocab, int max_nodes,
+                          const float* uniforms, const float* noise, const float* draft,
+                          const float* temperature, int32_t* count, int32_t* path, int32_t* next,
+                          int* err, int num_sms, cudaStream_t st);
+
 // ---------------------------------------------------------------- cider_api.cu
 // One linear / accumulator call, as the C entry points receive it.
 struct LinearArgs {
