@@ -18,6 +18,7 @@
 #include "cider_device.cuh"
 #include "cider_internal.h"
 #include "kv_common.cuh"
+#include "kv_parts.cuh"
 
 namespace cider {
 namespace {
@@ -105,10 +106,64 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attend_kernel(AttendArgs a) 
   }
 }
 
+// Share c begins within a unit and the share before it began the unit: adds the
+// unit's parts in the order of the shares and writes its rows.  One CTA of D
+// threads per (share, row).
+__global__ void join_kernel(AttendArgs a, PartsArgs parts, int ctas, int blocks, bool bf16) {
+  pdl_wait();
+  const int c = blockIdx.x, row = blockIdx.y, d = threadIdx.x, dim = blockDim.x;
+  if (c == 0) return;
+  const int64_t* info = parts.info + 4 * static_cast<int64_t>(c);
+  const int64_t begin = info[0], end = info[1];
+  if (begin < 0) return;
+  // the share before holds the unit's first tile unless it begins within it too
+  if (parts.info[4 * static_cast<int64_t>(c - 1)] == begin) return;
+  const Request r = request_of(a, static_cast<int>(info[2]), false);
+  const int group = a.q_heads / a.cache.heads;
+  const int unit = static_cast<int>(info[3]), head = unit / blocks, block = unit - head * blocks;
+  const int at = block * parts.rows + row;
+  if (at >= r.nodes * group) return;
+  // parts: the last slot of the share before, then the first slot of each share that begins within the unit
+  float top = -INFINITY, sum = 0.0f, o = 0.0f;
+  int last = c;
+  while (last + 1 < ctas && parts.info[4 * static_cast<int64_t>(last + 1)] == begin) ++last;
+  for (int j = c - 1; j <= last; ++j) {
+    const int64_t slot = 2 * static_cast<int64_t>(j) + (j == c - 1 ? 1 : 0);
+    top = fmaxf(top, parts.stat[slot * parts.rows + row].x);
+  }
+  for (int j = c - 1; j <= last; ++j) {
+    const int64_t slot = 2 * static_cast<int64_t>(j) + (j == c - 1 ? 1 : 0);
+    const float2 s = parts.stat[slot * parts.rows + row];
+    const float f = s.x == -INFINITY ? 0.0f : exp2f(s.x - top);
+    sum += s.y * f;
+    o += parts.out[(slot * parts.rows + row) * dim + d] * f;
+  }
+  (void)end;
+  const float v = sum > 0.0f ? o / sum : 0.0f;
+  const int node = at / group;
+  const int64_t dst = ((r.first + node) * a.q_heads + head * group + at - node * group) * dim + d;
+  static_cast<uint16_t*>(a.out)[dst] = bf16 ? y_bits<true>(v) : y_bits<false>(v);
+}
+
 }  // namespace
 
+cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, int blocks,
+                        bool bf16, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(static_cast<unsigned>(a.cache.head_dim));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, a, parts, ctas, blocks, bf16);
+}
+
 cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+  if (a.max_nodes * (a.q_heads / a.cache.heads) <= 32)
+    return launch_attend_rows(a, bf16, num_sms, st);
   const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>(a.q_heads));
   const bool wide = a.cache.head_dim == 128, b8 = a.cache.bits == 8;
   auto go = [&](auto t) {
