@@ -261,7 +261,8 @@ cider_status_t cider_w4a8_linear_ex(const void* x, int x_dtype, int64_t M, int64
  * A position p of request b lies in page table[b, p / page_size], row
  * p % page_size; its slot is page * page_size + row.  Table entries past a
  * request's last page are not read.  head_dim is 64 or 128, page_size 16, 32,
- * 64 or 128, bits 8 or 4; the four pointers are aligned to 16 bytes.
+ * 64 or 128, bits 8 or 4; pages * heads * page_size / 16 is below 2^31; the four
+ * pointers are aligned to 16 bytes.
  *
  * Checks on the host, in this order: an empty problem (no layers, pages,
  * tokens or requests) returns CIDER_OK; null pointers, negative or unsupported

@@ -42,6 +42,8 @@ cider_status_t check_cache(const cider_kv_cache_t& c) {
     return CIDER_ERR_INVALID_ARGUMENT;
   if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128)
     return CIDER_ERR_INVALID_ARGUMENT;
+  // 16-row blocks of a layer are counted in 32 bits
+  if (c.pages > kMaxDim / c.heads / (c.page_size / 16)) return CIDER_ERR_INVALID_ARGUMENT;
   if ((c.head_dim != 64 && c.head_dim != 128) || (c.bits != 8 && c.bits != 4))
     return CIDER_ERR_INVALID_ARGUMENT;
   return CIDER_OK;

@@ -31,6 +31,7 @@ struct Axis {
   int64_t unit_tiles;
   int64_t at, end;      // this CTA's current tile and the end of its share
   int64_t piece_begin, piece_end;   // tiles within the unit
+  int64_t total;        // tiles of the axis
   bool continued;       // the unit began in an earlier share
 
   __device__ static int64_t tiles_of(const Request& r, int tile) {
@@ -39,7 +40,7 @@ struct Axis {
   // Called by whole warps; blocks: row blocks per head.
   __device__ void begin(const AttendArgs& a, int tile, int lane, int blocks) {
     const int64_t units = static_cast<int64_t>(a.cache.heads) * blocks;
-    int64_t total = 0;
+    total = 0;
     for (int b0 = 0; b0 < a.requests; b0 += 32) {
       const int i = b0 + lane;
       if (i < a.requests) total += tiles_of(request_of(a, i, blockIdx.x == 0), tile) * units;
@@ -107,8 +108,13 @@ struct Axis {
 struct PartsArgs {
   float* out;       // [2 ctas][rows][D]
   float2* stat;     // [2 ctas][rows]: maximum (log2), sum
-  int64_t* info;    // [ctas][4]: of a share that begins within a unit, its unit's
-                    // first and end tile, request, unit; else first tile -1
+  // Of a share that begins within a unit: the unit's first and end tile on the
+  // axis, the axis' length, the request and the unit; else begin is -1.
+  struct Info {
+    int64_t begin, end, total;
+    int b, unit;
+  };
+  Info* info;       // [ctas]
   int rows;
 
   cudaError_t allocate(ScratchSource& scratch, int ctas, int rows_, int d) {
@@ -116,20 +122,17 @@ struct PartsArgs {
     const size_t o = static_cast<size_t>(2) * ctas * rows * d * 4;
     const size_t s = static_cast<size_t>(2) * ctas * rows * 8;
     void* p = nullptr;
-    if (scratch.get(o + s + static_cast<size_t>(ctas) * 32, &p) != CIDER_OK)
+    if (scratch.get(o + s + static_cast<size_t>(ctas) * sizeof(Info), &p) != CIDER_OK)
       return cudaErrorMemoryAllocation;
     out = static_cast<float*>(p);
     stat = reinterpret_cast<float2*>(static_cast<char*>(p) + o);
-    info = reinterpret_cast<int64_t*>(static_cast<char*>(p) + o + s);
+    info = reinterpret_cast<Info*>(static_cast<char*>(p) + o + s);
     return cudaSuccess;
   }
   __device__ void announce(const Axis& x) const {
-    int64_t* i = info + 4 * blockIdx.x;
     const bool mid = x.more() && x.continued;
-    i[0] = mid ? x.unit_begin : -1;
-    i[1] = mid ? x.unit_begin + x.unit_tiles : -1;
-    i[2] = mid ? x.b : 0;
-    i[3] = mid ? x.unit : 0;
+    info[blockIdx.x] = mid ? Info{x.unit_begin, x.unit_begin + x.unit_tiles, x.total, x.b, x.unit}
+                           : Info{-1, -1, 1, 0, 0};
   }
   __device__ void store(int slot, int row, int d_all, int d, const float4& v, float top,
                         float sum) const {

@@ -19,11 +19,9 @@
 // accumulator starts at -128 sum_d q_d 2^-24, which takes the offset out again
 // (magnitudes stay within 4x of the result's, in fp32).  Odd INT4 codes are
 // taken four bits up, 16 times as large, against q / 16.  q is first scaled by
-// a power of two per row so that it fits fp16 (bf16 reaches further).  For
+// a power of two so that it fits fp16 (bf16 reaches further).  For
 // p' . cv the offset would not stay small (it grows with the sum of the
-// weights while the values average out), so the value codes are centred: two
-// tokens' codes of one dimension are put in the mantissas of 1024 and the
-// offset subtracted, exactly.
+// weights while the values average out), so the value codes are centred, exactly.
 //
 // Layout: tokens are the tensor core's M (16), rows its N (8), so few rows
 // waste little and each code is converted once for all rows:
@@ -32,9 +30,9 @@
 // 16-byte chunks of a cached row and q is laid out to match.
 //
 // Bound: HBM (each code is read once; ~0.75 + 1.5 instructions a code).  Each
-// warp keeps its own ring of 16-position stages, filled by 16-byte asynchronous
+// warp keeps its own ring of stages of 16 or 32 positions, filled by 16-byte asynchronous
 // copies; there is no barrier in the loop.  The positions of all requests and
-// heads form one axis of 64-position tiles that is cut evenly over the resident
+// heads form one axis of tiles that is cut evenly over the resident
 // CTAs, on the device (only it knows the lengths): a request is cut where the
 // share of a CTA ends, its parts are joined by a second small kernel that is
 // launched as a programmatic dependent.  The shares depend on the lengths
@@ -56,29 +54,45 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSub = 16;               // positions per stage of a warp
-constexpr int kTile = kSub * kWarps;   // positions per tile of the axis
 
+// NB: blocks of 8 rows.
 template <int D, int BITS, int NB>
 struct RowsCfg {
+  static constexpr int kGroups = NB > 2 ? 1 : 2;            // groups of 16 positions per stage
+  static constexpr int kSub = 16 * kGroups;                 // positions per stage of a warp
+  static constexpr int kTile = kSub * kWarps;               // positions per tile of the axis
   static constexpr int kRowBytes = D * BITS / 8;
   static constexpr int kSide = kSub * kRowBytes;            // codes of K (or V) of a stage
   static constexpr int kStage = 2 * kSide + 2 * kSub * 4;   // and their scales
-  static constexpr int kStages = kRowBytes == 128 ? 4 : kRowBytes == 64 ? 6 : 8;
-  static constexpr int kRing = kStage * kStages;
   static constexpr int kRows = 8 * NB;
   static constexpr int kSteps = D / 16;                     // k-steps of q . ck, m-blocks of V^T
-  static constexpr int kQBytes = NB > 2 ? NB * kSteps * 32 * 8 : 0;
+  static constexpr bool kQInRegs = NB == 1;
+  static constexpr int kQBytes = kQInRegs ? 0 : NB * kSteps * 32 * 8;
   static constexpr int kOutBytes = kRows * D * 4;
   static constexpr int kStatBytes = kWarps * kRows * 8;
   static constexpr int kMaskBytes = kRows * 8;
-  static constexpr int kSmem = kWarps * kRing + kQBytes + kOutBytes + kStatBytes + kMaskBytes;
-  static constexpr int kCtas = NB > 2 ? 2 : 3;              // per SM
+  static constexpr int kScaleBytes = kWarps * kSub * 16;
+  static constexpr int kRest = kQBytes + kOutBytes + kStatBytes + kMaskBytes + kScaleBytes;
+  static constexpr int kCtas = NB == 1 || (NB == 2 && kRowBytes < 128) ? 3 : 2;   // per SM
+  // as many stages as the resident CTAs' shared memory holds, at most 6
+  static constexpr int kFit = (227 * 1024 / kCtas - 1024 - kRest) / (kWarps * kStage);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kRing = kStage * kStages;
+  static constexpr int kSmem = kWarps * kRing + kRest;
+  static_assert(kStages >= 2, "a stage is loaded while another is computed");
 };
 
+// d = a b + c, and the same with c = d.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -89,31 +103,40 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(valid ? 16 : 0)
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 16 bytes from src + SRC to dst + DST; bytes 0: zeros.
+template <int DST, int SRC>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0+%3], [%1+%4], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "n"(DST), "n"(SRC)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+// BYTES (4, 8 or 16) of a cached row from shared memory.
+template <int BYTES>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-
 // Where byte `o` of a stage's keys (values) is put: 16-byte chunks exchanged
 // within 128-byte lines so that the fragment loads below touch each bank once.
+// For the lanes' fixed pattern of rows and chunks the exchange is one xor that
+// is worked out once: every later address is that base plus a constant.
 template <int RB>
 __device__ __forceinline__ uint32_t swz_k(uint32_t o) {
   if constexpr (RB == 128) return o ^ ((o >> 7 & 1) << 6);
@@ -137,61 +160,60 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t u) {
   return h;
 }
 
-// Centred fp16 pairs (token a, token b) of the dims in the words wa, wb: four
-// INT8 codes or eight INT4 codes each, in order.
+// Centred fp16 pairs (token a, token b), times 2^-9, of the dims in the words
+// wa, wb: four INT8 codes or eight INT4 codes each, in order.  A code plus 128
+// (plus 8) as an fp16 subnormal is (code + 128) 2^-24; one fp16 FMA lifts it by
+// 2^15 and takes 128 2^-9 off, exactly (INT4 codes four bits up: 2^11).  Each
+// mask is then a single-constant operation: with the codes put under the
+// exponent of 1024 instead, a third of this loop was moves of constants.
 template <int BITS>
 __device__ __forceinline__ void value_pairs(uint32_t wa, uint32_t wb, uint32_t* out) {
+  const __half2 lift = bits_h2(0x78007800u);      // 2^15
+  const __half2 lift_hi = bits_h2(0x68006800u);   // 2^11
+  const __half2 off = bits_h2(BITS == 8 ? 0xB400B400u : 0xA400A400u);   // -128 2^-9, -8 2^-9
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const uint32_t x = __byte_perm(wa, wb, half == 0 ? 0x5410u : 0x7632u);
+    const uint32_t x = __byte_perm(wa, wb, half == 0 ? 0x5410u : 0x7632u) ^ (BITS == 8 ? 0x80808080u : 0x88888888u);
+    const uint32_t y = x >> 8;
     if constexpr (BITS == 8) {
-      const __half2 bias = bits_h2(0x64806480u);   // 1152
-      const uint32_t y = x >> 8;
-      out[2 * half] = h2_bits(__hsub2(bits_h2((x & 0x00FF00FFu) ^ 0x64806480u), bias));
-      out[2 * half + 1] = h2_bits(__hsub2(bits_h2((y & 0x00FF00FFu) ^ 0x64806480u), bias));
+      out[2 * half] = h2_bits(__hfma2(bits_h2(x & 0x00FF00FFu), lift, off));
+      out[2 * half + 1] = h2_bits(__hfma2(bits_h2(y & 0x00FF00FFu), lift, off));
     } else {
-      const __half2 bias_lo = bits_h2(0x64086408u);       // 1032
-      const __half2 sixteenth = bits_h2(0x2C002C00u);
-      const __half2 bias_hi = bits_h2(0xD480D480u);       // -72
-      const uint32_t y = x >> 8;
-      out[4 * half] = h2_bits(__hsub2(bits_h2((x & 0x000F000Fu) ^ 0x64086408u), bias_lo));
-      out[4 * half + 1] = h2_bits(__hfma2(bits_h2((x & 0x00F000F0u) ^ 0x64806480u), sixteenth, bias_hi));
-      out[4 * half + 2] = h2_bits(__hsub2(bits_h2((y & 0x000F000Fu) ^ 0x64086408u), bias_lo));
-      out[4 * half + 3] = h2_bits(__hfma2(bits_h2((y & 0x00F000F0u) ^ 0x64806480u), sixteenth, bias_hi));
+      out[4 * half] = h2_bits(__hfma2(bits_h2(x & 0x000F000Fu), lift, off));
+      out[4 * half + 1] = h2_bits(__hfma2(bits_h2(x & 0x00F000F0u), lift_hi, off));
+      out[4 * half + 2] = h2_bits(__hfma2(bits_h2(y & 0x000F000Fu), lift, off));
+      out[4 * half + 3] = h2_bits(__hfma2(bits_h2(y & 0x00F000F0u), lift_hi, off));
     }
   }
 }
 
-// One row of q for this lane: fp16 pairs in the order of the key fragments,
-// the sum of all its values (over the row's four lanes) and 2^-k of its scaling.
+// This lane's D / 4 values of a row of q, in the order of the key fragments:
+// INT8 the 16-byte chunks t, t + 4 of the cached row (16 dims each), INT4 a
+// quarter of the row.
 template <int D, int BITS>
-__device__ __forceinline__ void query_row(const AttendArgs& a, bool bf16, const uint16_t* q, bool have,
-                                          int t, uint32_t (&frag)[D / 16][2], float& sum, float& unscale) {
-  constexpr int kPer = D / 4;   // values per lane
-  float f[kPer];
-  // a lane's values: INT8 16-byte chunks t, t + 4 of the cached row (16 dims
-  // each); INT4 a quarter of the row
+__device__ __forceinline__ void query_load(const uint16_t* q, bool have, int t, uint4 (&w)[D / 32]) {
 #pragma unroll
-  for (int i = 0; i < kPer; i += 8) {
-    const int d = BITS == 8 ? (t + 4 * (i / 16)) * 16 + i % 16 : t * kPer + i;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (have) w = *reinterpret_cast<const uint4*>(q + d);
-    float e[8];
-    if (bf16) widen8<__nv_bfloat16>(w, e); else widen8<__half>(w, e);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[i + j] = e[j];
+  for (int i = 0; i < D / 4; i += 8) {
+    const int d = BITS == 8 ? (t + 4 * (i / 16)) * 16 + i % 16 : t * (D / 4) + i;
+    w[i / 8] = have ? *reinterpret_cast<const uint4*>(q + d) : make_uint4(0, 0, 0, 0);
   }
-  float top = 0.0f;
+}
+template <int D>
+__device__ __forceinline__ void query_values(bool bf16, const uint4 (&w)[D / 32], float (&f)[D / 4]) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(f[i]));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // the largest value to [2^13, 2^14)
-  int k = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-  k = top == 0.0f ? 0 : max(-126, min(k, 126));
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-  unscale = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  sum = 0.0f;
+  for (int i = 0; i < D / 32; ++i) {
+    float e[8];
+    if (bf16) widen8<__nv_bfloat16>(w[i], e); else widen8<__half>(w[i], e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[8 * i + j] = e[j];
+  }
+}
+
+// Those values times `up` as fp16 pairs per k-step, and the row's sum (over its four lanes).
+template <int D, int BITS>
+__device__ __forceinline__ float query_frags(const float (&f)[D / 4], float up,
+                                             uint32_t (&frag)[D / 16][2]) {
+  float sum = 0.0f;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     __half2 lo, hi;
@@ -211,6 +233,7 @@ __device__ __forceinline__ void query_row(const AttendArgs& a, bool bf16, const 
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  return sum;
 }
 
 template <int D, int BITS, int NB>
@@ -218,71 +241,112 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
     rows_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
   using C = RowsCfg<D, BITS, NB>;
   constexpr int RB = C::kRowBytes;
-  constexpr bool kQInRegs = NB <= 2;
+  constexpr int G = C::kGroups;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
-  uint2* q_smem = reinterpret_cast<uint2*>(smem + kWarps * C::kRing);
-  float* out_smem = reinterpret_cast<float*>(smem + kWarps * C::kRing + C::kQBytes);
-  float2* stat_smem = reinterpret_cast<float2*>(smem + kWarps * C::kRing + C::kQBytes + C::kOutBytes);
-  uint64_t* mask_smem = reinterpret_cast<uint64_t*>(smem + kWarps * C::kRing + C::kQBytes +
+  const uint8_t* const ring = smem + warp * C::kRing;
+  // copies: chunks lane, lane + 32, ...; 32 chunks further are 4, 8 or 16 rows
+  const uint32_t copy_k = smem_u32(ring) + swz_k<RB>(lane * 16);
+  const uint32_t copy_v = smem_u32(ring) + C::kSide + swz_v<RB>(lane * 16);
+  const uint32_t copy_s = smem_u32(ring) + 2 * C::kSide + (lane >> 2 & 1) * C::kSub * 4 + (lane & 3) * 16;
+  const float* const scale_src = (lane < 4 ? a.cache.k_scale : a.cache.v_scale) + (lane & 3) * 4;
+  // fragments: keys of row g, chunk t; values of rows 2 t and 2 t + 1, D / 8 dims from D / 8 g
+  constexpr int kChunk = RB / 4 < 16 ? RB / 4 : 16;   // bytes of one load of a key
+  constexpr int kBytes = RB / 8;                      // of a value row per lane
+  const uint32_t frag_k = swz_k<RB>(g * RB + t * kChunk);
+  const uint32_t frag_v0 = C::kSide + swz_v<RB>(2 * t * RB + g * kBytes);
+  const uint32_t frag_v1 = C::kSide + swz_v<RB>((2 * t + 1) * RB + g * kBytes);
+  uint8_t* rest = smem + kWarps * C::kRing;
+  float4* scale_smem = reinterpret_cast<float4*>(rest) + warp * C::kSub;
+  uint2* q_smem = reinterpret_cast<uint2*>(rest + C::kScaleBytes);
+  float* out_smem = reinterpret_cast<float*>(rest + C::kScaleBytes + C::kQBytes);
+  float2* stat_smem = reinterpret_cast<float2*>(rest + C::kScaleBytes + C::kQBytes + C::kOutBytes);
+  uint64_t* mask_smem = reinterpret_cast<uint64_t*>(rest + C::kScaleBytes + C::kQBytes +
                                                     C::kOutBytes + C::kStatBytes);
   const int group = a.q_heads / a.cache.heads;
 
   Axis axis;
-  axis.begin(a, kTile, lane, 1);
+  axis.begin(a, C::kTile, lane, 1);
   bool more = axis.more();
   if (threadIdx.x == 0) parts.announce(axis);
 
   // copies of the piece whose loads are in flight
-  int subs = 0;               // stages of this warp in the piece
-  int32_t ids = -1;           // lane l: the page of stage l, l + 32, ... of this warp
-  int ids_base = 0;
-  int64_t first_sub = 0;
+  int subs = 0;                 // stages of this warp in the piece
+  int first_pos = 0;            // position of its first stage; kTile further each
+  int last_pos = 0;             // the piece's positions end here
+  int rows32 = -1, next32 = -1;   // lane l: the cache row / 16 of 16 positions, -1 without a page
+  int load_slot = 0;            // byte offset of the slot that the next copy fills
   const int32_t* table = nullptr;
-  int head = 0;
-  auto load_ids = [&](int base) {
-    ids_base = base;
-    const int s = base + lane;
-    ids = -1;
-    if (s < subs) {
-      const int64_t pos = (first_sub + static_cast<int64_t>(s) * kWarps) * kSub;
-      const int32_t id = table[pos >> a.cache.page_shift];
-      if (id >= 0 && id < a.cache.pages) ids = id; else atomicOr(a.err, kDevErrIndex);
+  const int page16 = a.cache.page_shift - 4;
+  // the row of the i-th 16 positions of this warp (G to a stage)
+  auto load_rows16 = [&](int i) -> int {
+    const int pos = first_pos + (i / G) * C::kTile + (i % G) * 16;
+    if (i >= subs * G || pos >= last_pos) return -1;
+    const int32_t id = table[pos >> a.cache.page_shift];
+    if (id < 0 || id >= a.cache.pages) {
+      atomicOr(a.err, kDevErrIndex);
+      return -1;
     }
+    return ((id * a.cache.heads + axis.unit) << page16) + ((pos >> 4) & ((1 << page16) - 1));
   };
-  auto copy = [&](int s) {   // stage s of this warp into its slot
+  // a page holds at least 16 positions, and 16 positions of a stage lie in one;
+  // row numbers are loaded 32 at a time, 16 copies before their first use
+  auto copy = [&](int s) {   // stage s of this warp into the next slot
     if (s < subs) {
-      if (s >= ids_base + 32) load_ids(ids_base + 32);
-      const int32_t id = __shfl_sync(0xffffffffu, ids, s - ids_base);
-      const int64_t pos = (first_sub + static_cast<int64_t>(s) * kWarps) * kSub;
-      const int64_t row = a.cache.row(id < 0 ? 0 : id, head,
-                                      static_cast<int>(pos & ((1 << a.cache.page_shift) - 1)));
-      const uint32_t dst = ring + (s % C::kStages) * C::kStage;
-      const uint8_t* k = a.cache.k + row * RB;
-      const uint8_t* v = a.cache.v + row * RB;
 #pragma unroll
-      for (int c = lane; c < C::kSide / 16; c += 32) {
-        cp_async16(dst + swz_k<RB>(c * 16), k + c * 16, id >= 0);
-        cp_async16(dst + C::kSide + swz_v<RB>(c * 16), v + c * 16, id >= 0);
+      for (int u = 0; u < G; ++u) {
+        const int i = s * G + u;
+        if ((i & 15) == 0 && u == 0) {
+          if ((i & 31) == 0 && i > 0) rows32 = next32;
+          if ((i & 31) == 16) next32 = load_rows16(i + 16 + lane);
+        }
+        const int row = __shfl_sync(0xffffffffu, rows32, i & 31);
+        const int bytes = row >= 0 ? 16 : 0;
+        const int64_t at = max(row, 0);
+        const uint8_t* k = a.cache.k + at * (16 * RB) + lane * 16;
+        const uint8_t* v = a.cache.v + at * (16 * RB) + lane * 16;
+        const uint32_t dk = copy_k + load_slot, dv = copy_v + load_slot;
+        if constexpr (RB == 128) {
+          cp_async16<0, 0>(dk + u * 2048, k, bytes);
+          cp_async16<512, 512>(dk + u * 2048, k, bytes);
+          cp_async16<1024, 1024>(dk + u * 2048, k, bytes);
+          cp_async16<1536, 1536>(dk + u * 2048, k, bytes);
+          // 4 rows further the values' exchange has its upper bit turned round
+          cp_async16<0, 0>(dv + u * 2048, v, bytes);
+          cp_async16<512, 512>((dv ^ 64) + u * 2048, v, bytes);
+          cp_async16<1024, 1024>(dv + u * 2048, v, bytes);
+          cp_async16<1536, 1536>((dv ^ 64) + u * 2048, v, bytes);
+        } else if constexpr (RB == 64) {
+          cp_async16<0, 0>(dk + u * 1024, k, bytes);
+          cp_async16<512, 512>(dk + u * 1024, k, bytes);
+          cp_async16<0, 0>(dv + u * 1024, v, bytes);
+          cp_async16<512, 512>(dv + u * 1024, v, bytes);
+        } else {
+          cp_async16<0, 0>(dk + u * 512, k, bytes);
+          cp_async16<0, 0>(dv + u * 512, v, bytes);
+        }
+        if (lane < 8) cp_async16<0, 0>(copy_s + load_slot + u * 64, scale_src + at * 16, bytes);
       }
-      if (lane < 8) {
-        const float* s4 = (lane < 4 ? a.cache.k_scale : a.cache.v_scale) + row + (lane & 3) * 4;
-        cp_async16(dst + 2 * C::kSide + lane * 16, s4, id >= 0);
-      }
+      load_slot = load_slot + C::kStage == C::kRing ? 0 : load_slot + C::kStage;
     }
     cp_async_commit();
   };
+  auto q_row = [&](int r, bool have) {
+    const int node = have ? r / group : 0;
+    return static_cast<const uint16_t*>(a.q) + (axis.req.first + node) * a.q_stride +
+           static_cast<int64_t>(axis.unit * group + (have ? r - node * group : 0)) * D;
+  };
+  uint4 q_raw[C::kQInRegs ? D / 32 : 1];   // a single block of rows is loaded ahead too
   auto start = [&]() {   // the loads of the axis' current piece
-    const int64_t tiles = axis.piece_end - axis.piece_begin;
-    const int64_t length = axis.req.length;
-    first_sub = axis.piece_begin * kWarps + warp;
-    const int64_t all = (length + kSub - 1) / kSub;
-    const int64_t end = min((axis.piece_begin + tiles) * kWarps, all);
-    subs = first_sub < end ? static_cast<int>((end - first_sub + kWarps - 1) / kWarps) : 0;
+    const int64_t begin = axis.piece_begin * C::kTile + warp * C::kSub;
+    const int64_t end = min(axis.piece_end * C::kTile, axis.req.length);
+    subs = begin < end ? static_cast<int>((end - begin + C::kTile - 1) / C::kTile) : 0;
+    first_pos = static_cast<int>(begin);
+    last_pos = static_cast<int>(end);
     table = a.table + axis.b * a.table_width;
-    head = axis.unit;
-    load_ids(0);
+    load_slot = 0;
+    rows32 = load_rows16(lane);
+    if constexpr (C::kQInRegs) query_load<D, BITS>(q_row(g, g < axis.req.nodes * group), g < axis.req.nodes * group, t, q_raw);
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) copy(s);
   };
@@ -291,12 +355,12 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
   while (more) {
     // ------------------------------------------------------ the piece's rows
     const Request req = axis.req;
-    const int64_t context = req.context, length = req.length;
+    const int context = static_cast<int>(req.context);
     const int rows = req.nodes * group;
     const int my_subs = subs;
-    const int64_t my_first = first_sub;
-    uint32_t qf[kQInRegs ? NB : 1][C::kSteps][2];
-    float start_s[NB][2], mul[NB][2];
+    int pos = first_pos;
+    uint32_t qf[C::kQInRegs ? C::kSteps : 1][2];
+    float start_s[NB][2];
     if (threadIdx.x < C::kRows) {
       const int node = threadIdx.x / group;
       uint64_t m = 0;
@@ -304,30 +368,52 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
         m = a.tree ? static_cast<uint64_t>(a.tree[req.first + node]) : ~0ull >> (63 - node);
       mask_smem[threadIdx.x] = m;
     }
+    // one power of two for all rows puts the largest value in [2^13, 2^14):
+    // what a smaller row loses is 2^-38 of it, absolutely
+    float top = 0.0f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = nb * 8 + g;
-      const bool have = r < rows;
-      const int node = have ? r / group : 0;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (req.first + node) * a.q_stride +
-                          static_cast<int64_t>(axis.unit * group + (have ? r - node * group : 0)) * D;
-      float sum, unscale;
+      uint4 w[D / 32];
+      float f[D / 4];
+      if constexpr (C::kQInRegs) {
+        query_values<D>(bf16, q_raw, f);
+      } else {
+        query_load<D, BITS>(q_row(r, r < rows), r < rows, t, w);
+        query_values<D>(bf16, w, f);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(f[i]));
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    int lift = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+    lift = top == 0.0f ? 0 : max(-126, min(lift, 126));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + lift) << 23);
+    // 2^24 of the subnormals, and the scaling of q, taken out again
+    const float mul = a.scale * 1.44269504f * 16777216.0f *
+                      __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = nb * 8 + g;
+      uint4 w[D / 32];
+      float f[D / 4];
+      if constexpr (C::kQInRegs) {
+        query_values<D>(bf16, q_raw, f);
+      } else {
+        query_load<D, BITS>(q_row(r, r < rows), r < rows, t, w);
+        query_values<D>(bf16, w, f);
+      }
       uint32_t frag[C::kSteps][2];
-      query_row<D, BITS>(a, bf16, q, have, t, frag, sum, unscale);
-      // 2^24 of the subnormals; 24 - k stays an exponent: k >= -100 but for
-      // rows that reach past 2^113, where the product overflows anyway
-      const float m = a.scale * 1.44269504f * 16777216.0f * unscale;
+      const float sum = query_frags<D, BITS>(f, up, frag);
       const float off = -(BITS == 8 ? 128.0f : 8.0f) * 0x1p-24f * sum;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mul[nb][e] = __shfl_sync(0xffffffffu, m, (2 * t + e) * 4);
-        start_s[nb][e] = __shfl_sync(0xffffffffu, off, (2 * t + e) * 4);
-      }
-      if constexpr (kQInRegs) {
+      for (int e = 0; e < 2; ++e) start_s[nb][e] = __shfl_sync(0xffffffffu, off, (2 * t + e) * 4);
+      if constexpr (C::kQInRegs) {
 #pragma unroll
         for (int s = 0; s < C::kSteps; ++s) {
-          qf[nb][s][0] = frag[s][0];
-          qf[nb][s][1] = frag[s][1];
+          qf[s][0] = frag[s][0];
+          qf[s][1] = frag[s][1];
         }
       } else if (nb % kWarps == warp) {
 #pragma unroll
@@ -353,87 +439,103 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
       }
     }
 
-    for (int s = 0; s < my_subs; ++s) {
+    const uint8_t* st = ring;
+    for (int s = 0; s < my_subs; ++s, pos += C::kTile) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();
       copy(s + C::kStages - 1);
-      const uint32_t st = ring + (s % C::kStages) * C::kStage;
+      // each position's scales once: sk, log2 sv, 1 / sv
+      if (C::kSub == 32 || lane < C::kSub) {
+        const float sk = reinterpret_cast<const float*>(st + 2 * C::kSide)[lane];
+        const float sv = reinterpret_cast<const float*>(st + 2 * C::kSide)[C::kSub + lane];
+        const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        scale_smem[lane] = make_float4(sk * mul, log2_approx(kept),
+                                       kept > 0.0f && kept < INFINITY ? rcp_approx(kept) : 0.0f, 0.0f);
+      }
       // -------------------------------------------------- S^T = K Q^T
-      float x[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nb][e] = start_s[nb][e & 1];
-      constexpr int kChunk = RB / 4 < 16 ? RB / 4 : 16;   // bytes of one load
+      float x[NB][G][4];
 #pragma unroll
       for (int c = 0; c < RB / 4 / kChunk; ++c) {
-        uint32_t wa[4], wb[4];
-        const uint32_t oa = g * RB + (t + 4 * c) * kChunk, ob = oa + 8 * RB;
-        if constexpr (kChunk == 16) {
-          const uint4 u = lds128(st + swz_k<RB>(oa)), v = lds128(st + swz_k<RB>(ob));
-          wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
-          wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
-        } else {
-          const uint2 u = lds64(st + oa), v = lds64(st + ob);
-          wa[0] = u.x; wa[1] = u.y;
-          wb[0] = v.x; wb[1] = v.y;
-        }
+        uint32_t w[G][2][kChunk / 4];
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            // INT8, D 128: the second 64 bytes of a row are the exchange's own bit
+            load_words<kChunk>(st + (c == 0 ? frag_k : frag_k ^ 64) + (u * 16 + 8 * h) * RB, w[u][h]);
 #pragma unroll
         for (int i = 0; i < kChunk / 4; ++i) {
           constexpr int kPerWord = BITS == 8 ? 1 : 2;   // k-steps
 #pragma unroll
           for (int e = 0; e < kPerWord; ++e) {
-            uint32_t f[4];
-            if constexpr (BITS == 8) {
-              const uint32_t u = wa[i] ^ 0x80808080u, v = wb[i] ^ 0x80808080u;
-              f[0] = u & 0x00FF00FFu;
-              f[1] = v & 0x00FF00FFu;
-              f[2] = __byte_perm(u, 0u, 0x4341u);
-              f[3] = __byte_perm(v, 0u, 0x4341u);
-            } else {
-              const uint32_t u = e ? wa[i] >> 8 : wa[i], v = e ? wb[i] >> 8 : wb[i];
-              f[0] = (u & 0x000F000Fu) ^ 0x00080008u;
-              f[1] = (v & 0x000F000Fu) ^ 0x00080008u;
-              f[2] = (u & 0x00F000F0u) ^ 0x00800080u;
-              f[3] = (v & 0x00F000F0u) ^ 0x00800080u;
-            }
             const int step = (c * (kChunk / 4) + i) * kPerWord + e;
+            uint32_t f[G][4];
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if constexpr (BITS == 8) {
+                  const uint32_t v = w[u][h][i] ^ 0x80808080u;
+                  f[u][h] = v & 0x00FF00FFu;
+                  f[u][h + 2] = __byte_perm(v, 0u, 0x4341u);
+                } else {
+                  const uint32_t x8 = w[u][h][i] ^ 0x88888888u;
+                  const uint32_t v = e ? x8 >> 8 : x8;
+                  f[u][h] = v & 0x000F000Fu;
+                  f[u][h + 2] = v & 0x00F000F0u;
+                }
+              }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              if constexpr (kQInRegs) {
-                mma_f16(x[nb], f, qf[nb][step][0], qf[nb][step][1]);
-              } else {
-                const uint2 b = q_smem[(nb * C::kSteps + step) * 32 + lane];
-                mma_f16(x[nb], f, b.x, b.y);
+              uint2 b;
+              if constexpr (C::kQInRegs)
+                b = make_uint2(qf[step][0], qf[step][1]);
+              else
+                b = q_smem[(nb * C::kSteps + step) * 32 + lane];
+#pragma unroll
+              for (int u = 0; u < G; ++u) {
+                if (step == 0)
+                  mma_f16(x[nb][u], f[u], b.x, b.y, start_s[nb][0], start_s[nb][1]);
+                else
+                  mma_f16(x[nb][u], f[u], b.x, b.y);
               }
             }
           }
         }
       }
       // -------------------------------------------------- scales and masks
-      float sk[2], lg[2], inv[2];
+      uint32_t v0[4][kBytes / 4];   // the first values, on their way meanwhile
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sk[e] = __uint_as_float(lds32(st + 2 * C::kSide + (g + 8 * e) * 4));
-        const float sv = __uint_as_float(lds32(st + 2 * C::kSide + 64 + (g + 8 * e) * 4));
-        const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
-        lg[e] = __log2f(kept);
-        inv[e] = kept > 0.0f && kept < INFINITY ? __frcp_rn(kept) : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r)
+        load_words<kBytes>(st + (r & 1 ? frag_v1 : frag_v0) + 8 * (r >> 1) * RB, v0[r]);
+      __syncwarp();
+      float inv[G][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int u = 0; u < G; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nb][e] = fmaf(x[nb][e] * mul[nb][e & 1], sk[e >> 1], lg[e >> 1]);
-      const int64_t pos = (my_first + static_cast<int64_t>(s) * kWarps) * kSub;
-      if (pos + kSub > context) {
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = scale_smem[u * 16 + 8 * h + g];
+          inv[u][h] = v.z;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[nb][u][2 * h + e] = fmaf(x[nb][u][2 * h + e], v.x, v.y);
+        }
+      if (context - pos < C::kSub) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t ahead = pos + g + 8 * (e >> 1) - context;
-            const uint64_t m = mask_smem[nb * 8 + 2 * t + (e & 1)];
-            const bool seen = ahead < 0 || (ahead < req.nodes && (m >> ahead & 1));
-            if (!seen) x[nb][e] = -INFINITY;
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t m = mask_smem[nb * 8 + 2 * t + e];
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int ahead = pos - context + u * 16 + 8 * h + g;
+                const bool seen = ahead < 0 || (ahead < req.nodes && (m >> ahead & 1));
+                if (!seen) x[nb][u][2 * h + e] = -INFINITY;
+              }
           }
       }
       // -------------------------------------------------- raise the maximum
@@ -441,21 +543,24 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) raise |= x[nb][e] > limit[nb][e & 1];
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) raise |= x[nb][u][e] > limit[nb][e & 1];
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(x[nb][e], x[nb][e + 2]);
+            float high = fmaxf(x[nb][0][e], x[nb][0][e + 2]);
+            if constexpr (G == 2) high = fmaxf(high, fmaxf(x[nb][G - 1][e], x[nb][G - 1][e + 2]));
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (top > limit[nb][e]) {
-              // p' near 2^6 for the largest
-              const float now = top - 6.0f;
-              const float f = limit[nb][e] == -INFINITY ? 0.0f : exp2f(mu[nb][e] - now);
+            for (int d = 4; d < 32; d <<= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+            if (high > limit[nb][e]) {
+              // p' is 2^6 for the largest
+              const float now = high - 6.0f;
+              const float f = limit[nb][e] == -INFINITY ? 0.0f : exp2_approx(mu[nb][e] - now);
               mu[nb][e] = now;
-              limit[nb][e] = top + 8.0f;
+              limit[nb][e] = high + 8.0f;
               l[nb][e] *= f;
 #pragma unroll
               for (int b = 0; b < C::kSteps; ++b) {
@@ -466,48 +571,49 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
           }
       }
       // -------------------------------------------------- P^T
-      uint32_t p[NB][2];
+      uint32_t p[NB][G][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nb][e] = exp2_approx(x[nb][e] - mu[nb][e & 1]);
-          l[nb][e & 1] = fmaf(x[nb][e], inv[e >> 1], l[nb][e & 1]);
+        for (int u = 0; u < G; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[nb][u][e] = exp2_approx(x[nb][u][e] - mu[nb][e & 1]);
+            l[nb][e & 1] = fmaf(x[nb][u][e], inv[u][e >> 1], l[nb][e & 1]);
+          }
+          p[nb][u][0] = transpose8x8(h2_bits(__floats2half2_rn(x[nb][u][0], x[nb][u][1])));
+          p[nb][u][1] = transpose8x8(h2_bits(__floats2half2_rn(x[nb][u][2], x[nb][u][3])));
         }
-        p[nb][0] = transpose8x8(h2_bits(__floats2half2_rn(x[nb][0], x[nb][1])));
-        p[nb][1] = transpose8x8(h2_bits(__floats2half2_rn(x[nb][2], x[nb][3])));
-      }
       // -------------------------------------------------- O^T += V^T P^T
-      constexpr int kBytes = RB / 8;   // of a row per lane
-      const uint32_t sv0 = st + C::kSide;
-      uint32_t w[4][kBytes / 4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t o0 = (2 * t + (r & 1) + 8 * (r >> 1)) * RB + g * kBytes;
-        if constexpr (kBytes == 16) {
-          const uint4 u = lds128(sv0 + swz_v<RB>(o0));
-          w[r][0] = u.x; w[r][1] = u.y; w[r][2] = u.z; w[r][3] = u.w;
-        } else if constexpr (kBytes == 8) {
-          const uint2 u = lds64(sv0 + swz_v<RB>(o0));
-          w[r][0] = u.x; w[r][1] = u.y;
+      for (int u = 0; u < G; ++u) {
+        uint32_t w[4][kBytes / 4];
+        if (u == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) w[r][i] = v0[r][i];
         } else {
-          w[r][0] = lds32(sv0 + swz_v<RB>(o0));
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            load_words<kBytes>(st + (r & 1 ? frag_v1 : frag_v0) + (u * 16 + 8 * (r >> 1)) * RB, w[r]);
+        }
+        constexpr int kCodes = BITS == 8 ? 4 : 8;   // per word
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) {
+          uint32_t lo[kCodes], hi[kCodes];
+          value_pairs<BITS>(w[0][i], w[1][i], lo);
+          value_pairs<BITS>(w[2][i], w[3][i], hi);
+#pragma unroll
+          for (int j = 0; j < kCodes / 2; ++j) {
+            const uint32_t f[4] = {lo[2 * j], lo[2 * j + 1], hi[2 * j], hi[2 * j + 1]};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma_f16(o[nb][i * (kCodes / 2) + j], f, p[nb][u][0], p[nb][u][1]);
+          }
         }
       }
-      constexpr int kCodes = BITS == 8 ? 4 : 8;   // per word
-#pragma unroll
-      for (int i = 0; i < kBytes / 4; ++i) {
-        uint32_t lo[kCodes], hi[kCodes];
-        value_pairs<BITS>(w[0][i], w[1][i], lo);
-        value_pairs<BITS>(w[2][i], w[3][i], hi);
-#pragma unroll
-        for (int j = 0; j < kCodes / 2; ++j) {
-          const uint32_t f[4] = {lo[2 * j], lo[2 * j + 1], hi[2 * j], hi[2 * j + 1]};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma_f16(o[nb][i * (kCodes / 2) + j], f, p[nb][0], p[nb][1]);
-        }
-      }
+      st = st + C::kStage == ring + C::kRing ? ring : st + C::kStage;
     }
 
     // the next piece's loads overlap the join of this one
@@ -515,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
     const int slot = axis.slot();
     const int unit = axis.unit;
     __syncwarp();
-    more = axis.next(a, kTile, lane, 1);
+    more = axis.next(a, C::kTile, lane, 1);
     if (more) start(); else pdl_launch_dependents();
 
     // -------------------------------------------- join the warps' parts
@@ -540,9 +646,10 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat_smem[w * C::kRows + r].x);
         const float mine = stat_smem[warp * C::kRows + r].x;
-        f[nb][e] = mine == -INFINITY ? 0.0f : exp2f(mine - top);
+        f[nb][e] = mine == -INFINITY ? 0.0f : exp2f(mine - top) * 512.0f;   // and the codes' 2^9
       }
-    // the warps add their outputs one after another, always in this order
+    // the warps add their outputs one after another, always in this order; an
+    // element lies at [2 b + e / 2][g][row] so that a warp touches 64 words in a row
 #pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       if (w == warp) {
@@ -551,11 +658,16 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
 #pragma unroll
           for (int b = 0; b < C::kSteps; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // O^T element: dim (D / 8) g + 2 b + e / 2, row 2 t + e % 2
-              float* dst = out_smem + (nb * 8 + 2 * t + (e & 1)) * D + g * (D / 8) + 2 * b + (e >> 1);
-              const float v = o[nb][b][e] * f[nb][e & 1];
-              *dst = w == 0 ? v : *dst + v;
+            for (int h = 0; h < 2; ++h) {
+              // O^T element: dim (D / 8) g + 2 b + h, rows 2 t and 2 t + 1
+              float2* dst = reinterpret_cast<float2*>(out_smem + nb * 8 * D + (2 * b + h) * 64 + g * 8 + 2 * t);
+              float2 v = make_float2(o[nb][b][2 * h] * f[nb][0], o[nb][b][2 * h + 1] * f[nb][1]);
+              if (w > 0) {
+                const float2 old = *dst;
+                v.x += old.x;
+                v.y += old.y;
+              }
+              *dst = v;
             }
       }
       __syncthreads();
@@ -571,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
         const float2 s = stat_smem[w * C::kRows + r];
         sum += s.x == -INFINITY ? 0.0f : s.y * exp2f(s.x - top);
       }
-      const float4 v = *reinterpret_cast<const float4*>(out_smem + r * D + d);
+      const float* src = out_smem + (r >> 3) * 8 * D + d % (D / 8) * 64 + d / (D / 8) * 8 + (r & 7);
+      const float4 v = make_float4(src[0], src[64], src[128], src[192]);
       if (whole) {
         const int node = r / group;
         store_out4(a.out, bf16,
@@ -588,7 +701,6 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
 template <int D, int BITS, int NB>
 cudaError_t launch_rows(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
   using C = RowsCfg<D, BITS, NB>;
-  static_assert(C::kCtas * (C::kSmem + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(rows_kernel<D, BITS, NB>),
                                           C::kSmem, done);
