@@ -157,6 +157,8 @@ cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStrea
 // kv_rows.cu: at most 32 query rows (new tokens x grouped heads) per request
 // and key/value head.
 cudaError_t launch_attend_rows(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st);
+// kv_tree.cu: any number of query rows, 128 at a time.
+cudaError_t launch_attend_tree(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_verify(const void* logits, int64_t logits_stride, bool bf16,
                           const int32_t* tokens, const int32_t* parents, const int32_t* offsets,
                           int requests, int64_t nodes, int vocab, int max_nodes,

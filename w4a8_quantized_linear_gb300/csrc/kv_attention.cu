@@ -23,95 +23,12 @@
 namespace cider {
 namespace {
 
-constexpr int kPlainWarps = 4;
-
-// Value `lane * PER + e` of a row of codes.
-template <int D, int BITS>
-__device__ __forceinline__ void row_values(const uint8_t* row, int lane, float (&f)[D / 32]) {
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    const int d = lane * (D / 32) + e;
-    if constexpr (BITS == 8) {
-      f[e] = static_cast<float>(static_cast<int8_t>(row[d]));
-    } else {
-      const int w = row[d / 2];
-      f[e] = static_cast<float>(static_cast<int>(static_cast<unsigned>(w) << (28 - 4 * (d & 1))) >> 28);
-    }
-  }
-}
-
-// One CTA per (row of q, query head); its warps take positions in turn, each
-// with its own running maximum, sum and output, joined at the end.
-template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(32 * kPlainWarps) attend_kernel(AttendArgs a) {
-  constexpr int kPer = D / 32;
-  constexpr int kRowBytes = D * BITS / 8;
-  __shared__ float sm[kPlainWarps], sl[kPlainWarps], so[kPlainWarps][D];
-  const int64_t i = blockIdx.x;
-  const int hq = blockIdx.y, head = hq / (a.q_heads / a.cache.heads);
-  const int b = find_request(a.offsets, a.requests, i);
-  if (b < 0) return;
-  const Request r = request_of(a, b);
-  if (r.nodes == 0) return;
-  const int t = static_cast<int>(i - r.first);
-  const uint64_t mask = a.tree ? static_cast<uint64_t>(a.tree[i]) : (~0ull >> (63 - t));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* q = static_cast<const T*>(a.q) + i * a.q_stride + static_cast<int64_t>(hq) * D;
-  float qf[kPer], o[kPer], f[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    qf[e] = static_cast<float>(q[lane * kPer + e]);
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = warp; j < r.length; j += kPlainWarps) {
-    const int64_t ahead = j - r.context;
-    if (ahead >= 0 && !(mask >> ahead & 1)) continue;
-    const int64_t at = cache_row_of(a.cache, a.table, a.table_width, b, j, head);
-    if (at < 0) {
-      if (lane == 0) atomicOr(a.err, kDevErrIndex);
-      continue;
-    }
-    row_values<D, BITS>(a.cache.k + at * kRowBytes, lane, f);
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s += qf[e] * f[e];
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale * a.cache.k_scale[at];
-    const float top = fmaxf(m, s);
-    const float keep = __expf(m - top), p = __expf(s - top);
-    m = top;
-    l = l * keep + p;
-    row_values<D, BITS>(a.cache.v + at * kRowBytes, lane, f);
-    const float pv = p * a.cache.v_scale[at];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = o[e] * keep + pv * f[e];
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kPlainWarps; ++w) top = fmaxf(top, sm[w]);
-  for (int w = 0; w < kPlainWarps; ++w) sum += top == -INFINITY ? 0.0f : sl[w] * __expf(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += 32 * kPlainWarps) {
-    float x = 0.0f;
-    for (int w = 0; w < kPlainWarps; ++w)
-      x += top == -INFINITY ? 0.0f : so[w][d] * __expf(sm[w] - top);
-    static_cast<T*>(a.out)[(i * a.q_heads + hq) * D + d] = static_cast<T>(sum > 0.0f ? x / sum : 0.0f);
-  }
-}
-
 // Share c begins within a unit and the share before it began the unit: adds the
 // unit's parts in the order of the shares and writes its rows.  One CTA of D
 // threads per (share, row).  The shares' ends follow from the axis' length, so
 // the parts' statistics are loaded side by side; walking from share to share
 // cost a memory round trip each (18 us for 57 parts).
-__global__ void join_kernel(AttendArgs a, PartsArgs parts, int blocks, bool bf16) {
+__global__ void join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
   extern __shared__ float2 weight[];   // per part: its factor
   __shared__ float2 red[4];
   pdl_wait();
@@ -122,6 +39,7 @@ __global__ void join_kernel(AttendArgs a, PartsArgs parts, int blocks, bool bf16
   if (i.begin < 0 || parts.info[c - 1].begin == i.begin) return;
   const Request r = request_of(a, i.b, false);
   const int group = a.q_heads / a.cache.heads;
+  const int blocks = Axis::blocks_of(a, r, parts.rows);
   const int head = i.unit / blocks, block = i.unit - head * blocks;
   const int at = block * parts.rows + row;
   if (at >= r.nodes * group) return;
@@ -164,8 +82,8 @@ __global__ void join_kernel(AttendArgs a, PartsArgs parts, int blocks, bool bf16
 
 }  // namespace
 
-cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, int blocks,
-                        bool bf16, cudaStream_t st) {
+cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, bool bf16,
+                        cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows));
   cfg.blockDim = dim3(static_cast<unsigned>(a.cache.head_dim));
@@ -176,23 +94,12 @@ cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, a, parts, blocks, bf16);
+  return cudaLaunchKernelEx(&cfg, join_kernel, a, parts, bf16);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
-  if (a.max_nodes * (a.q_heads / a.cache.heads) <= 32)
-    return launch_attend_rows(a, bf16, num_sms, st);
-  const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>(a.q_heads));
-  const bool wide = a.cache.head_dim == 128, b8 = a.cache.bits == 8;
-  auto go = [&](auto t) {
-    using T = decltype(t);
-    if (wide && b8) attend_kernel<T, 128, 8><<<grid, 32 * kPlainWarps, 0, st>>>(a);
-    else if (wide) attend_kernel<T, 128, 4><<<grid, 32 * kPlainWarps, 0, st>>>(a);
-    else if (b8) attend_kernel<T, 64, 8><<<grid, 32 * kPlainWarps, 0, st>>>(a);
-    else attend_kernel<T, 64, 4><<<grid, 32 * kPlainWarps, 0, st>>>(a);
-  };
-  if (bf16) go(__nv_bfloat16()); else go(__half());
-  return cudaGetLastError();
+  return a.max_nodes * (a.q_heads / a.cache.heads) <= 16 ? launch_attend_rows(a, bf16, num_sms, st)
+                                                         : launch_attend_tree(a, bf16, num_sms, st);
 }
 
 }  // namespace cider

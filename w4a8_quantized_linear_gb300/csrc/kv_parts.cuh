@@ -26,7 +26,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 struct Axis {
   Request req;          // of request b
-  int b, unit;          // unit: head * row blocks + row block
+  int b, unit;          // unit: head * (the request's row blocks) + row block
   int64_t unit_begin;   // the unit's first tile on the axis
   int64_t unit_tiles;
   int64_t at, end;      // this CTA's current tile and the end of its share
@@ -37,13 +37,19 @@ struct Axis {
   __device__ static int64_t tiles_of(const Request& r, int tile) {
     return r.nodes == 0 ? 0 : (r.length + tile - 1) / tile;
   }
-  // Called by whole warps; blocks: row blocks per head.
-  __device__ void begin(const AttendArgs& a, int tile, int lane, int blocks) {
-    const int64_t units = static_cast<int64_t>(a.cache.heads) * blocks;
+  // Row blocks per head of a request.
+  __device__ static int blocks_of(const AttendArgs& a, const Request& r, int block_rows) {
+    return (r.nodes * (a.q_heads / a.cache.heads) + block_rows - 1) / block_rows;
+  }
+  // Called by whole warps; block_rows: query rows of a unit at most.
+  __device__ void begin(const AttendArgs& a, int tile, int lane, int block_rows) {
     total = 0;
     for (int b0 = 0; b0 < a.requests; b0 += 32) {
       const int i = b0 + lane;
-      if (i < a.requests) total += tiles_of(request_of(a, i, blockIdx.x == 0), tile) * units;
+      if (i < a.requests) {
+        const Request r = request_of(a, i, blockIdx.x == 0);
+        total += tiles_of(r, tile) * a.cache.heads * blocks_of(a, r, block_rows);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -57,7 +63,11 @@ struct Axis {
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {
       const int i = b0 + lane;
-      const int64_t mine = i < a.requests ? tiles_of(request_of(a, i, false), tile) * units : 0;
+      int64_t mine = 0;
+      if (i < a.requests) {
+        const Request r = request_of(a, i, false);
+        mine = tiles_of(r, tile) * a.cache.heads * blocks_of(a, r, block_rows);
+      }
       int64_t sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -88,11 +98,11 @@ struct Axis {
   __device__ bool whole() const { return piece_begin == 0 && piece_end == unit_tiles; }
   // Where a part goes: two slots per CTA.
   __device__ int slot() const { return 2 * blockIdx.x + (continued ? 0 : 1); }
-  __device__ bool next(const AttendArgs& a, int tile, int lane, int blocks) {
+  __device__ bool next(const AttendArgs& a, int tile, int block_rows) {
     at = unit_begin + piece_end;
     if (at >= end) return false;
     unit_begin += unit_tiles;
-    if (++unit == a.cache.heads * blocks) {
+    if (++unit == a.cache.heads * blocks_of(a, req, block_rows)) {
       unit = 0;
       do {
         req = request_of(a, ++b, false);
@@ -154,8 +164,8 @@ __device__ __forceinline__ void store_out4(void* out, bool bf16, int64_t at, con
 }
 
 // Joins the parts of every cut unit (kv_attention.cu).  rows: at most this many
-// rows of a unit exist; blocks: row blocks per head.
-cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, int blocks,
-                        bool bf16, cudaStream_t st);
+// rows of a unit exist; its kernel is a programmatic dependent of the launch before.
+cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, bool bf16,
+                        cudaStream_t st);
 
 }  // namespace cider

@@ -73,7 +73,7 @@ struct RowsCfg {
   static constexpr int kMaskBytes = kRows * 8;
   static constexpr int kScaleBytes = kWarps * kSub * 16;
   static constexpr int kRest = kQBytes + kOutBytes + kStatBytes + kMaskBytes + kScaleBytes;
-  static constexpr int kCtas = NB == 1 || (NB == 2 && kRowBytes < 128) ? 3 : 2;   // per SM
+  static constexpr int kCtas = NB == 1 ? (D == 128 ? 3 : 4) : 2;   // per SM
   // as many stages as the resident CTAs' shared memory holds, at most 6
   static constexpr int kFit = (227 * 1024 / kCtas - 1024 - kRest) / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
   const int group = a.q_heads / a.cache.heads;
 
   Axis axis;
-  axis.begin(a, C::kTile, lane, 1);
+  axis.begin(a, C::kTile, lane, C::kRows);
   bool more = axis.more();
   if (threadIdx.x == 0) parts.announce(axis);
 
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
     const int slot = axis.slot();
     const int unit = axis.unit;
     __syncwarp();
-    more = axis.next(a, C::kTile, lane, 1);
+    more = axis.next(a, C::kTile, C::kRows);
     if (more) start(); else pdl_launch_dependents();
 
     // -------------------------------------------- join the warps' parts
@@ -713,7 +713,7 @@ cudaError_t launch_rows(const AttendArgs& a, bool bf16, int num_sms, cudaStream_
   rows_kernel<D, BITS, NB><<<ctas, kThreads, C::kSmem, st>>>(a, parts, bf16);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join(a, parts, ctas, std::min(C::kRows, a.max_nodes * (a.q_heads / a.cache.heads)), 1,
+  return launch_join(a, parts, ctas, std::min(C::kRows, a.max_nodes * (a.q_heads / a.cache.heads)),
                      bf16, st);
 }
 

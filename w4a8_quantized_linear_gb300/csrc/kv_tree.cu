@@ -1,0 +1,847 @@
+// kv_tree.cu -- attention over the paged, quantized cache for many query rows
+// per key/value head (trees of drafted tokens x grouped heads): 128 rows and
+// 128 positions at a time on the tensor core.
+//
+// Mathematics as in kv_rows.cu: x_ij = scale log2(e) sk_j (q_i . ck_j) + log2
+// sv_j, p'_ij = 2^(x_ij - m_i), o_i = sum p' cv / sum p' / sv.  The codes become
+// exact fp16 values once per tile, for all rows; q is fp16 (bf16 rows are
+// scaled by one power of two first), p' is rounded to fp16, sums are fp32.
+//
+// Per tile: S = Q K^T with Q in tensor memory and K's tile in shared memory,
+// p' back into the tensor memory of its own S, O += P V with V's tile as it
+// lies ([position][dim], the operand's "MN-major" form).  Tensor memory: two S
+// tiles (one is computed while the other is in softmax), O, Q: 448 columns.
+// Both operands from shared memory would need the SM's whole shared-memory
+// bandwidth; with Q and P in tensor memory it is half.
+//
+// Bound: HBM for INT8 up to 128 rows in theory (a tile is 33 KiB: ~1400 cycles
+// of an SM's share of HBM against 1024 of tensor work), the issue of the
+// conversion and softmax instructions in practice.
+//
+// Roles (640 threads, one CTA per SM, persistent over its share of the axis):
+//   warp 0        one thread issues the MMAs
+//   warps 4-11    converters: codes from global memory (prefetched to L2 four
+//                 to seven tiles ahead, to registers one ahead) to fp16 tiles
+//                 in shared memory; each position's sk, log2 sv, 1 / sv
+//   warps 12-19   softmax: warps 12-15 the tile's first 64 positions, 16-19 the
+//                 last 64, each warp its quarter of the rows.  S is read in the
+//                 layout that gives a thread 4 rows x 2 neighbouring positions,
+//                 so that a position's scales are loaded once for 4 rows.  m_i
+//                 is only raised when a p' passes 2^14: the two warps of a
+//                 quarter agree on that with one reducing barrier per tile.
+// Q is staged by warps 12-15, one row per thread.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "cider_device.cuh"
+#include "cider_internal.h"
+#include "kv_common.cuh"
+#include "kv_parts.cuh"
+
+namespace cider {
+namespace {
+
+constexpr int kTileRows = 128;    // query rows of a unit
+constexpr int kTilePos = 128;     // positions of a tile
+constexpr int kThreads = 640;
+constexpr int kConvWarp0 = 4, kConvWarps = 8;
+constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
+constexpr int kRegsMisc = 32, kRegsConv = 80, kRegsSoft = 144, kRegsLaunch = 96;
+constexpr int kRegsNeeded = 128 * kRegsMisc + 256 * kRegsConv + 256 * kRegsSoft;
+static_assert(kRegsNeeded <= kThreads * kRegsLaunch, "register split exceeds the launch's registers");
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColAll = 512;
+constexpr float kNone = -3.0e38f;   // m of a row that has seen nothing: any x is far above it
+
+template <int D, int BITS>
+struct TreeCfg {
+  static constexpr int kRowBytes = D * BITS / 8;
+  static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
+  static constexpr int kCodes = 128 / BITS;                  // codes of a chunk
+  static constexpr int kUnits = kCodes / 8;                  // 16-byte fp16 units of a chunk
+  static constexpr int kRowsPer = 512 / kRowBytes;           // rows of one warp load
+  static constexpr int kLoads = kTilePos / (kConvWarps * kRowsPer);   // per thread, K or V
+  static constexpr int kSub = 16384;                         // [128][64] fp16, 128-byte swizzle
+  static constexpr int kSide = kSub * (D / 64);              // a K or V tile
+  static constexpr int kScaleOffset = 4 * kSide;             // two stages of K, V
+  static constexpr int kScaleStage = 64 * 16 + 64 * 8;       // per pair of positions: sk sk lg lg, inv inv
+  static constexpr int kStatOffset = kScaleOffset + 2 * kScaleStage;
+  static constexpr int kStatBytes = 2 * kTileRows * 8;       // per half and row: two floats
+  static constexpr int kMaskOffset = kStatOffset + kStatBytes;
+  static constexpr int kBarOffset = kMaskOffset + kTileRows * 8;
+  static constexpr int kSmem = kBarOffset + 32 * 8 + 64 + 1024;
+  // Order of the dims in the fp16 tiles: unit `lin` of a row (8 values) holds
+  // codes (lin / kChunks) * 8 .. + 8 of chunk lin % kChunks, so that the lanes
+  // that convert a row's chunks store to different banks.
+  __host__ __device__ static constexpr int dim_of(int lin) {
+    return lin % kChunks * kCodes + lin / kChunks * 8;
+  }
+};
+
+// Barriers, by number.
+enum Bar : int {
+  kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScEmpty = 8, kSFull = 10, kPReady = 12,
+  kQFull = 14, kOFull = 15, kOEmpty = 16, kDone = 17, kBars = 18
+};
+
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// A K-major / MN-major tile's descriptors, 128-byte swizzle.  MN-major (the
+// values, [position][dim]): 64 dims are a row of 128 bytes, 8 positions 1024
+// bytes (stride offset), the next 64 dims `kSub` further (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t leading) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((leading >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+constexpr uint32_t kBMajorMn = 1u << 16;   // instruction descriptor: B is MN-major
+
+// 16 lanes x 32 columns (fp32): register 4 i + 2 h + e of thread T is lane
+// T / 4 + 8 h, column 8 i + 2 (T % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float (&r)[16]) {
+  uint32_t u[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
+}
+// After tmem_wait_ld: nothing that reads these registers is moved above the wait.
+template <int N>
+__device__ __forceinline__ void loaded(float (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+}
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// 16 lanes x 32 columns: register 2 i + h of thread T is lane T / 4 + 8 h, column 4 i + T % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Whether any thread of the `count` threads of barrier `id` has `v`.
+__device__ __forceinline__ bool barrier_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// Two fp32 operations at once.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un2(const F2& x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(const F2& a, const F2& b, const F2& c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(const F2& a, const F2& b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(const F2& a, const F2& b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t u) {
+  __half2 h;
+  memcpy(&h, &u, 4);
+  return h;
+}
+
+// Unit h of a 16-byte chunk as 8 fp16 values.  INT8: the codes in order.  INT4:
+// code 2^-9, in the order 0 4 1 5 2 6 3 7 (code + 8 as a subnormal, lifted).
+template <int BITS>
+__device__ __forceinline__ uint4 convert_unit(const uint4& c, int h) {
+  uint4 r;
+  if constexpr (BITS == 8) {
+    s8x4_to_h2x2(h == 0 ? c.x : c.z, r.x, r.y);
+    s8x4_to_h2x2(h == 0 ? c.y : c.w, r.z, r.w);
+  } else {
+    const uint32_t x = (h == 0 ? c.x : h == 1 ? c.y : h == 2 ? c.z : c.w) ^ 0x88888888u;
+    const uint32_t y = x >> 8;
+    const __half2 lift = as_h2(0x78007800u), lift_hi = as_h2(0x68006800u), off = as_h2(0xA400A400u);
+    auto f = [&](uint32_t u, __half2 m) {
+      const __half2 v = __hfma2(as_h2(u), m, off);
+      uint32_t w;
+      memcpy(&w, &v, 4);
+      return w;
+    };
+    r.x = f(x & 0x000F000Fu, lift);
+    r.y = f(x & 0x00F000F0u, lift_hi);
+    r.z = f(y & 0x000F000Fu, lift);
+    r.w = f(y & 0x00F000F0u, lift_hi);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)),
+               "r"(bytes)
+               : "memory");
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
+  using C = TreeCfg<D, BITS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.q_heads / a.cache.heads;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kBarOffset + kBars * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOffset + kBars * 8 + 4);
+  float* unlift_smem = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 8);
+  float* lift_max = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 16);   // 4 warps
+  auto bar = [&](int i) { return sbase + C::kBarOffset + i * 8; };
+  auto wait = [&](int i, uint32_t parity) {
+    return mbar_wait_bounded(bar(i), parity & 1, abort_flag, a.err, kWaitNs);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      *abort_flag = 0;
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(bar(kKFull + s), kConvWarps);
+        mbar_init(bar(kKEmpty + s), 1);
+        mbar_init(bar(kVFull + s), kConvWarps);
+        mbar_init(bar(kVEmpty + s), 1);
+        mbar_init(bar(kScEmpty + s), kSoftWarps);
+        mbar_init(bar(kSFull + s), 1);
+        mbar_init(bar(kPReady + s), kSoftWarps);
+      }
+      mbar_init(bar(kQFull), 4);
+      mbar_init(bar(kOFull), 1);
+      mbar_init(bar(kOEmpty), kSoftWarps);
+      mbar_init(bar(kDone), 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), kColAll);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Every role walks the same pieces.  A wait that gives up raises the abort
+  // flag; the roles then run to their ends without waiting (all their memory
+  // accesses stay in bounds), so that no barrier is left with a thread missing.
+  if (warp < kConvWarp0) {
+    regs_dec<kRegsMisc>();
+    if (warp == 0) {
+      Axis axis;
+      axis.begin(a, kTilePos, lane, kTileRows);
+      if (lane == 0) parts.announce(axis);
+      bool more = axis.more();
+      uint32_t n = 0, piece = 0;
+      // whole-warp waits; one lane issues
+      while (more) {
+        const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+        bool ok = wait(kQFull, piece);
+        tc_fence_after();
+        for (int i = 0; i <= tiles; ++i) {
+          if (i < tiles) {   // S(n) = Q K(n)^T
+            const uint32_t st = n & 1, ph = n >> 1;
+            ok = wait(kKFull + st, ph) && ok;
+            tc_fence_after();
+            if (lane == 0 && ok) {
+              const uint32_t kt = sbase + st * 2 * C::kSide;
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s)
+                tc_mma_ts(tmem + kColS + st * 128, tmem + kColQ + s * 8,
+                          smem_desc_k_sw128(kt + (s >> 2) * C::kSub + (s & 3) * 32),
+                          idesc_f16_f32(128, 128), s > 0);
+              tc_commit(bar(kSFull + st));
+              tc_commit(bar(kKEmpty + st));
+            }
+            __syncwarp();
+          }
+          if (i > 0) {   // O += P(n - 1) V(n - 1)
+            const uint32_t m = n - 1, st = m & 1, ph = m >> 1;
+            if (i == 1) ok = wait(kOEmpty, piece + 1) && ok;
+            ok = wait(kPReady + st, ph) && ok;
+            ok = wait(kVFull + st, ph) && ok;
+            tc_fence_after();
+            if (lane == 0 && ok) {
+              const uint32_t vt = sbase + st * 2 * C::kSide + C::kSide;
+#pragma unroll
+              for (int s = 0; s < kTilePos / 16; ++s)
+                tc_mma_ts(tmem + kColO, tmem + kColS + st * 128 + (s >> 2) * 64 + (s & 3) * 8,
+                          smem_desc_mn_sw128(vt + s * 2048, C::kSub),
+                          idesc_f16_f32(128, D) | kBMajorMn, (i > 1 || s > 0) ? 1u : 0u);
+              tc_commit(bar(kVEmpty + st));
+              if (i == tiles) tc_commit(bar(kOFull));
+            }
+            __syncwarp();
+          }
+          if (i < tiles) ++n;
+        }
+        ++piece;
+        more = axis.next(a, kTilePos, kTileRows);
+      }
+      // no MMA may be in flight when the tensor memory is freed, also after an abort
+      if (lane == 0) {
+        tc_commit(bar(kDone));
+        volatile uint32_t keep_waiting = 0u;
+        mbar_wait_bounded(bar(kDone), 0, &keep_waiting, a.err, kWaitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp < kSoftWarp0) {
+    regs_dec<kRegsConv>();
+    // ------------------------------------------------------------ converters
+    const int cw = warp - kConvWarp0;
+    int c, row;   // this lane's chunk, and its row among the rows of one load
+    if constexpr (C::kChunks == 8) {
+      c = lane & 7;
+      row = lane >> 3;
+    } else if constexpr (C::kChunks == 4) {
+      c = lane & 3;
+      row = (lane >> 3) + 4 * (lane >> 2 & 1);
+    } else {
+      c = lane & 1;
+      row = (lane >> 3 & 1) + 2 * (lane >> 1 & 3) + 8 * (lane >> 4);
+    }
+    const int token0 = cw * C::kRowsPer + row;   // of load j: + j * kConvWarps * kRowsPer
+    const int token_s = (cw & 3) * 32 + lane;    // warps 4-7: this lane's position's scales
+    const int page16 = a.cache.page_shift - 4;
+    const float mul = a.scale * 1.44269504f * (BITS == 4 ? 512.0f : 1.0f);
+
+    Axis axis;
+    axis.begin(a, kTilePos, lane, kTileRows);
+    bool more = axis.more();
+    // the cursor of the loads, one tile ahead of the conversion
+    int tile = 0, tiles = 0, first_block = 0, last_block = 0;   // 16-position blocks of the piece
+    int ids = -1, next_ids = -1;   // lane l: row / 16 of block 32 i + l (four tiles), -1 without a page
+    const int32_t* table = nullptr;
+    auto load_ids = [&](int base) -> int {
+      const int blk = first_block + base + lane;
+      if (blk >= last_block) return -1;
+      const int32_t id = table[blk >> page16];
+      if (id < 0 || id >= a.cache.pages) {
+        atomicOr(a.err, kDevErrIndex);
+        return -1;
+      }
+      const int head = axis.unit / Axis::blocks_of(a, axis.req, kTileRows);
+      return ((id * a.cache.heads + head) << page16) + (blk & ((1 << page16) - 1));
+    };
+    auto open = [&]() {   // the cursor to the first tile of the axis' piece
+      tile = 0;
+      tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+      first_block = static_cast<int>(axis.piece_begin) * 8;
+      last_block = static_cast<int>(min(axis.piece_end * 8, (axis.req.length + 15) / 16));
+      table = a.table + axis.b * a.table_width;
+      ids = load_ids(0);
+      next_ids = -1;
+    };
+    // row / 16 of 16-position block `blk` (0 .. 7) of the cursor's tile
+    auto block_row = [&](int blk) { return __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + blk); };
+    auto load_side = [&](const uint8_t* codes, uint4 (&r)[C::kLoads]) {
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j) {
+        const int first = (j * kConvWarps + cw) * C::kRowsPer;   // of the warp's rows
+        const int at = block_row(first >> 4);
+        const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (first & 15) + row;
+        r[j] = at >= 0 ? *reinterpret_cast<const uint4*>(codes + src * C::kRowBytes + c * 16)
+                       : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_scales = [&](float& sk, float& sv) {
+      const int at = block_row(token_s >> 4);
+      const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (token_s & 15);
+      sk = at >= 0 ? a.cache.k_scale[src] : 0.0f;
+      sv = at >= 0 ? a.cache.v_scale[src] : 0.0f;
+    };
+    // after a tile's loads: the cursor moves on; ids for the four tiles after
+    // the next boundary are loaded one tile after a boundary, and their codes
+    // prefetched to L2 one tile later
+    auto step = [&]() {
+      if ((tile & 3) == 0) next_ids = load_ids((tile + 4) * 8);
+      if ((tile & 3) == 1 && (lane & 7) == cw && next_ids >= 0) {
+        const int64_t r = static_cast<int64_t>(next_ids) * 16;
+        prefetch_l2(a.cache.k + r * C::kRowBytes, 16 * C::kRowBytes);
+        prefetch_l2(a.cache.v + r * C::kRowBytes, 16 * C::kRowBytes);
+        prefetch_l2(a.cache.k_scale + r, 64);
+        prefetch_l2(a.cache.v_scale + r, 64);
+      }
+      ++tile;
+      if ((tile & 3) == 0) ids = next_ids;
+      if (tile == tiles) {
+        more = axis.next(a, kTilePos, kTileRows);
+        if (more) open();
+      }
+    };
+    auto store_side = [&](uint8_t* dst, const uint4 (&r)[C::kLoads]) {
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j) {
+        const int token = token0 + j * kConvWarps * C::kRowsPer;
+#pragma unroll
+        for (int h = 0; h < C::kUnits; ++h) {
+          const int lin = c + C::kChunks * h;
+          const uint4 v = convert_unit<BITS>(r[j], h);
+          *reinterpret_cast<uint4*>(dst + (lin >> 3) * C::kSub + token * 128 +
+                                    (((lin & 7) ^ (token & 7)) << 4)) = v;
+        }
+      }
+    };
+    uint4 rk[C::kLoads], rv[C::kLoads];
+    float sk = 0.0f, sv = 0.0f;
+    if (more) {
+      open();
+      load_side(a.cache.k, rk);
+      load_scales(sk, sv);
+      load_side(a.cache.v, rv);
+    }
+    uint32_t n = 0;
+    bool have = more;
+    while (have) {
+      const uint32_t st = n & 1, ph = n >> 1;
+      uint8_t* kt = smem + st * 2 * C::kSide;
+      wait(kKEmpty + st, ph + 1);
+      wait(kScEmpty + st, ph + 1);
+      store_side(kt, rk);
+      if (cw < 4) {
+        float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + st * C::kScaleStage);
+        const int pair = token_s >> 1, e = token_s & 1;
+        const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        float lg, inv;
+        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(kept));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(kept));
+        f[pair * 4 + e] = sk * mul;
+        f[pair * 4 + 2 + e] = lg;
+        f[256 + pair * 2 + e] = kept > 0.0f && kept < INFINITY ? inv : 0.0f;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKFull + st));
+      // the values of this tile are in registers; the cursor moves on, but the
+      // registers of V are only loaded again once they are stored
+      step();
+      if (more) {
+        load_side(a.cache.k, rk);
+        load_scales(sk, sv);
+      }
+      wait(kVEmpty + st, ph + 1);
+      store_side(kt + C::kSide, rv);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kVFull + st));
+      if (more) load_side(a.cache.v, rv);
+      have = more;
+      ++n;
+    }
+  } else {
+    regs_inc<kRegsSoft>();
+    // --------------------------------------------------------------- softmax
+    const int sw = warp - kSoftWarp0, quarter = sw & 3, half = sw >> 2;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float2* stat = reinterpret_cast<float2*>(smem + C::kStatOffset);
+    uint64_t* masks = reinterpret_cast<uint64_t*>(smem + C::kMaskOffset);
+    const int pair_bar = 1 + quarter;   // the two warps of a quarter
+
+    Axis axis;
+    axis.begin(a, kTilePos, lane, kTileRows);
+    bool more = axis.more();
+    uint32_t n = 0, piece = 0;
+    while (more) {
+      const Request req = axis.req;
+      const int blocks = Axis::blocks_of(a, req, kTileRows);
+      const int head = axis.unit / blocks, block = axis.unit - head * blocks;
+      const int rows = min(kTileRows, req.nodes * group - block * kTileRows);
+      const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+      // ------------------------------------------------- one row per thread
+      const int row = quarter * 32 + lane;
+      const int at = block * kTileRows + row;
+      const int node = row < rows ? at / group : 0;
+      const int64_t head_at = static_cast<int64_t>(head) * group + (row < rows ? at - node * group : 0);
+      if (half == 0) {
+        uint64_t m = 0;
+        if (row < rows)
+          m = a.tree ? static_cast<uint64_t>(a.tree[req.first + node]) : ~0ull >> (63 - node);
+        masks[row] = m;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (req.first + node) * a.q_stride + head_at * D;
+        float lift = 1.0f;
+        if (bf16) {
+          // one power of two for all rows puts the largest value in [2^13, 2^14)
+          float top = 0.0f;
+          for (int i = 0; i < D; i += 8) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < rows) w = *reinterpret_cast<const uint4*>(q + i);
+            float f[8];
+            widen8<__nv_bfloat16>(w, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0) lift_max[quarter] = top;
+          named_barrier_sync(5, 128);
+          top = fmaxf(fmaxf(lift_max[0], lift_max[1]), fmaxf(lift_max[2], lift_max[3]));
+          int k = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+          k = top == 0.0f ? 0 : max(-126, min(k, 126));
+          lift = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          if (threadIdx.x == kSoftWarp0 * 32)
+            *unlift_smem = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        } else if (threadIdx.x == kSoftWarp0 * 32) {
+          *unlift_smem = 1.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s) {
+          uint32_t u[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < rows) w = *reinterpret_cast<const uint4*>(q + C::dim_of(s * 8 + j));
+            if (bf16) {
+              float f[8];
+              widen8<__nv_bfloat16>(w, f);
+              w = make_uint4(pack_h2(f[0] * lift, f[1] * lift), pack_h2(f[2] * lift, f[3] * lift),
+                             pack_h2(f[4] * lift, f[5] * lift), pack_h2(f[6] * lift, f[7] * lift));
+            }
+            if constexpr (BITS == 4)   // the order of the converted codes
+              w = make_uint4(__byte_perm(w.x, w.z, 0x5410u), __byte_perm(w.x, w.z, 0x7632u),
+                             __byte_perm(w.y, w.w, 0x5410u), __byte_perm(w.y, w.w, 0x7632u));
+            u[4 * j] = w.x;
+            u[4 * j + 1] = w.y;
+            u[4 * j + 2] = w.z;
+            u[4 * j + 3] = w.w;
+          }
+          tmem_st32(lanes + kColQ + s * 32, u);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQFull));
+      }
+      wait(kQFull, piece);   // also: the masks and the scaling are there
+      const float unlift = *unlift_smem;
+      const F2 unlift2 = f2(unlift, unlift);
+
+      // ------------------------------------------------------ the piece's tiles
+      const bool active = quarter * 32 < rows;   // some row of this warp exists
+      float mu[4], l[4];   // rows g, g + 8, g + 16, g + 24 of the quarter
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        mu[r] = kNone;
+        l[r] = 0.0f;
+      }
+      int pos = static_cast<int>(axis.piece_begin) * kTilePos + half * 64;
+      const int context = static_cast<int>(req.context);
+      for (int i = 0; i < tiles; ++i, pos += kTilePos, ++n) {
+        const uint32_t st = n & 1, ph = n >> 1;
+        wait(kKFull + st, ph);   // the scales
+        wait(kSFull + st, ph);
+        tc_fence_after();
+        if (active) {
+          const uint32_t s_at = lanes + kColS + st * 128 + half * 64;
+          const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOffset + st * C::kScaleStage) +
+                             half * 32 + t;
+          const float2* iv = reinterpret_cast<const float2*>(smem + C::kScaleOffset + st * C::kScaleStage + 1024) +
+                             half * 32 + t;
+          const bool masked = context - pos < 64;
+          // x of 32 positions (chunk ch), for the rows g + 8 h + 16 hh: [hh][4 j + 2 h + e]
+          auto load_x = [&](int ch, float (&x)[2][16]) {
+            tmem_ld_16x256b_x4(s_at + ch * 32, x[0]);
+            tmem_ld_16x256b_x4(s_at + ch * 32 + (16u << 16), x[1]);
+            tmem_wait_ld();
+            loaded(x[0]);
+            loaded(x[1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 v = sc[ch * 16 + 4 * j];
+              const F2 sk2 = mul2(f2(v.x, v.y), unlift2), lg2 = f2(v.z, v.w);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float& x0 = x[r >> 1][4 * j + 2 * (r & 1)];
+                float& x1 = x[r >> 1][4 * j + 2 * (r & 1) + 1];
+                un2(fma2(f2(x0, x1), sk2, lg2), x0, x1);
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint64_t m = masks[quarter * 32 + 8 * r + g];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int ahead = pos - context + ch * 32 + 8 * j + 2 * t + e;
+                    const bool seen = ahead < 0 || (ahead < req.nodes && (m >> ahead & 1));
+                    if (!seen) x[r >> 1][4 * j + 2 * (r & 1) + e] = -INFINITY;
+                  }
+              }
+            }
+          };
+          uint32_t p[2][16];   // [hh][2 j + h], j: 8-position groups of the 64
+          float add[4];
+          auto weights = [&]() -> bool {
+            __half2 high[4];
+            F2 sum[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              high[r] = __half2half2(__ushort_as_half(0));
+              sum[r] = f2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              float x[2][16];
+              load_x(ch, x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 v = iv[ch * 16 + 4 * j];
+                const F2 inv2 = f2(v.x, v.y);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const F2 d = add2(f2(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]),
+                                    f2(-mu[r], -mu[r]));
+                  float d0, d1;
+                  un2(d, d0, d1);
+                  const float p0 = exp2_approx(d0), p1 = exp2_approx(d1);
+                  sum[r] = fma2(f2(p0, p1), inv2, sum[r]);
+                  const uint32_t u = pack_h2(p0, p1);
+                  high[r] = __hmax2(high[r], as_h2(u));
+                  p[r >> 1][2 * (ch * 4 + j) + (r & 1)] = u;
+                }
+              }
+            }
+            bool over = false;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float s0, s1;
+              un2(sum[r], s0, s1);
+              add[r] = s0 + s1;
+              over |= __half2float(__hmax(__low2half(high[r]), __high2half(high[r]))) > 16384.0f;
+            }
+            return over;
+          };
+          if (barrier_or(pair_bar, 64, weights())) {
+            // some row's m is raised: its maximum over the tile, from both halves
+            float top[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top[r] = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              float x[2][16];
+              load_x(ch, x);
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  top[r] = fmaxf(top[r], fmaxf(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]));
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+              if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g].x = top[r];
+            }
+            named_barrier_sync(pair_bar, 64);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              top[r] = fmaxf(top[r], stat[(half ^ 1) * kTileRows + quarter * 32 + 8 * r + g].x);
+              if (top[r] > mu[r] + 14.0f) {
+                const float now = top[r] - 6.0f;
+                const float f = exp2_approx(mu[r] - now);
+                l[r] *= f;
+                mu[r] = now;
+                if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g].y = f;
+              } else if (t == 0) {
+                stat[half * kTileRows + quarter * 32 + 8 * r + g].y = 1.0f;
+              }
+            }
+            if (i > 0) {   // this warp's half of O's columns; the products so far are done
+              wait(kVEmpty + ((n - 1) & 1), (n - 1) >> 1);
+              tc_fence_after();
+              __syncwarp();
+              const float f = stat[half * kTileRows + quarter * 32 + lane].y;
+#pragma unroll
+              for (int ch = 0; ch < D / 64; ++ch) {
+                uint32_t o[32];
+                const uint32_t o_at = lanes + kColO + half * (D / 2) + ch * 32;
+                tmem_ld32(o_at, o);
+                tmem_wait_ld();
+                loaded(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(o_at, o);
+              }
+            }
+            weights();
+            // the partner has read this warp's maxima before they are written again
+            named_barrier_sync(pair_bar, 64);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) l[r] += add[r];
+          // P over this half's own columns of S
+          tmem_st_16x128b_x8(s_at, p[0]);
+          tmem_st_16x128b_x8(s_at + (16u << 16), p[1]);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kScEmpty + st));
+          mbar_arrive(bar(kPReady + st));
+        }
+      }
+
+      // ------------------------------------------------------------ the output
+      const bool whole = axis.whole();
+      const int slot = axis.slot();
+      more = axis.next(a, kTilePos, kTileRows);
+      if (active) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+          l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+          if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g] = make_float2(mu[r], l[r]);
+        }
+        named_barrier_sync(pair_bar, 64);
+      }
+      wait(kOFull, piece);
+      tc_fence_after();
+      if (active) {
+        const float2 s0 = stat[row], s1 = stat[kTileRows + row];
+        const float sum = s0.y + s1.y;
+        const float top = s0.x == kNone ? -INFINITY : s0.x;
+        const float codes = BITS == 4 ? 512.0f : 1.0f;
+        const float f = whole ? (sum > 0.0f ? codes / sum : 0.0f) : codes;
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kColO + half * (D / 2) + ch * 32, o);
+          tmem_wait_ld();
+          loaded(o);
+          if (row < rows) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int d = C::dim_of((half * (D / 2) + ch * 32) / 8 + j);
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)   // INT4 units hold the dims 0 4 1 5 2 6 3 7
+                v[BITS == 4 ? (e & 1) * 4 + (e >> 1) : e] = __uint_as_float(o[8 * j + e]) * f;
+              const float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+              if (whole) {
+                const int64_t dst = ((req.first + node) * a.q_heads + head_at) * D + d;
+                store_out4(a.out, bf16, dst, lo, 1.0f);
+                store_out4(a.out, bf16, dst + 4, hi, 1.0f);
+              } else {
+                parts.store(slot, row, D, d, lo, top, sum);
+                parts.store(slot, row, D, d + 4, hi, top, sum);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kOEmpty));
+      // every warp is past this piece's statistics, masks and scaling before they are written again
+      named_barrier_sync(6, 256);
+      ++piece;
+    }
+  }
+  __syncwarp();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kColAll);
+  }
+}
+
+template <int D, int BITS>
+cudaError_t launch_tree(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
+  using C = TreeCfg<D, BITS>;
+  static_assert(C::kSmem <= 232448, "shared memory budget");
+  const void* kern = reinterpret_cast<const void*>(tree_kernel<D, BITS>);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ensure_max_dynamic_smem(kern, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  // the warpgroups' register increase draws on what the CTA was launched with
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+  PartsArgs parts;
+  ScratchSource scratch = ScratchSource::pooled(st);
+  e = parts.allocate(scratch, num_sms, kTileRows, D);
+  if (e != cudaSuccess) return e;
+  tree_kernel<D, BITS><<<num_sms, kThreads, C::kSmem, st>>>(a, parts, bf16);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join(a, parts, num_sms, std::min(kTileRows, a.max_nodes * (a.q_heads / a.cache.heads)),
+                     bf16, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tree(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
+  if (a.cache.head_dim == 128)
+    return a.cache.bits == 8 ? launch_tree<128, 8>(a, bf16, num_sms, st)
+                             : launch_tree<128, 4>(a, bf16, num_sms, st);
+  return a.cache.bits == 8 ? launch_tree<64, 8>(a, bf16, num_sms, st)
+                           : launch_tree<64, 4>(a, bf16, num_sms, st);
+}
+
+}  // namespace cider
