@@ -20,9 +20,11 @@
 //
 // Roles (640 threads, one CTA per SM, persistent over its share of the axis):
 //   warp 0        one thread issues the MMAs
-//   warps 4-11    converters: codes from global memory (prefetched to L2 four
-//                 to seven tiles ahead, to registers one ahead) to fp16 tiles
-//                 in shared memory; each position's sk, log2 sv, 1 / sv
+//   warps 4-11    converters: codes by asynchronous copies into a ring in which
+//                 every thread reads back only its own 16-byte chunks (no
+//                 barrier; loads into registers, half a tile ahead, left them
+//                 waiting for 5000 cycles a tile), to fp16 tiles in shared
+//                 memory; each position's sk, log2 sv, 1 / sv
 //   warps 12-19   softmax: warps 12-15 the tile's first 64 positions, 16-19 the
 //                 last 64, each warp its quarter of the rows.  S is read in the
 //                 layout that gives a thread 4 rows x 2 neighbouring positions,
@@ -73,7 +75,15 @@ struct TreeCfg {
   static constexpr int kStatOffset = kScaleOffset + 2 * kScaleStage;
   static constexpr int kStatBytes = 2 * kTileRows * 8;       // per half and row: two floats
   static constexpr int kMaskOffset = kStatOffset + kStatBytes;
-  static constexpr int kBarOffset = kMaskOffset + kTileRows * 8;
+  // Codes on their way: each converter thread's own chunks of a K or V tile per
+  // slot, and the scales of a tile's positions.
+  static constexpr int kRingOffset = kMaskOffset + kTileRows * 8;
+  static constexpr int kRingSlot = kConvWarps * 32 * kLoads * 16;
+  static constexpr int kScaleRing = 4 * 2 * kTilePos * 4;    // four tiles of sk, sv
+  static constexpr int kFit = (231 * 1024 - 4096 - kRingOffset - kScaleRing) / kRingSlot;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;         // at most: the scales' four tiles
+  static constexpr int kScaleRingOffset = kRingOffset + kSlots * kRingSlot;
+  static constexpr int kBarOffset = kScaleRingOffset + kScaleRing;
   static constexpr int kSmem = kBarOffset + 32 * 8 + 64 + 1024;
   // Order of the dims in the fp16 tiles: unit `lin` of a row (8 values) holds
   // codes (lin / kChunks) * 8 .. + 8 of chunk lin % kChunks, so that the lanes
@@ -226,10 +236,15 @@ __device__ __forceinline__ uint4 convert_unit(const uint4& c, int h) {
   return r;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)),
-               "r"(bytes)
-               : "memory");
+// BYTES from global to shared memory; zeros without `there`.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src, bool there) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
+                 : "memory");
+  else
+    cp_async4(dst, src, there);
 }
 
 template <int D, int BITS>
@@ -363,10 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     Axis axis;
     axis.begin(a, kTilePos, lane, kTileRows);
-    bool more = axis.more();
-    // the cursor of the loads, one tile ahead of the conversion
+    const int64_t all = axis.more() ? axis.end - axis.at : 0;   // tiles of the share
+    // the cursor of the copies runs kSlots - 1 tiles of K or V ahead of the conversion
+    bool more = axis.more(), values = false;
     int tile = 0, tiles = 0, first_block = 0, last_block = 0;   // 16-position blocks of the piece
     int ids = -1, next_ids = -1;   // lane l: row / 16 of block 32 i + l (four tiles), -1 without a page
+    uint32_t slot_in = 0, tile_in = 0;
     const int32_t* table = nullptr;
     auto load_ids = [&](int base) -> int {
       const int blk = first_block + base + lane;
@@ -386,75 +403,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       last_block = static_cast<int>(min(axis.piece_end * 8, (axis.req.length + 15) / 16));
       table = a.table + axis.b * a.table_width;
       ids = load_ids(0);
-      next_ids = -1;
+      next_ids = load_ids(32);
     };
-    // row / 16 of 16-position block `blk` (0 .. 7) of the cursor's tile
-    auto block_row = [&](int blk) { return __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + blk); };
-    auto load_side = [&](const uint8_t* codes, uint4 (&r)[C::kLoads]) {
+    const uint32_t own = sbase + C::kRingOffset + (threadIdx.x - kConvWarp0 * 32) * 16;
+    const uint32_t own_scale = sbase + C::kScaleRingOffset + token_s * 4;
+    auto copy_next = [&]() {   // the cursor's K or V tile into the next slot
+      if (more) {
+        const uint8_t* codes = values ? a.cache.v : a.cache.k;
+#pragma unroll
+        for (int j = 0; j < C::kLoads; ++j) {
+          const int first = (j * kConvWarps + cw) * C::kRowsPer;   // of the warp's rows
+          const int at = __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + (first >> 4));
+          const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (first & 15) + row;
+          cp_async_bytes<16>(own + slot_in * C::kRingSlot + j * (kConvWarps * 32 * 16),
+                             codes + src * C::kRowBytes + c * 16, at >= 0);
+        }
+        if (!values) {
+          const int at = __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + (token_s >> 4));
+          const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (token_s & 15);
+          if (cw < 4) {
+            const uint32_t dst = own_scale + (tile_in & 3) * (2 * kTilePos * 4);
+            cp_async_bytes<4>(dst, a.cache.k_scale + src, at >= 0);
+            cp_async_bytes<4>(dst + kTilePos * 4, a.cache.v_scale + src, at >= 0);
+          }
+        }
+        slot_in = slot_in + 1 == C::kSlots ? 0 : slot_in + 1;
+        if (values) {
+          ++tile_in;
+          if ((++tile & 3) == 0) {   // ids four tiles further are loaded when these begin
+            ids = next_ids;
+            next_ids = load_ids((tile + 4) * 8);
+          }
+          if (tile == tiles) {
+            more = axis.next(a, kTilePos, kTileRows);
+            if (more) open();
+          }
+        }
+        values = !values;
+      }
+      cp_async_commit();
+    };
+    uint32_t slot_out = 0;
+    auto convert_side = [&](uint8_t* dst) {
+      cp_async_wait<C::kSlots - 2>();
+      const uint8_t* src = smem + C::kRingOffset + slot_out * C::kRingSlot +
+                           (threadIdx.x - kConvWarp0 * 32) * 16;
+      slot_out = slot_out + 1 == C::kSlots ? 0 : slot_out + 1;
 #pragma unroll
       for (int j = 0; j < C::kLoads; ++j) {
-        const int first = (j * kConvWarps + cw) * C::kRowsPer;   // of the warp's rows
-        const int at = block_row(first >> 4);
-        const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (first & 15) + row;
-        r[j] = at >= 0 ? *reinterpret_cast<const uint4*>(codes + src * C::kRowBytes + c * 16)
-                       : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto load_scales = [&](float& sk, float& sv) {
-      const int at = block_row(token_s >> 4);
-      const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (token_s & 15);
-      sk = at >= 0 ? a.cache.k_scale[src] : 0.0f;
-      sv = at >= 0 ? a.cache.v_scale[src] : 0.0f;
-    };
-    // after a tile's loads: the cursor moves on; ids for the four tiles after
-    // the next boundary are loaded one tile after a boundary, and their codes
-    // prefetched to L2 one tile later
-    auto step = [&]() {
-      if ((tile & 3) == 0) next_ids = load_ids((tile + 4) * 8);
-      if ((tile & 3) == 1 && (lane & 7) == cw && next_ids >= 0) {
-        const int64_t r = static_cast<int64_t>(next_ids) * 16;
-        prefetch_l2(a.cache.k + r * C::kRowBytes, 16 * C::kRowBytes);
-        prefetch_l2(a.cache.v + r * C::kRowBytes, 16 * C::kRowBytes);
-        prefetch_l2(a.cache.k_scale + r, 64);
-        prefetch_l2(a.cache.v_scale + r, 64);
-      }
-      ++tile;
-      if ((tile & 3) == 0) ids = next_ids;
-      if (tile == tiles) {
-        more = axis.next(a, kTilePos, kTileRows);
-        if (more) open();
-      }
-    };
-    auto store_side = [&](uint8_t* dst, const uint4 (&r)[C::kLoads]) {
-#pragma unroll
-      for (int j = 0; j < C::kLoads; ++j) {
+        const uint4 in = *reinterpret_cast<const uint4*>(src + j * (kConvWarps * 32 * 16));
         const int token = token0 + j * kConvWarps * C::kRowsPer;
 #pragma unroll
         for (int h = 0; h < C::kUnits; ++h) {
           const int lin = c + C::kChunks * h;
-          const uint4 v = convert_unit<BITS>(r[j], h);
           *reinterpret_cast<uint4*>(dst + (lin >> 3) * C::kSub + token * 128 +
-                                    (((lin & 7) ^ (token & 7)) << 4)) = v;
+                                    (((lin & 7) ^ (token & 7)) << 4)) = convert_unit<BITS>(in, h);
         }
       }
     };
-    uint4 rk[C::kLoads], rv[C::kLoads];
-    float sk = 0.0f, sv = 0.0f;
-    if (more) {
-      open();
-      load_side(a.cache.k, rk);
-      load_scales(sk, sv);
-      load_side(a.cache.v, rv);
-    }
-    uint32_t n = 0;
-    bool have = more;
-    while (have) {
+    if (more) open();
+#pragma unroll 1
+    for (int i = 0; i < C::kSlots - 1; ++i) copy_next();
+    for (uint32_t n = 0; n < all; ++n) {
       const uint32_t st = n & 1, ph = n >> 1;
       uint8_t* kt = smem + st * 2 * C::kSide;
       wait(kKEmpty + st, ph + 1);
       wait(kScEmpty + st, ph + 1);
-      store_side(kt, rk);
+      convert_side(kt);
       if (cw < 4) {
+        const float* in = reinterpret_cast<const float*>(smem + C::kScaleRingOffset) + (n & 3) * 2 * kTilePos + token_s;
+        const float sk = in[0], sv = in[kTilePos];
         float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + st * C::kScaleStage);
         const int pair = token_s >> 1, e = token_s & 1;
         const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
@@ -468,22 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKFull + st));
-      // the values of this tile are in registers; the cursor moves on, but the
-      // registers of V are only loaded again once they are stored
-      step();
-      if (more) {
-        load_side(a.cache.k, rk);
-        load_scales(sk, sv);
-      }
+      copy_next();   // into the slot that was just read
       wait(kVEmpty + st, ph + 1);
-      store_side(kt + C::kSide, rv);
+      convert_side(kt + C::kSide);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kVFull + st));
-      if (more) load_side(a.cache.v, rv);
-      have = more;
-      ++n;
+      copy_next();
     }
+    cp_async_wait<0>();
   } else {
     regs_inc<kRegsSoft>();
     // --------------------------------------------------------------- softmax
