@@ -19,7 +19,7 @@
 // conversion and softmax instructions in practice.
 //
 // Roles (640 threads, one CTA per SM, persistent over its share of the axis):
-//   warp 0        one thread issues the MMAs
+//   warps 0, 1    one thread each issues the MMAs of S and of O
 //   warps 4-11    converters: codes by asynchronous copies into a ring in which
 //                 every thread reads back only its own 16-byte chunks (no
 //                 barrier; loads into registers, half a tile ahead, left them
@@ -96,7 +96,7 @@ struct TreeCfg {
 // Barriers, by number.
 enum Bar : int {
   kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScEmpty = 8, kSFull = 10, kPReady = 12,
-  kQFull = 14, kOFull = 15, kOEmpty = 16, kDone = 17, kBars = 18
+  kQFull = 14, kOFull = 15, kOEmpty = 16, kDone = 17, kBars = 19
 };
 
 template <int R>
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kOFull), 1);
       mbar_init(bar(kOEmpty), kSoftWarps);
       mbar_init(bar(kDone), 1);
+      mbar_init(bar(kDone + 1), 1);
       fence_mbar_init();
     }
     __syncwarp();
@@ -297,62 +298,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   // accesses stay in bounds), so that no barrier is left with a thread missing.
   if (warp < kConvWarp0) {
     regs_dec<kRegsMisc>();
+    // Two issuers: an MMA takes a thread ~75 cycles and more to issue, sixteen a
+    // tile are more than the tile's tensor time.  Whole-warp waits, one lane issues.
     if (warp == 0) {
+      // S(n) = Q K(n)^T
       Axis axis;
       axis.begin(a, kTilePos, lane, kTileRows);
       if (lane == 0) parts.announce(axis);
       bool more = axis.more();
+      const uint64_t desc0 = smem_desc_k_sw128(sbase);
       uint32_t n = 0, piece = 0;
-      // whole-warp waits; one lane issues
+      bool ok = true;
       while (more) {
         const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
-        bool ok = wait(kQFull, piece);
-        tc_fence_after();
-        for (int i = 0; i <= tiles; ++i) {
-          if (i < tiles) {   // S(n) = Q K(n)^T
-            const uint32_t st = n & 1, ph = n >> 1;
-            ok = wait(kKFull + st, ph) && ok;
-            tc_fence_after();
-            if (lane == 0 && ok) {
-              const uint32_t kt = sbase + st * 2 * C::kSide;
+        more = axis.next(a, kTilePos, kTileRows);
+        ok = wait(kQFull, piece) && ok;
+        for (int i = 0; i < tiles; ++i, ++n) {
+          const uint32_t st = n & 1, ph = n >> 1;
+          ok = wait(kKFull + st, ph) && ok;
+          ok = wait(kVEmpty + st, ph + 1) && ok;   // P(n - 2), in the same columns, is read
+          tc_fence_after();
+          if (lane == 0 && ok) {
+            const uint64_t desc = desc0 + st * (2 * C::kSide >> 4);
+            const uint32_t d = tmem + kColS + st * 128;
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s)
-                tc_mma_ts(tmem + kColS + st * 128, tmem + kColQ + s * 8,
-                          smem_desc_k_sw128(kt + (s >> 2) * C::kSub + (s & 3) * 32),
-                          idesc_f16_f32(128, 128), s > 0);
-              tc_commit(bar(kSFull + st));
-              tc_commit(bar(kKEmpty + st));
-            }
-            __syncwarp();
+            for (int s = 0; s < D / 16; ++s)
+              tc_mma_ts(d, tmem + kColQ + s * 8, desc + ((s >> 2) * C::kSub + (s & 3) * 32 >> 4),
+                        idesc_f16_f32(128, 128), s > 0);
+            tc_commit(bar(kSFull + st));
+            tc_commit(bar(kKEmpty + st));
           }
-          if (i > 0) {   // O += P(n - 1) V(n - 1)
-            const uint32_t m = n - 1, st = m & 1, ph = m >> 1;
-            if (i == 1) ok = wait(kOEmpty, piece + 1) && ok;
-            ok = wait(kPReady + st, ph) && ok;
-            ok = wait(kVFull + st, ph) && ok;
-            tc_fence_after();
-            if (lane == 0 && ok) {
-              const uint32_t vt = sbase + st * 2 * C::kSide + C::kSide;
-#pragma unroll
-              for (int s = 0; s < kTilePos / 16; ++s)
-                tc_mma_ts(tmem + kColO, tmem + kColS + st * 128 + (s >> 2) * 64 + (s & 3) * 8,
-                          smem_desc_mn_sw128(vt + s * 2048, C::kSub),
-                          idesc_f16_f32(128, D) | kBMajorMn, (i > 1 || s > 0) ? 1u : 0u);
-              tc_commit(bar(kVEmpty + st));
-              if (i == tiles) tc_commit(bar(kOFull));
-            }
-            __syncwarp();
-          }
-          if (i < tiles) ++n;
+          __syncwarp();
         }
         ++piece;
-        more = axis.next(a, kTilePos, kTileRows);
       }
-      // no MMA may be in flight when the tensor memory is freed, also after an abort
+    } else if (warp == 1) {
+      // O += P(n) V(n)
+      Axis axis;
+      axis.begin(a, kTilePos, lane, kTileRows);
+      bool more = axis.more();
+      const uint64_t desc0 = smem_desc_mn_sw128(sbase + C::kSide, C::kSub);
+      uint32_t n = 0, piece = 0;
+      bool ok = true;
+      while (more) {
+        const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+        more = axis.next(a, kTilePos, kTileRows);
+        ok = wait(kOEmpty, piece + 1) && ok;
+        for (int i = 0; i < tiles; ++i, ++n) {
+          const uint32_t st = n & 1, ph = n >> 1;
+          ok = wait(kVFull + st, ph) && ok;
+          ok = wait(kPReady + st, ph) && ok;
+          tc_fence_after();
+          if (lane == 0 && ok) {
+            const uint64_t desc = desc0 + st * (2 * C::kSide >> 4);
+            const uint32_t p = tmem + kColS + st * 128;
+#pragma unroll
+            for (int s = 0; s < kTilePos / 16; ++s)
+              tc_mma_ts(tmem + kColO, p + (s >> 2) * 64 + (s & 3) * 8, desc + (s * 2048 >> 4),
+                        idesc_f16_f32(128, D) | kBMajorMn, (i > 0 || s > 0) ? 1u : 0u);
+            tc_commit(bar(kVEmpty + st));
+            if (i == tiles - 1) tc_commit(bar(kOFull));
+          }
+          __syncwarp();
+        }
+        ++piece;
+      }
+    }
+    // no MMA may be in flight when the tensor memory is freed, also after an abort
+    if (warp < 2) {
       if (lane == 0) {
-        tc_commit(bar(kDone));
+        tc_commit(bar(kDone + warp));
         volatile uint32_t keep_waiting = 0u;
-        mbar_wait_bounded(bar(kDone), 0, &keep_waiting, a.err, kWaitNs);
+        mbar_wait_bounded(bar(kDone + warp), 0, &keep_waiting, a.err, kWaitNs);
       }
       __syncwarp();
     }
@@ -605,11 +622,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2* iv = reinterpret_cast<const float2*>(smem + C::kScaleOffset + st * C::kScaleStage + 1024) +
                              half * 32 + t;
           const bool masked = context - pos < 64;
-          // x of 32 positions (chunk ch), for the rows g + 8 h + 16 hh: [hh][4 j + 2 h + e]
-          auto load_x = [&](int ch, float (&x)[2][16]) {
+          auto fetch = [&](int ch, float (&x)[2][16]) {
             tmem_ld_16x256b_x4(s_at + ch * 32, x[0]);
             tmem_ld_16x256b_x4(s_at + ch * 32 + (16u << 16), x[1]);
-            tmem_wait_ld();
+          };
+          // x of 32 positions (chunk ch), for the rows g + 8 h + 16 hh: [hh][4 j + 2 h + e]
+          auto scale_x = [&](int ch, float (&x)[2][16]) {
             loaded(x[0]);
             loaded(x[1]);
 #pragma unroll
@@ -648,10 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               high[r] = __half2half2(__ushort_as_half(0));
               sum[r] = f2(0.0f, 0.0f);
             }
+            float xs[2][2][16];
+            fetch(0, xs[0]);
+            fetch(1, xs[1]);
+            tmem_wait_ld();
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
-              float x[2][16];
-              load_x(ch, x);
+              float (&x)[2][16] = xs[ch];
+              scale_x(ch, x);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const float2 v = iv[ch * 16 + 4 * j];
@@ -688,7 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
               float x[2][16];
-              load_x(ch, x);
+              fetch(ch, x);
+              tmem_wait_ld();
+              scale_x(ch, x);
 #pragma unroll
               for (int r = 0; r < 4; ++r)
 #pragma unroll
