@@ -20,11 +20,12 @@
 //
 // Roles (640 threads, one CTA per SM, persistent over its share of the axis):
 //   warps 0, 1    one thread each issues the MMAs of S and of O
-//   warps 4-11    converters: codes by asynchronous copies into a ring in which
-//                 every thread reads back only its own 16-byte chunks (no
-//                 barrier; loads into registers, half a tile ahead, left them
-//                 waiting for 5000 cycles a tile), to fp16 tiles in shared
-//                 memory; each position's sk, log2 sv, 1 / sv
+//   warp 2        loads the codes as they are cached, by bulk copies of 16
+//                 positions (one per lane), into a ring in shared memory
+//   warps 4-11    converters: codes to fp16 tiles in shared memory; each
+//                 position's sk, log2 sv, 1 / sv.  (Loading the codes themselves,
+//                 to registers or by asynchronous copies, was what held a tile
+//                 up: 5000 and 3300 cycles.)
 //   warps 12-19   softmax: warps 12-15 the tile's first 64 positions, 16-19 the
 //                 last 64, each warp its quarter of the rows.  S is read in the
 //                 layout that gives a thread 4 rows x 2 neighbouring positions,
@@ -53,7 +54,7 @@ constexpr int kTilePos = 128;     // positions of a tile
 constexpr int kThreads = 640;
 constexpr int kConvWarp0 = 4, kConvWarps = 8;
 constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
-constexpr int kRegsMisc = 32, kRegsConv = 80, kRegsSoft = 144, kRegsLaunch = 96;
+constexpr int kRegsMisc = 64, kRegsConv = 64, kRegsSoft = 144, kRegsLaunch = 96;
 constexpr int kRegsNeeded = 128 * kRegsMisc + 256 * kRegsConv + 256 * kRegsSoft;
 static_assert(kRegsNeeded <= kThreads * kRegsLaunch, "register split exceeds the launch's registers");
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -72,19 +73,19 @@ struct TreeCfg {
   static constexpr int kSide = kSub * (D / 64);              // a K or V tile
   static constexpr int kScaleOffset = 4 * kSide;             // two stages of K, V
   static constexpr int kScaleStage = 64 * 16 + 64 * 8;       // per pair of positions: sk sk lg lg, inv inv
-  static constexpr int kStatOffset = kScaleOffset + 2 * kScaleStage;
+  static constexpr int kStatOffset = kScaleOffset + 4 * kScaleStage;
   static constexpr int kStatBytes = 2 * kTileRows * 8;       // per half and row: two floats
   static constexpr int kMaskOffset = kStatOffset + kStatBytes;
-  // Codes on their way: each converter thread's own chunks of a K or V tile per
-  // slot, and the scales of a tile's positions.
+  // Codes as they are cached, on their way to the converters: a K or a V tile
+  // per slot, and the scales of a tile's positions.
   static constexpr int kRingOffset = kMaskOffset + kTileRows * 8;
-  static constexpr int kRingSlot = kConvWarps * 32 * kLoads * 16;
+  static constexpr int kRingSlot = kTilePos * kRowBytes;
   static constexpr int kScaleRing = 4 * 2 * kTilePos * 4;    // four tiles of sk, sv
-  static constexpr int kFit = (231 * 1024 - 4096 - kRingOffset - kScaleRing) / kRingSlot;
+  static constexpr int kFit = (226 * 1024 - kRingOffset - kScaleRing) / kRingSlot;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;         // at most: the scales' four tiles
   static constexpr int kScaleRingOffset = kRingOffset + kSlots * kRingSlot;
   static constexpr int kBarOffset = kScaleRingOffset + kScaleRing;
-  static constexpr int kSmem = kBarOffset + 32 * 8 + 64 + 1024;
+  static constexpr int kSmem = kBarOffset + 40 * 8 + 64 + 1024;
   // Order of the dims in the fp16 tiles: unit `lin` of a row (8 values) holds
   // codes (lin / kChunks) * 8 .. + 8 of chunk lin % kChunks, so that the lanes
   // that convert a row's chunks store to different banks.
@@ -95,8 +96,8 @@ struct TreeCfg {
 
 // Barriers, by number.
 enum Bar : int {
-  kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScEmpty = 8, kSFull = 10, kPReady = 12,
-  kQFull = 14, kOFull = 15, kOEmpty = 16, kDone = 17, kBars = 19
+  kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kQFull = 12,
+  kOFull = 13, kOEmpty = 14, kDone = 15, kRawFull = 17, kRawEmpty = 25, kBars = 33
 };
 
 template <int R>
@@ -236,15 +237,22 @@ __device__ __forceinline__ uint4 convert_unit(const uint4& c, int h) {
   return r;
 }
 
-// BYTES from global to shared memory; zeros without `there`.
-template <int BYTES>
-__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src, bool there) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
-                 : "memory");
-  else
-    cp_async4(dst, src, there);
+// The MMAs of a tile in stage ST: S = Q K^T, and O (+)= P V.
+template <typename C, int ST>
+__device__ __forceinline__ void issue_s(uint32_t sbase) {
+  const uint64_t desc = smem_desc_k_sw128(sbase + ST * 2 * C::kSide);
+#pragma unroll
+  for (int s = 0; s < C::kSide / C::kSub * 4; ++s)
+    tc_mma_ts(kColS + ST * 128, kColQ + s * 8, desc + ((s >> 2) * C::kSub + (s & 3) * 32 >> 4),
+              idesc_f16_f32(128, 128), s > 0);
+}
+template <typename C, int D, int ST>
+__device__ __forceinline__ void issue_o(uint32_t sbase, bool add) {
+  const uint64_t desc = smem_desc_mn_sw128(sbase + ST * 2 * C::kSide + C::kSide, C::kSub);
+#pragma unroll
+  for (int s = 0; s < kTilePos / 16; ++s)
+    tc_mma_ts(kColO, kColS + ST * 128 + (s >> 2) * 64 + (s & 3) * 8, desc + (s * 2048 >> 4),
+              idesc_f16_f32(128, D) | kBMajorMn, s > 0 ? 1u : add ? 1u : 0u);
 }
 
 template <int D, int BITS>
@@ -273,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(kKEmpty + s), 1);
         mbar_init(bar(kVFull + s), kConvWarps);
         mbar_init(bar(kVEmpty + s), 1);
-        mbar_init(bar(kScEmpty + s), kSoftWarps);
         mbar_init(bar(kSFull + s), 1);
         mbar_init(bar(kPReady + s), kSoftWarps);
       }
@@ -282,6 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kOEmpty), kSoftWarps);
       mbar_init(bar(kDone), 1);
       mbar_init(bar(kDone + 1), 1);
+      for (int s = 0; s < C::kSlots; ++s) {
+        mbar_init(bar(kRawFull + s), 1);
+        mbar_init(bar(kRawEmpty + s), kConvWarps);
+      }
       fence_mbar_init();
     }
     __syncwarp();
@@ -291,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // all 512 columns are this CTA's: they begin at 0 (a constant for the MMAs' operands)
+  constexpr uint32_t tmem = 0;
 
   // Every role walks the same pieces.  A wait that gives up raises the abort
   // flag; the roles then run to their ends without waiting (all their memory
@@ -306,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       axis.begin(a, kTilePos, lane, kTileRows);
       if (lane == 0) parts.announce(axis);
       bool more = axis.more();
-      const uint64_t desc0 = smem_desc_k_sw128(sbase);
       uint32_t n = 0, piece = 0;
       bool ok = true;
       while (more) {
@@ -319,12 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kVEmpty + st, ph + 1) && ok;   // P(n - 2), in the same columns, is read
           tc_fence_after();
           if (lane == 0 && ok) {
-            const uint64_t desc = desc0 + st * (2 * C::kSide >> 4);
-            const uint32_t d = tmem + kColS + st * 128;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              tc_mma_ts(d, tmem + kColQ + s * 8, desc + ((s >> 2) * C::kSub + (s & 3) * 32 >> 4),
-                        idesc_f16_f32(128, 128), s > 0);
+            // a constant stage keeps every operand a constant or uniform
+            if (st == 0) issue_s<C, 0>(sbase); else issue_s<C, 1>(sbase);
             tc_commit(bar(kSFull + st));
             tc_commit(bar(kKEmpty + st));
           }
@@ -337,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       Axis axis;
       axis.begin(a, kTilePos, lane, kTileRows);
       bool more = axis.more();
-      const uint64_t desc0 = smem_desc_mn_sw128(sbase + C::kSide, C::kSub);
       uint32_t n = 0, piece = 0;
       bool ok = true;
       while (more) {
@@ -350,12 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kPReady + st, ph) && ok;
           tc_fence_after();
           if (lane == 0 && ok) {
-            const uint64_t desc = desc0 + st * (2 * C::kSide >> 4);
-            const uint32_t p = tmem + kColS + st * 128;
-#pragma unroll
-            for (int s = 0; s < kTilePos / 16; ++s)
-              tc_mma_ts(tmem + kColO, p + (s >> 2) * 64 + (s & 3) * 8, desc + (s * 2048 >> 4),
-                        idesc_f16_f32(128, D) | kBMajorMn, (i > 0 || s > 0) ? 1u : 0u);
+            if (st == 0) issue_o<C, D, 0>(sbase, i > 0); else issue_o<C, D, 1>(sbase, i > 0);
             tc_commit(bar(kVEmpty + st));
             if (i == tiles - 1) tc_commit(bar(kOFull));
           }
@@ -363,6 +364,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++piece;
       }
+    }
+    else if (warp == 2) {
+      // loads: lanes 0-7 a tile's eight runs of 16 positions, K and then V, lanes
+      // 8-15 and 16-23 their scales; each run is contiguous in its page
+      Axis axis;
+      axis.begin(a, kTilePos, lane, kTileRows);
+      bool more = axis.more();
+      const int page16 = a.cache.page_shift - 4;
+      const int blk = lane & 7;
+      uint32_t side = 0, slot = 0, n = 0;   // slot = side mod kSlots
+      while (more) {
+        const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+        const int first = static_cast<int>(axis.piece_begin) * 8;
+        const int last = static_cast<int>(min(axis.piece_end * 8, (axis.req.length + 15) / 16));
+        const int head = axis.unit / Axis::blocks_of(a, axis.req, kTileRows);
+        const int32_t* table = a.table + axis.b * a.table_width;
+        // lane l: row / 16 of run 32 i + l (four tiles), -1 without a page; loaded four tiles ahead
+        auto load_ids = [&](int base) -> int {
+          const int at = first + base + lane;
+          if (at >= last) return -1;
+          const int32_t id = table[at >> page16];
+          if (id < 0 || id >= a.cache.pages) {
+            atomicOr(a.err, kDevErrIndex);
+            return -1;
+          }
+          return ((id * a.cache.heads + head) << page16) + (at & ((1 << page16) - 1));
+        };
+        int ids = load_ids(0), next = load_ids(32);
+        more = axis.next(a, kTilePos, kTileRows);
+        for (int i = 0; i < tiles; ++i, ++n) {
+          if (i > 0 && (i & 3) == 0) {
+            ids = next;
+            next = load_ids((i + 4) * 8);
+          }
+          const int run = __shfl_sync(0xffffffffu, ids, (i & 3) * 8 + blk);
+          const int64_t row = static_cast<int64_t>(max(run, 0)) * 16;
+          const uint32_t there = __popc(__ballot_sync(0xffffffffu, run >= 0) & 0xFFu);
+          const uint32_t scales = sbase + C::kScaleRingOffset + (n & 3) * 2 * kTilePos * 4 +
+                                  (lane < 16 ? 0 : kTilePos * 4) + blk * 64;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            wait(kRawEmpty + slot, side / C::kSlots + 1);
+            // a position without a page counts as one with scales of 0
+            if (v == 0 && run < 0 && lane >= 8 && lane < 24) {
+              const uint32_t zero[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) st_shared_v4(scales + 16 * j, zero);
+            }
+            __syncwarp();
+            const uint32_t full = bar(kRawFull + slot);
+            if (lane == 0) mbar_arrive_expect_tx(full, there * (16 * C::kRowBytes + (v == 0 ? 128 : 0)));
+            __syncwarp();
+            if (run >= 0) {
+              if (lane < 8)
+                bulk_load(sbase + C::kRingOffset + slot * C::kRingSlot + blk * 16 * C::kRowBytes,
+                          (v == 0 ? a.cache.k : a.cache.v) + row * C::kRowBytes, 16 * C::kRowBytes, full);
+              else if (v == 0 && lane < 24)
+                bulk_load(scales, (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + row, 64, full);
+            }
+            __syncwarp();
+            ++side;
+            slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+          }
+        }
+      }
+      // no copy may be in flight when the CTA ends, also after an abort
+      volatile uint32_t keep_waiting = 0u;
+      for (uint32_t j = side > C::kSlots ? side - C::kSlots : 0; j < side; ++j)
+        mbar_wait_bounded(bar(kRawFull + j % C::kSlots), j / C::kSlots & 1, &keep_waiting, a.err, kWaitNs);
     }
     // no MMA may be in flight when the tensor memory is freed, also after an abort
     if (warp < 2) {
@@ -390,107 +460,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int token0 = cw * C::kRowsPer + row;   // of load j: + j * kConvWarps * kRowsPer
     const int token_s = (cw & 3) * 32 + lane;    // warps 4-7: this lane's position's scales
-    const int page16 = a.cache.page_shift - 4;
     const float mul = a.scale * 1.44269504f * (BITS == 4 ? 512.0f : 1.0f);
+    uint8_t* dst[C::kUnits];                     // of load 0: 1024 bytes further for 8 tokens
+#pragma unroll
+    for (int h = 0; h < C::kUnits; ++h) {
+      const int lin = c + C::kChunks * h;
+      dst[h] = smem + (lin >> 3) * C::kSub + token0 * 128 + (((lin & 7) ^ (token0 & 7)) << 4);
+    }
+    static_assert(kConvWarps * C::kRowsPer % 8 == 0, "the swizzle of a lane's rows is the same");
+    const uint8_t* src0 = smem + C::kRingOffset + token0 * C::kRowBytes + c * 16;
+    uint32_t side = 0, slot = 0;
+    auto convert_side = [&](int to) {   // the next slot's tile to the stage at `to`
+      wait(kRawFull + slot, side / C::kSlots);
+      uint4 in[C::kLoads];
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j)
+        in[j] = *reinterpret_cast<const uint4*>(src0 + slot * C::kRingSlot + j * (kConvWarps * 512));
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j)
+#pragma unroll
+        for (int h = 0; h < C::kUnits; ++h)
+          *reinterpret_cast<uint4*>(dst[h] + to + j * (kConvWarps * C::kRowsPer * 128)) =
+              convert_unit<BITS>(in[j], h);
+    };
+    auto release_side = [&]() {   // after the warp's loads of the slot
+      if (lane == 0) mbar_arrive(bar(kRawEmpty + slot));
+      ++side;
+      slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+    };
 
     Axis axis;
     axis.begin(a, kTilePos, lane, kTileRows);
     const int64_t all = axis.more() ? axis.end - axis.at : 0;   // tiles of the share
-    // the cursor of the copies runs kSlots - 1 tiles of K or V ahead of the conversion
-    bool more = axis.more(), values = false;
-    int tile = 0, tiles = 0, first_block = 0, last_block = 0;   // 16-position blocks of the piece
-    int ids = -1, next_ids = -1;   // lane l: row / 16 of block 32 i + l (four tiles), -1 without a page
-    uint32_t slot_in = 0, tile_in = 0;
-    const int32_t* table = nullptr;
-    auto load_ids = [&](int base) -> int {
-      const int blk = first_block + base + lane;
-      if (blk >= last_block) return -1;
-      const int32_t id = table[blk >> page16];
-      if (id < 0 || id >= a.cache.pages) {
-        atomicOr(a.err, kDevErrIndex);
-        return -1;
-      }
-      const int head = axis.unit / Axis::blocks_of(a, axis.req, kTileRows);
-      return ((id * a.cache.heads + head) << page16) + (blk & ((1 << page16) - 1));
-    };
-    auto open = [&]() {   // the cursor to the first tile of the axis' piece
-      tile = 0;
-      tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
-      first_block = static_cast<int>(axis.piece_begin) * 8;
-      last_block = static_cast<int>(min(axis.piece_end * 8, (axis.req.length + 15) / 16));
-      table = a.table + axis.b * a.table_width;
-      ids = load_ids(0);
-      next_ids = load_ids(32);
-    };
-    const uint32_t own = sbase + C::kRingOffset + (threadIdx.x - kConvWarp0 * 32) * 16;
-    const uint32_t own_scale = sbase + C::kScaleRingOffset + token_s * 4;
-    auto copy_next = [&]() {   // the cursor's K or V tile into the next slot
-      if (more) {
-        const uint8_t* codes = values ? a.cache.v : a.cache.k;
-#pragma unroll
-        for (int j = 0; j < C::kLoads; ++j) {
-          const int first = (j * kConvWarps + cw) * C::kRowsPer;   // of the warp's rows
-          const int at = __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + (first >> 4));
-          const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (first & 15) + row;
-          cp_async_bytes<16>(own + slot_in * C::kRingSlot + j * (kConvWarps * 32 * 16),
-                             codes + src * C::kRowBytes + c * 16, at >= 0);
-        }
-        if (!values) {
-          const int at = __shfl_sync(0xffffffffu, ids, (tile & 3) * 8 + (token_s >> 4));
-          const int64_t src = static_cast<int64_t>(max(at, 0)) * 16 + (token_s & 15);
-          if (cw < 4) {
-            const uint32_t dst = own_scale + (tile_in & 3) * (2 * kTilePos * 4);
-            cp_async_bytes<4>(dst, a.cache.k_scale + src, at >= 0);
-            cp_async_bytes<4>(dst + kTilePos * 4, a.cache.v_scale + src, at >= 0);
-          }
-        }
-        slot_in = slot_in + 1 == C::kSlots ? 0 : slot_in + 1;
-        if (values) {
-          ++tile_in;
-          if ((++tile & 3) == 0) {   // ids four tiles further are loaded when these begin
-            ids = next_ids;
-            next_ids = load_ids((tile + 4) * 8);
-          }
-          if (tile == tiles) {
-            more = axis.next(a, kTilePos, kTileRows);
-            if (more) open();
-          }
-        }
-        values = !values;
-      }
-      cp_async_commit();
-    };
-    uint32_t slot_out = 0;
-    auto convert_side = [&](uint8_t* dst) {
-      cp_async_wait<C::kSlots - 2>();
-      const uint8_t* src = smem + C::kRingOffset + slot_out * C::kRingSlot +
-                           (threadIdx.x - kConvWarp0 * 32) * 16;
-      slot_out = slot_out + 1 == C::kSlots ? 0 : slot_out + 1;
-#pragma unroll
-      for (int j = 0; j < C::kLoads; ++j) {
-        const uint4 in = *reinterpret_cast<const uint4*>(src + j * (kConvWarps * 32 * 16));
-        const int token = token0 + j * kConvWarps * C::kRowsPer;
-#pragma unroll
-        for (int h = 0; h < C::kUnits; ++h) {
-          const int lin = c + C::kChunks * h;
-          *reinterpret_cast<uint4*>(dst + (lin >> 3) * C::kSub + token * 128 +
-                                    (((lin & 7) ^ (token & 7)) << 4)) = convert_unit<BITS>(in, h);
-        }
-      }
-    };
-    if (more) open();
-#pragma unroll 1
-    for (int i = 0; i < C::kSlots - 1; ++i) copy_next();
     for (uint32_t n = 0; n < all; ++n) {
       const uint32_t st = n & 1, ph = n >> 1;
-      uint8_t* kt = smem + st * 2 * C::kSide;
+      // K's stage is free: S(n - 2) is done, so O(n - 4) is, and the softmax is
+      // past the scales of tile n - 4
       wait(kKEmpty + st, ph + 1);
-      wait(kScEmpty + st, ph + 1);
-      convert_side(kt);
+      convert_side(st * 2 * C::kSide);
       if (cw < 4) {
         const float* in = reinterpret_cast<const float*>(smem + C::kScaleRingOffset) + (n & 3) * 2 * kTilePos + token_s;
         const float sk = in[0], sv = in[kTilePos];
-        float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + st * C::kScaleStage);
+        float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage);
         const int pair = token_s >> 1, e = token_s & 1;
         const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
         float lg, inv;
@@ -503,15 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKFull + st));
-      copy_next();   // into the slot that was just read
+      release_side();
       wait(kVEmpty + st, ph + 1);
-      convert_side(kt + C::kSide);
+      convert_side(st * 2 * C::kSide + C::kSide);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kVFull + st));
-      copy_next();
+      release_side();
     }
-    cp_async_wait<0>();
   } else {
     regs_inc<kRegsSoft>();
     // --------------------------------------------------------------- softmax
@@ -617,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (active) {
           const uint32_t s_at = lanes + kColS + st * 128 + half * 64;
-          const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOffset + st * C::kScaleStage) +
+          const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage) +
                              half * 32 + t;
-          const float2* iv = reinterpret_cast<const float2*>(smem + C::kScaleOffset + st * C::kScaleStage + 1024) +
+          const float2* iv = reinterpret_cast<const float2*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage + 1024) +
                              half * 32 + t;
           const bool masked = context - pos < 64;
           auto fetch = [&](int ch, float (&x)[2][16]) {
@@ -769,10 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kScEmpty + st));
-          mbar_arrive(bar(kPReady + st));
-        }
+        if (lane == 0) mbar_arrive(bar(kPReady + st));
       }
 
       // ------------------------------------------------------------ the output
