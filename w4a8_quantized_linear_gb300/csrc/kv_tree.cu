@@ -20,8 +20,10 @@
 //
 // Roles (640 threads, one CTA per SM, persistent over its share of the axis):
 //   warps 0, 1    one thread each issues the MMAs of S and of O
-//   warp 2        loads the codes as they are cached, by bulk copies of 16
-//                 positions (one per lane), into a ring in shared memory
+//   warps 2, 3    load the codes as they are cached, keys and values, by bulk
+//                 copies of a page's part of a tile (each takes a lane ~80
+//                 cycles to issue, one lane after another), into a ring in
+//                 shared memory
 //   warps 4-11    converters: codes to fp16 tiles in shared memory; each
 //                 position's sk, log2 sv, 1 / sv.  (Loading the codes themselves,
 //                 to registers or by asynchronous copies, was what held a tile
@@ -365,73 +367,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++piece;
       }
     }
-    else if (warp == 2) {
-      // loads: lanes 0-7 a tile's eight runs of 16 positions, K and then V, lanes
-      // 8-15 and 16-23 their scales; each run is contiguous in its page
+    else {
+      // loads: warp 2 the keys and their scales, warp 3 the values and theirs, a
+      // run of positions that lie in one page per lane
+      const bool v = warp == 3;
+      const uint8_t* const codes = v ? a.cache.v : a.cache.k;
+      const float* const scale_src = v ? a.cache.v_scale : a.cache.k_scale;
       Axis axis;
       axis.begin(a, kTilePos, lane, kTileRows);
       bool more = axis.more();
-      const int page16 = a.cache.page_shift - 4;
-      const int blk = lane & 7;
-      uint32_t side = 0, slot = 0, n = 0;   // slot = side mod kSlots
+      const int run_shift = min(a.cache.page_shift, 7);
+      const int runs = kTilePos >> run_shift;                 // of a tile: 1, 2, 4 or 8
+      const uint32_t run_bytes = static_cast<uint32_t>(C::kRowBytes) << run_shift;
+      const uint32_t scale_bytes = 4u << run_shift;
+      uint32_t side = v ? 1 : 0, slot = side, n = 0;          // slot = side mod kSlots
       while (more) {
         const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
-        const int first = static_cast<int>(axis.piece_begin) * 8;
-        const int last = static_cast<int>(min(axis.piece_end * 8, (axis.req.length + 15) / 16));
+        const int first = static_cast<int>(axis.piece_begin) * runs;
+        const int last = static_cast<int>(min(axis.piece_end * runs,
+                                              (axis.req.length + (1 << run_shift) - 1) >> run_shift));
         const int head = axis.unit / Axis::blocks_of(a, axis.req, kTileRows);
         const int32_t* table = a.table + axis.b * a.table_width;
-        // lane l: row / 16 of run 32 i + l (four tiles), -1 without a page; loaded four tiles ahead
+        // lane l: the page of run 32 i + l, -1 without one
         auto load_ids = [&](int base) -> int {
           const int at = first + base + lane;
           if (at >= last) return -1;
-          const int32_t id = table[at >> page16];
-          if (id < 0 || id >= a.cache.pages) {
-            atomicOr(a.err, kDevErrIndex);
-            return -1;
-          }
-          return ((id * a.cache.heads + head) << page16) + (at & ((1 << page16) - 1));
+          const int32_t id = table[at >> (a.cache.page_shift - run_shift)];
+          if (id >= 0 && id < a.cache.pages) return id;
+          atomicOr(a.err, kDevErrIndex);
+          return -1;
         };
         int ids = load_ids(0), next = load_ids(32);
         more = axis.next(a, kTilePos, kTileRows);
         for (int i = 0; i < tiles; ++i, ++n) {
-          if (i > 0 && (i & 3) == 0) {
+          const int base = i * runs;
+          if (i > 0 && (base & 31) == 0) {
             ids = next;
-            next = load_ids((i + 4) * 8);
+            next = load_ids(base + 32);
           }
-          const int run = __shfl_sync(0xffffffffu, ids, (i & 3) * 8 + blk);
-          const int64_t row = static_cast<int64_t>(max(run, 0)) * 16;
-          const uint32_t there = __popc(__ballot_sync(0xffffffffu, run >= 0) & 0xFFu);
+          const int id = __shfl_sync(0xffffffffu, ids, (base & 31) + (lane & (runs - 1)));
+          const uint32_t there = __popc(__ballot_sync(0xffffffffu, id >= 0) & ((1u << runs) - 1));
+          // a page of 128 positions or fewer is one run
+          const int64_t row = a.cache.row(max(id, 0), head, 0);
           const uint32_t scales = sbase + C::kScaleRingOffset + (n & 3) * 2 * kTilePos * 4 +
-                                  (lane < 16 ? 0 : kTilePos * 4) + blk * 64;
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            wait(kRawEmpty + slot, side / C::kSlots + 1);
-            // a position without a page counts as one with scales of 0
-            if (v == 0 && run < 0 && lane >= 8 && lane < 24) {
-              const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) st_shared_v4(scales + 16 * j, zero);
-            }
-            __syncwarp();
-            const uint32_t full = bar(kRawFull + slot);
-            if (lane == 0) mbar_arrive_expect_tx(full, there * (16 * C::kRowBytes + (v == 0 ? 128 : 0)));
-            __syncwarp();
-            if (run >= 0) {
-              if (lane < 8)
-                bulk_load(sbase + C::kRingOffset + slot * C::kRingSlot + blk * 16 * C::kRowBytes,
-                          (v == 0 ? a.cache.k : a.cache.v) + row * C::kRowBytes, 16 * C::kRowBytes, full);
-              else if (v == 0 && lane < 24)
-                bulk_load(scales, (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + row, 64, full);
-            }
-            __syncwarp();
-            ++side;
-            slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+                                  (v ? kTilePos * 4 : 0) + lane * scale_bytes;
+          wait(kRawEmpty + slot, side / C::kSlots + 1);
+          // a position without a page counts as one with scales of 0
+          if (id < 0 && lane < runs) {
+            const uint32_t zero[4] = {0, 0, 0, 0};
+            for (uint32_t j = 0; j < scale_bytes; j += 16) st_shared_v4(scales + j, zero);
           }
+          __syncwarp();
+          const uint32_t full = bar(kRawFull + slot);
+          if (lane == 0) mbar_arrive_expect_tx(full, there * (run_bytes + scale_bytes));
+          __syncwarp();
+          if (id >= 0 && lane < runs) {
+            bulk_load(sbase + C::kRingOffset + slot * C::kRingSlot + lane * run_bytes,
+                      codes + row * C::kRowBytes, run_bytes, full);
+            bulk_load(scales, scale_src + row, scale_bytes, full);
+          }
+          __syncwarp();
+          side += 2;
+          slot = slot + 2 >= C::kSlots ? slot + 2 - C::kSlots : slot + 2;
         }
       }
       // no copy may be in flight when the CTA ends, also after an abort
       volatile uint32_t keep_waiting = 0u;
-      for (uint32_t j = side > C::kSlots ? side - C::kSlots : 0; j < side; ++j)
+      const uint32_t end = side, begin = v ? 1u : 0u;
+      for (uint32_t j = end > C::kSlots + begin ? end - (C::kSlots & ~1u) : begin; j < end; j += 2)
         mbar_wait_bounded(bar(kRawFull + j % C::kSlots), j / C::kSlots & 1, &keep_waiting, a.err, kWaitNs);
     }
     // no MMA may be in flight when the tensor memory is freed, also after an abort
@@ -499,6 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(kKEmpty + st, ph + 1);
       convert_side(st * 2 * C::kSide);
       if (cw < 4) {
+        // the values' scales come with the next slot
+        wait(kRawFull + (slot + 1 == C::kSlots ? 0 : slot + 1), (side + 1) / C::kSlots);
         const float* in = reinterpret_cast<const float*>(smem + C::kScaleRingOffset) + (n & 3) * 2 * kTilePos + token_s;
         const float sk = in[0], sv = in[kTilePos];
         float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage);
