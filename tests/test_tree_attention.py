@@ -135,6 +135,19 @@ def test_long_axis_and_many_requests(bits, dtype, nodes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("nodes", [1, 6])
+@pytest.mark.parametrize("bits,dtype,scale,page", [(8, "fp16", None, 16), (4, "bf16", 0.6, 64), (8, "bf16", 0.6, 128)])
+def test_many_tiles_per_share(nodes, bits, dtype, scale, page):
+    """Far more positions than the GPU has SMs: each works through many tiles and
+    several requests in a row, with maxima that rise on the way."""
+    cider = require_gpu()
+    rng = np.random.default_rng(31 + bits)
+    lengths = [int(x) for x in rng.integers(400, 1900, 40)]
+    run(cider, rng, lengths, [nodes - (i % 2 if nodes > 1 else 0) for i in range(40)], 32, 8, 128, page, bits, dtype,
+        scale=scale)
+
+
+@pytest.mark.gpu
 def test_sharp_and_flat_scores():
     """Scores far apart (one position takes all) and all equal (scale 0)."""
     cider = require_gpu()

@@ -18,7 +18,7 @@
 // of an SM's share of HBM against 1024 of tensor work), the issue of the
 // conversion and softmax instructions in practice.
 //
-// Roles (640 threads, one CTA per SM, persistent over its share of the axis):
+// Roles (896 threads, one CTA per SM, persistent over its share of the axis):
 //   warps 0, 1    one thread each issues the MMAs of S and of O
 //   warps 2, 3    load the codes as they are cached, keys and values, by bulk
 //                 copies of a page's part of a tile (each takes a lane ~80
@@ -28,13 +28,13 @@
 //                 position's sk, log2 sv, 1 / sv.  (Loading the codes themselves,
 //                 to registers or by asynchronous copies, was what held a tile
 //                 up: 5000 and 3300 cycles.)
-//   warps 12-19   softmax: warps 12-15 the tile's first 64 positions, 16-19 the
-//                 last 64, each warp its quarter of the rows.  S is read in the
-//                 layout that gives a thread 4 rows x 2 neighbouring positions,
-//                 so that a position's scales are loaded once for 4 rows.  m_i
-//                 is only raised when a p' passes 2^14: the two warps of a
-//                 quarter agree on that with one reducing barrier per tile.
-// Q is staged by warps 12-15, one row per thread.
+//   warps 12-27   softmax: four warps per quarter of the rows, 32 positions of
+//                 the tile each.  S is read in the layout that gives a thread 4
+//                 rows x 2 neighbouring positions, so that a position's scales
+//                 are loaded once for 4 rows.  m_i is only raised when a p'
+//                 passes 2^14: the four warps of a quarter agree on that with
+//                 one reducing barrier per tile.  They also put Q's tile into
+//                 tensor memory and take O's out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -53,11 +53,12 @@ namespace {
 
 constexpr int kTileRows = 128;    // query rows of a unit
 constexpr int kTilePos = 128;     // positions of a tile
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kConvWarp0 = 4, kConvWarps = 8;
-constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
-constexpr int kRegsMisc = 64, kRegsConv = 64, kRegsSoft = 144, kRegsLaunch = 96;
-constexpr int kRegsNeeded = 128 * kRegsMisc + 256 * kRegsConv + 256 * kRegsSoft;
+constexpr int kSoftWarp0 = 12, kSoftWarps = 16;
+constexpr int kParts = 4;         // of a tile's positions (and of O's columns): one softmax warp each per quarter
+constexpr int kRegsMisc = 64, kRegsConv = 56, kRegsSoft = 80, kRegsLaunch = 72;
+constexpr int kRegsNeeded = 128 * kRegsMisc + 256 * kRegsConv + 512 * kRegsSoft;
 static_assert(kRegsNeeded <= kThreads * kRegsLaunch, "register split exceeds the launch's registers");
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColAll = 512;
@@ -76,7 +77,7 @@ struct TreeCfg {
   static constexpr int kScaleOffset = 4 * kSide;             // two stages of K, V
   static constexpr int kScaleStage = 64 * 16 + 64 * 8;       // per pair of positions: sk sk lg lg, inv inv
   static constexpr int kStatOffset = kScaleOffset + 4 * kScaleStage;
-  static constexpr int kStatBytes = 2 * kTileRows * 8;       // per half and row: two floats
+  static constexpr int kStatBytes = kParts * kTileRows * 8;  // per part and row: two floats
   static constexpr int kMaskOffset = kStatOffset + kStatBytes;
   // Codes as they are cached, on their way to the converters: a K or a V tile
   // per slot, and the scales of a tile's positions.
@@ -87,7 +88,7 @@ struct TreeCfg {
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;         // at most: the scales' four tiles
   static constexpr int kScaleRingOffset = kRingOffset + kSlots * kRingSlot;
   static constexpr int kBarOffset = kScaleRingOffset + kScaleRing;
-  static constexpr int kSmem = kBarOffset + 40 * 8 + 64 + 1024;
+  static constexpr int kSmem = kBarOffset + 40 * 8 + 128 + 1024;
   // Order of the dims in the fp16 tiles: unit `lin` of a row (8 values) holds
   // codes (lin / kChunks) * 8 .. + 8 of chunk lin % kChunks, so that the lanes
   // that convert a row's chunks store to different banks.
@@ -99,7 +100,7 @@ struct TreeCfg {
 // Barriers, by number.
 enum Bar : int {
   kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kQFull = 12,
-  kOFull = 13, kOEmpty = 14, kDone = 15, kRawFull = 17, kRawEmpty = 25, kBars = 33
+  kOFull = 13, kOEmpty = 14, kDone = 15, kRawFull = 17, kRawEmpty = 25, kScFull = 33, kBars = 37
 };
 
 template <int R>
@@ -151,14 +152,48 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-// 16 lanes x 32 columns: register 2 i + h of thread T is lane T / 4 + 8 h, column 4 i + T % 4.
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 lanes x 16 columns: register 2 i + h of thread T is lane T / 4 + 8 h, column 4 i + T % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
+}
+// One lane per thread, N consecutive columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
+    tmem_ld32(taddr, r);
+  } else {
+    static_assert(N == 16);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_row(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
+    tmem_st32(taddr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  } else {
+    static_assert(N == 8);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+  }
 }
 // Whether any thread of the `count` threads of barrier `id` has `v`.
 __device__ __forceinline__ bool barrier_or(int id, int count, bool v) {
@@ -252,8 +287,8 @@ template <typename C, int D, int ST>
 __device__ __forceinline__ void issue_o(uint32_t sbase, bool add) {
   const uint64_t desc = smem_desc_mn_sw128(sbase + ST * 2 * C::kSide + C::kSide, C::kSub);
 #pragma unroll
-  for (int s = 0; s < kTilePos / 16; ++s)
-    tc_mma_ts(kColO, kColS + ST * 128 + (s >> 2) * 64 + (s & 3) * 8, desc + (s * 2048 >> 4),
+  for (int s = 0; s < kTilePos / 16; ++s)   // P of each part lies at the beginning of its columns of S
+    tc_mma_ts(kColO, kColS + ST * 128 + (s >> 1) * 32 + (s & 1) * 8, desc + (s * 2048 >> 4),
               idesc_f16_f32(128, D) | kBMajorMn, s > 0 ? 1u : add ? 1u : 0u);
 }
 
@@ -268,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int group = a.q_heads / a.cache.heads;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kBarOffset + kBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOffset + kBars * 8 + 4);
-  float* unlift_smem = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 8);
-  float* lift_max = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 16);   // 4 warps
+  float* lift_max = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 16);   // 16 warps
   auto bar = [&](int i) { return sbase + C::kBarOffset + i * 8; };
   auto wait = [&](int i, uint32_t parity) {
     return mbar_wait_bounded(bar(i), parity & 1, abort_flag, a.err, kWaitNs);
@@ -286,11 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(kSFull + s), 1);
         mbar_init(bar(kPReady + s), kSoftWarps);
       }
-      mbar_init(bar(kQFull), 4);
+      mbar_init(bar(kQFull), kSoftWarps);
       mbar_init(bar(kOFull), 1);
       mbar_init(bar(kOEmpty), kSoftWarps);
       mbar_init(bar(kDone), 1);
       mbar_init(bar(kDone + 1), 1);
+      for (int s = 0; s < 4; ++s) mbar_init(bar(kScFull + s), 4);
       for (int s = 0; s < C::kSlots; ++s) {
         mbar_init(bar(kRawFull + s), 1);
         mbar_init(bar(kRawEmpty + s), kConvWarps);
@@ -308,8 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t tmem = 0;
 
   // Every role walks the same pieces.  A wait that gives up raises the abort
-  // flag; the roles then run to their ends without waiting (all their memory
-  // accesses stay in bounds), so that no barrier is left with a thread missing.
+  // flag.  Then no more MMAs or copies are issued, and the other roles run to
+  // their ends without waiting (all their memory accesses stay in bounds), so
+  // that no named barrier is left with a thread missing.
   if (warp < kConvWarp0) {
     regs_dec<kRegsMisc>();
     // Two issuers: an MMA takes a thread ~75 cycles and more to issue, sixteen a
@@ -411,11 +447,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t row = a.cache.row(max(id, 0), head, 0);
           const uint32_t scales = sbase + C::kScaleRingOffset + (n & 3) * 2 * kTilePos * 4 +
                                   (v ? kTilePos * 4 : 0) + lane * scale_bytes;
-          wait(kRawEmpty + slot, side / C::kSlots + 1);
+          // after a wait that gave up nothing more is loaded: a barrier that
+          // expects bytes must not be arrived at twice in a phase
+          if (!__all_sync(0xffffffffu, wait(kRawEmpty + slot, side / C::kSlots + 1))) {
+            more = false;
+            break;
+          }
           // a position without a page counts as one with scales of 0
           if (id < 0 && lane < runs) {
             const uint32_t zero[4] = {0, 0, 0, 0};
             for (uint32_t j = 0; j < scale_bytes; j += 16) st_shared_v4(scales + j, zero);
+            fence_proxy_async_smem();   // later tiles' copies write here too
           }
           __syncwarp();
           const uint32_t full = bar(kRawFull + slot);
@@ -515,6 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         f[pair * 4 + e] = sk * mul;
         f[pair * 4 + 2 + e] = lg;
         f[256 + pair * 2 + e] = kept > 0.0f && kept < INFINITY ? inv : 0.0f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kScFull + (n & 3)));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -530,89 +574,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_inc<kRegsSoft>();
     // --------------------------------------------------------------- softmax
-    const int sw = warp - kSoftWarp0, quarter = sw & 3, half = sw >> 2;
+    const int sw = warp - kSoftWarp0, quarter = sw & 3, part = sw >> 2;
     const int g = lane >> 2, t = lane & 3;
+    constexpr int kCols = D / kParts;   // of O (and dims of Q) per thread
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOffset);
+    float2* my_stat = stat + part * kTileRows + quarter * 32;
     uint64_t* masks = reinterpret_cast<uint64_t*>(smem + C::kMaskOffset);
-    const int pair_bar = 1 + quarter;   // the two warps of a quarter
+    const int quarter_bar = 1 + quarter;   // the four warps of a quarter
 
     Axis axis;
     axis.begin(a, kTilePos, lane, kTileRows);
     bool more = axis.more();
     uint32_t n = 0, piece = 0;
-    while (more) {
-      const Request req = axis.req;
-      const int blocks = Axis::blocks_of(a, req, kTileRows);
+    // This thread's row of the axis' piece, and its dims of that row of q.
+    int rows = 0, row = quarter * 32 + lane;
+    int64_t out_at = 0;
+    uint4 raw[kCols / 8];
+    uint64_t mask = 0;
+    auto load_q = [&]() {
+      const int blocks = Axis::blocks_of(a, axis.req, kTileRows);
       const int head = axis.unit / blocks, block = axis.unit - head * blocks;
-      const int rows = min(kTileRows, req.nodes * group - block * kTileRows);
-      const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
-      // ------------------------------------------------- one row per thread
-      const int row = quarter * 32 + lane;
+      rows = min(kTileRows, axis.req.nodes * group - block * kTileRows);
+      const bool have = row < rows;
       const int at = block * kTileRows + row;
-      const int node = row < rows ? at / group : 0;
-      const int64_t head_at = static_cast<int64_t>(head) * group + (row < rows ? at - node * group : 0);
-      if (half == 0) {
-        uint64_t m = 0;
-        if (row < rows)
-          m = a.tree ? static_cast<uint64_t>(a.tree[req.first + node]) : ~0ull >> (63 - node);
-        masks[row] = m;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (req.first + node) * a.q_stride + head_at * D;
-        float lift = 1.0f;
-        if (bf16) {
-          // one power of two for all rows puts the largest value in [2^13, 2^14)
-          float top = 0.0f;
-          for (int i = 0; i < D; i += 8) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row < rows) w = *reinterpret_cast<const uint4*>(q + i);
+      const int node = have ? at / group : 0;
+      const int hq = head * group + (have ? at - node * group : 0);
+      out_at = ((axis.req.first + node) * a.q_heads + hq) * D;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (axis.req.first + node) * a.q_stride +
+                          static_cast<int64_t>(hq) * D;
+#pragma unroll
+      for (int i = 0; i < kCols / 8; ++i)
+        raw[i] = have ? *reinterpret_cast<const uint4*>(q + C::dim_of(part * (kCols / 8) + i))
+                      : make_uint4(0, 0, 0, 0);
+      mask = 0;
+      if (have && part == 0)
+        mask = a.tree ? static_cast<uint64_t>(a.tree[axis.req.first + node]) : ~0ull >> (63 - node);
+    };
+    if (more) load_q();
+    while (more) {
+      // ------------------------------------------------------------- Q's tile
+      const int nodes = axis.req.nodes, context = static_cast<int>(axis.req.context);
+      const int tiles = static_cast<int>(axis.piece_end - axis.piece_begin);
+      if (part == 0) masks[row] = mask;
+      float lift = 1.0f, unlift = 1.0f;
+      if (bf16) {
+        // one power of two for all rows puts the largest value in [2^13, 2^14)
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          float f[8];
+          widen8<__nv_bfloat16>(raw[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) lift_max[sw] = top;
+        named_barrier_sync(5, 32 * kSoftWarps);
+        top = lift_max[lane & 15];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int k = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+        k = top == 0.0f ? 0 : max(-126, min(k, 126));
+        lift = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        unlift = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      }
+      {
+        uint32_t u[kCols / 2];
+#pragma unroll
+        for (int j = 0; j < kCols / 8; ++j) {
+          uint4 w = raw[j];
+          if (bf16) {
             float f[8];
             widen8<__nv_bfloat16>(w, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+            w = make_uint4(pack_h2(f[0] * lift, f[1] * lift), pack_h2(f[2] * lift, f[3] * lift),
+                           pack_h2(f[4] * lift, f[5] * lift), pack_h2(f[6] * lift, f[7] * lift));
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) lift_max[quarter] = top;
-          named_barrier_sync(5, 128);
-          top = fmaxf(fmaxf(lift_max[0], lift_max[1]), fmaxf(lift_max[2], lift_max[3]));
-          int k = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-          k = top == 0.0f ? 0 : max(-126, min(k, 126));
-          lift = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-          if (threadIdx.x == kSoftWarp0 * 32)
-            *unlift_smem = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-        } else if (threadIdx.x == kSoftWarp0 * 32) {
-          *unlift_smem = 1.0f;
+          if constexpr (BITS == 4)   // the order of the converted codes
+            w = make_uint4(__byte_perm(w.x, w.z, 0x5410u), __byte_perm(w.x, w.z, 0x7632u),
+                           __byte_perm(w.y, w.w, 0x5410u), __byte_perm(w.y, w.w, 0x7632u));
+          u[4 * j] = w.x;
+          u[4 * j + 1] = w.y;
+          u[4 * j + 2] = w.z;
+          u[4 * j + 3] = w.w;
         }
-#pragma unroll
-        for (int s = 0; s < D / 64; ++s) {
-          uint32_t u[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row < rows) w = *reinterpret_cast<const uint4*>(q + C::dim_of(s * 8 + j));
-            if (bf16) {
-              float f[8];
-              widen8<__nv_bfloat16>(w, f);
-              w = make_uint4(pack_h2(f[0] * lift, f[1] * lift), pack_h2(f[2] * lift, f[3] * lift),
-                             pack_h2(f[4] * lift, f[5] * lift), pack_h2(f[6] * lift, f[7] * lift));
-            }
-            if constexpr (BITS == 4)   // the order of the converted codes
-              w = make_uint4(__byte_perm(w.x, w.z, 0x5410u), __byte_perm(w.x, w.z, 0x7632u),
-                             __byte_perm(w.y, w.w, 0x5410u), __byte_perm(w.y, w.w, 0x7632u));
-            u[4 * j] = w.x;
-            u[4 * j + 1] = w.y;
-            u[4 * j + 2] = w.z;
-            u[4 * j + 3] = w.w;
-          }
-          tmem_st32(lanes + kColQ + s * 32, u);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQFull));
+        tmem_st_row(lanes + kColQ + part * (kCols / 2), u);
       }
-      wait(kQFull, piece);   // also: the masks and the scaling are there
-      const float unlift = *unlift_smem;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQFull));
+      wait(kQFull, piece);   // also: the masks are there
       const F2 unlift2 = f2(unlift, unlift);
 
       // ------------------------------------------------------ the piece's tiles
@@ -623,31 +676,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mu[r] = kNone;
         l[r] = 0.0f;
       }
-      int pos = static_cast<int>(axis.piece_begin) * kTilePos + half * 64;
-      const int context = static_cast<int>(req.context);
+      int pos = static_cast<int>(axis.piece_begin) * kTilePos + part * 32;
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i, pos += kTilePos, ++n) {
         const uint32_t st = n & 1, ph = n >> 1;
-        wait(kKFull + st, ph);   // the scales
+        // not K's own barrier, which may be two tiles on by now: a waiter must
+        // never be more than one phase behind.  The scales have four stages, and
+        // none is written again before this warp's P of the tile that it holds
+        wait(kScFull + (n & 3), n >> 2);
         wait(kSFull + st, ph);
         tc_fence_after();
         if (active) {
-          const uint32_t s_at = lanes + kColS + st * 128 + half * 64;
-          const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage) +
-                             half * 32 + t;
-          const float2* iv = reinterpret_cast<const float2*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage + 1024) +
-                             half * 32 + t;
-          const bool masked = context - pos < 64;
-          auto fetch = [&](int ch, float (&x)[2][16]) {
-            tmem_ld_16x256b_x4(s_at + ch * 32, x[0]);
-            tmem_ld_16x256b_x4(s_at + ch * 32 + (16u << 16), x[1]);
-          };
-          // x of 32 positions (chunk ch), for the rows g + 8 h + 16 hh: [hh][4 j + 2 h + e]
-          auto scale_x = [&](int ch, float (&x)[2][16]) {
+          const uint32_t s_at = lanes + kColS + st * 128 + part * 32;
+          const uint8_t* sc = smem + C::kScaleOffset + (n & 3) * C::kScaleStage;
+          uint32_t p[2][8];   // [hh][2 j + h]: 8-position groups j, rows g + 8 h + 16 hh
+          float add[4];
+          bool raised = false;
+          for (;;) {
+            // x of the 32 positions: [hh][4 j + 2 h + e]
+            float x[2][16];
+            tmem_ld_16x256b_x4(s_at, x[0]);
+            tmem_ld_16x256b_x4(s_at + (16u << 16), x[1]);
+            tmem_wait_ld();
             loaded(x[0]);
             loaded(x[1]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float4 v = sc[ch * 16 + 4 * j];
+              const float4 v = reinterpret_cast<const float4*>(sc)[part * 16 + 4 * j + t];
               const F2 sk2 = mul2(f2(v.x, v.y), unlift2), lg2 = f2(v.z, v.w);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -656,55 +711,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 un2(fma2(f2(x0, x1), sk2, lg2), x0, x1);
               }
             }
-            if (masked) {
-#pragma unroll
+            if (context - pos < 32) {
+#pragma unroll 1
               for (int r = 0; r < 4; ++r) {
                 const uint64_t m = masks[quarter * 32 + 8 * r + g];
+                uint32_t seen = 0;   // bit 2 j + e
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    const int ahead = pos - context + ch * 32 + 8 * j + 2 * t + e;
-                    const bool seen = ahead < 0 || (ahead < req.nodes && (m >> ahead & 1));
-                    if (!seen) x[r >> 1][4 * j + 2 * (r & 1) + e] = -INFINITY;
+                    const int ahead = pos - context + 8 * j + 2 * t + e;
+                    if (ahead < 0 || (ahead < nodes && (m >> ahead & 1))) seen |= 1u << (2 * j + e);
                   }
+#pragma unroll
+                for (int rr = 0; rr < 4; ++rr)
+                  if (rr == r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e)
+                        if (!(seen >> (2 * j + e) & 1)) x[rr >> 1][4 * j + 2 * (rr & 1) + e] = -INFINITY;
               }
             }
-          };
-          uint32_t p[2][16];   // [hh][2 j + h], j: 8-position groups of the 64
-          float add[4];
-          auto weights = [&]() -> bool {
             __half2 high[4];
             F2 sum[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              high[r] = __half2half2(__ushort_as_half(0));
+              high[r] = as_h2(0u);
               sum[r] = f2(0.0f, 0.0f);
             }
-            float xs[2][2][16];
-            fetch(0, xs[0]);
-            fetch(1, xs[1]);
-            tmem_wait_ld();
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              float (&x)[2][16] = xs[ch];
-              scale_x(ch, x);
+            for (int j = 0; j < 4; ++j) {
+              const float2 v = reinterpret_cast<const float2*>(sc + 1024)[part * 16 + 4 * j + t];
+              const F2 inv2 = f2(v.x, v.y);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 v = iv[ch * 16 + 4 * j];
-                const F2 inv2 = f2(v.x, v.y);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const F2 d = add2(f2(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]),
-                                    f2(-mu[r], -mu[r]));
-                  float d0, d1;
-                  un2(d, d0, d1);
-                  const float p0 = exp2_approx(d0), p1 = exp2_approx(d1);
-                  sum[r] = fma2(f2(p0, p1), inv2, sum[r]);
-                  const uint32_t u = pack_h2(p0, p1);
-                  high[r] = __hmax2(high[r], as_h2(u));
-                  p[r >> 1][2 * (ch * 4 + j) + (r & 1)] = u;
-                }
+              for (int r = 0; r < 4; ++r) {
+                float d0, d1;
+                un2(add2(f2(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]),
+                         f2(-mu[r], -mu[r])), d0, d1);
+                const float p0 = exp2_approx(d0), p1 = exp2_approx(d1);
+                sum[r] = fma2(f2(p0, p1), inv2, sum[r]);
+                const uint32_t u = pack_h2(p0, p1);
+                high[r] = __hmax2(high[r], as_h2(u));
+                p[r >> 1][2 * j + (r & 1)] = u;
               }
             }
             bool over = false;
@@ -715,71 +764,56 @@ __global__ void __launch_bounds__(kThreads, 1)
               add[r] = s0 + s1;
               over |= __half2float(__hmax(__low2half(high[r]), __high2half(high[r]))) > 16384.0f;
             }
-            return over;
-          };
-          if (barrier_or(pair_bar, 64, weights())) {
-            // some row's m is raised: its maximum over the tile, from both halves
+            if (raised || !barrier_or(quarter_bar, 32 * kParts, over)) break;
+            // some row's m is raised: its maximum over the tile, from all parts
+            raised = true;
             float top[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) top[r] = -INFINITY;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              float x[2][16];
-              fetch(ch, x);
-              tmem_wait_ld();
-              scale_x(ch, x);
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  top[r] = fmaxf(top[r], fmaxf(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]));
-            }
-#pragma unroll
             for (int r = 0; r < 4; ++r) {
+              top[r] = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top[r] = fmaxf(top[r], fmaxf(x[r >> 1][4 * j + 2 * (r & 1)], x[r >> 1][4 * j + 2 * (r & 1) + 1]));
               top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
               top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-              if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g].x = top[r];
+              if (t == 0) my_stat[8 * r + g].x = top[r];
             }
-            named_barrier_sync(pair_bar, 64);
+            named_barrier_sync(quarter_bar, 32 * kParts);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              top[r] = fmaxf(top[r], stat[(half ^ 1) * kTileRows + quarter * 32 + 8 * r + g].x);
+#pragma unroll
+              for (int w = 0; w < kParts; ++w)
+                top[r] = fmaxf(top[r], stat[w * kTileRows + quarter * 32 + 8 * r + g].x);
+              float f = 1.0f;
               if (top[r] > mu[r] + 14.0f) {
-                const float now = top[r] - 6.0f;
-                const float f = exp2_approx(mu[r] - now);
+                const float now = top[r] - 6.0f;   // p' is 2^6 for the largest
+                f = exp2_approx(mu[r] - now);
                 l[r] *= f;
                 mu[r] = now;
-                if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g].y = f;
-              } else if (t == 0) {
-                stat[half * kTileRows + quarter * 32 + 8 * r + g].y = 1.0f;
               }
+              if (t == 0) my_stat[8 * r + g].y = f;
             }
-            if (i > 0) {   // this warp's half of O's columns; the products so far are done
+            if (i > 0) {   // this warp's columns of O; the products so far are done
               wait(kVEmpty + ((n - 1) & 1), (n - 1) >> 1);
               tc_fence_after();
               __syncwarp();
-              const float f = stat[half * kTileRows + quarter * 32 + lane].y;
+              const float f = my_stat[lane].y;
+              uint32_t o[kCols];
+              tmem_ld_row(lanes + kColO + part * kCols, o);
+              tmem_wait_ld();
+              loaded(o);
 #pragma unroll
-              for (int ch = 0; ch < D / 64; ++ch) {
-                uint32_t o[32];
-                const uint32_t o_at = lanes + kColO + half * (D / 2) + ch * 32;
-                tmem_ld32(o_at, o);
-                tmem_wait_ld();
-                loaded(o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(o_at, o);
-              }
+              for (int j = 0; j < kCols; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_row(lanes + kColO + part * kCols, o);
             }
-            weights();
-            // the partner has read this warp's maxima before they are written again
-            named_barrier_sync(pair_bar, 64);
+            // the others have read this warp's maxima before they are written again
+            named_barrier_sync(quarter_bar, 32 * kParts);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) l[r] += add[r];
-          // P over this half's own columns of S
-          tmem_st_16x128b_x8(s_at, p[0]);
-          tmem_st_16x128b_x8(s_at + (16u << 16), p[1]);
+          // P over this part's own columns of S
+          tmem_st_16x128b_x4(s_at, p[0]);
+          tmem_st_16x128b_x4(s_at + (16u << 16), p[1]);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -789,48 +823,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ------------------------------------------------------------ the output
       const bool whole = axis.whole();
-      const int slot = axis.slot();
+      const int slot = axis.slot(), my_rows = rows;
+      const int64_t my_out = out_at;
       more = axis.next(a, kTilePos, kTileRows);
+      if (more) load_q();   // on its way during the output
       if (active) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
           l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-          if (t == 0) stat[half * kTileRows + quarter * 32 + 8 * r + g] = make_float2(mu[r], l[r]);
+          if (t == 0) my_stat[8 * r + g] = make_float2(mu[r], l[r]);
         }
-        named_barrier_sync(pair_bar, 64);
+        named_barrier_sync(quarter_bar, 32 * kParts);
       }
       wait(kOFull, piece);
       tc_fence_after();
       if (active) {
-        const float2 s0 = stat[row], s1 = stat[kTileRows + row];
-        const float sum = s0.y + s1.y;
-        const float top = s0.x == kNone ? -INFINITY : s0.x;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) sum += stat[w * kTileRows + row].y;
+        const float m = stat[row].x;
+        const float top = m == kNone ? -INFINITY : m;
         const float codes = BITS == 4 ? 512.0f : 1.0f;
         const float f = whole ? (sum > 0.0f ? codes / sum : 0.0f) : codes;
+        uint32_t o[kCols];
+        tmem_ld_row(lanes + kColO + part * kCols, o);
+        tmem_wait_ld();
+        loaded(o);
+        if (row < my_rows) {
 #pragma unroll
-        for (int ch = 0; ch < D / 64; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kColO + half * (D / 2) + ch * 32, o);
-          tmem_wait_ld();
-          loaded(o);
-          if (row < rows) {
+          for (int j = 0; j < kCols / 8; ++j) {
+            const int d = C::dim_of(part * (kCols / 8) + j);
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = C::dim_of((half * (D / 2) + ch * 32) / 8 + j);
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)   // INT4 units hold the dims 0 4 1 5 2 6 3 7
-                v[BITS == 4 ? (e & 1) * 4 + (e >> 1) : e] = __uint_as_float(o[8 * j + e]) * f;
-              const float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
-              if (whole) {
-                const int64_t dst = ((req.first + node) * a.q_heads + head_at) * D + d;
-                store_out4(a.out, bf16, dst, lo, 1.0f);
-                store_out4(a.out, bf16, dst + 4, hi, 1.0f);
-              } else {
-                parts.store(slot, row, D, d, lo, top, sum);
-                parts.store(slot, row, D, d + 4, hi, top, sum);
-              }
+            for (int e = 0; e < 8; ++e)   // INT4 units hold the dims 0 4 1 5 2 6 3 7
+              v[BITS == 4 ? (e & 1) * 4 + (e >> 1) : e] = __uint_as_float(o[8 * j + e]) * f;
+            const float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+            if (whole) {
+              store_out4(a.out, bf16, my_out + d, lo, 1.0f);
+              store_out4(a.out, bf16, my_out + d + 4, hi, 1.0f);
+            } else {
+              parts.store(slot, row, D, d, lo, top, sum);
+              parts.store(slot, row, D, d + 4, hi, top, sum);
             }
           }
         }
@@ -838,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kOEmpty));
-      // every warp is past this piece's statistics, masks and scaling before they are written again
-      named_barrier_sync(6, 256);
+      // every warp is past this piece's statistics and masks before they are written again
+      named_barrier_sync(6, 32 * kSoftWarps);
       ++piece;
     }
   }
