@@ -11,7 +11,6 @@ raise.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import struct
 import threading
@@ -420,70 +419,98 @@ def cider_kv_cache(layers: int, pages: int, heads: int, head_dim: int, page_size
     return tuple(out)
 
 
-def _cache_args(cache):
-    """-> (cider_kv_cache_t as bytes, its device, heads, head_dim, layers)."""
+# The checks below run on every call of a decoding step, whose kernels take a few
+# microseconds: each tensor is passed by one chained condition, and only a
+# tensor that fails it goes through the function that says what is wrong.
+_I32, _I64, _F32, _I8, _U8 = torch.int32, torch.int64, torch.float32, torch.int8, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index
+
+
+def _refuse_cache(cache):
     k, ks, v, vs = cache
-    layers, pages, heads, page, width = k.shape
-    bits = 8 if k.dtype == torch.int8 else 4
-    if k.dtype not in (torch.int8, torch.uint8) or v.dtype != k.dtype:
-        raise TypeError("cache codes must be int8 or (packed INT4) uint8")
-    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
-        raise TypeError("cache scales must be float32")
-    if v.shape != k.shape or ks.shape != k.shape[:-1] or vs.shape != k.shape[:-1]:
-        raise ValueError("cache tensors do not match")
-    dim = width if bits == 8 else 2 * width
     for t in (k, ks, v, vs):
-        if not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError("cache must be CUDA tensors")
-        if not t.is_contiguous():
-            raise ValueError("cache must be contiguous")
+    if k.dtype not in (_I8, _U8) or v.dtype != k.dtype:
+        raise TypeError("cache codes must be int8 or (packed INT4) uint8")
+    if ks.dtype != _F32 or vs.dtype != _F32:
+        raise TypeError("cache scales must be float32")
+    if k.dim() != 5 or v.shape != k.shape or ks.shape != k.shape[:-1] or vs.shape != k.shape[:-1]:
+        raise ValueError("cache tensors do not match")
+    if not all(t.is_contiguous() for t in (k, ks, v, vs)):
+        raise ValueError("cache must be contiguous")
+    raise ValueError("cache tensors are on different devices")
+
+
+def _cache_args(cache):
+    """-> (cider_kv_cache_t as bytes, device index, heads, head_dim, layers)."""
+    k, ks, v, vs = cache
+    shape, kind, dev = k.shape, k.dtype, k.get_device()
+    if not (len(shape) == 5 and (kind is _I8 or kind is _U8) and v.dtype is kind and ks.dtype is _F32
+            and vs.dtype is _F32 and v.shape == shape and dev >= 0 and ks.get_device() == dev
+            and v.get_device() == dev and vs.get_device() == dev and k.is_contiguous()
+            and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and ks.shape == shape[:4] and vs.shape == shape[:4]):
+        _refuse_cache(cache)
+    layers, pages, heads, page, width = shape
+    bits, dim = (8, width) if kind is _I8 else (4, 2 * width)
     return (_CACHE.pack(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), layers, pages,
-                        heads, page, dim, bits), k.device, heads, dim, layers)
+                        heads, page, dim, bits), dev, heads, dim, layers)
 
 
-def _rows(t, name, heads, dim):
+def _rows(t, name, heads, dim, dev):
     """dtype and token stride of a [tokens, heads, dim] tensor with dense heads."""
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the cache {heads} heads of {dim}")
-    n, h, d = t.shape
-    stride = t.stride()
-    if stride[2] != 1 or (h > 1 and stride[1] != d):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, the cache {heads} heads of {dim}")
+    n, h, d = shape
+    token, row, one = t.stride()
+    if one != 1 or (h > 1 and row != d):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
-    return _DTYPES[t.dtype], stride[0] if n > 1 else h * d
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    return _DTYPES[t.dtype], token if n > 1 else h * d
 
 
-def _flat(t, dtype, name, *shape):
-    """A contiguous CUDA tensor of this type and shape (None: any size) -> its pointer."""
+def _flat(t, dtype, name, shape, dev):
+    """A contiguous tensor of this type and shape on this device -> its pointer."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on another device")
 
 
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _width(t, name):
+    """The columns of a matrix."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    return shape[1]
 
 
 def cider_kv_append(k, v, slots, cache, layer: int = 0) -> None:
     """Quantize k, v [tokens, heads, D] (fp16 or bf16, any token stride) into
     slots int64 [tokens] (page * page_size + row, negative: skip) of a layer."""
     c, dev, heads, dim, _ = _cache_args(cache)
-    dt, ks = _rows(k, "k", heads, dim)
-    dv, vs = _rows(v, "v", heads, dim)
+    dt, ks = _rows(k, "k", heads, dim, dev)
+    dv, vs = _rows(v, "v", heads, dim, dev)
     n = k.shape[0]
     if dv != dt or v.shape[0] != n:
         raise ValueError("k and v must have the same type and tokens")
-    sp = _flat(slots, torch.int64, "slots", n)
-    _check("cider_kv_append",
-           _load().cider_kv_append(c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n,
-                                   _raw_stream(dev)))
+    sp = _flat(slots, _I64, "slots", (n,), dev)
+    st = (_lib or _load()).cider_kv_append(c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n,
+                                           _raw_stream(dev))
+    if st:
+        _check("cider_kv_append", st)
 
 
 def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float16, layer=None,
@@ -492,22 +519,26 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
     layer None): request b's positions starts[b], starts[b] + 1, ... for its
     output rows offsets[b] .. offsets[b + 1]."""
     c, dev, heads, dim, layers = _cache_args(cache)
-    n = starts.shape[0]
-    tp = _flat(table, torch.int32, "table", n, None)
-    sp = _flat(starts, torch.int32, "starts", n)
-    op = _flat(offsets, torch.int32, "offsets", n + 1)
+    n, width = starts.shape[0], _width(table, "table")
+    tp = _flat(table, _I32, "table", (n, width), dev)
+    sp = _flat(starts, _I32, "starts", (n,), dev)
+    op = _flat(offsets, _I32, "offsets", (n + 1,), dev)
     shape = (tokens, heads, dim) if layer is not None else (layers, tokens, heads, dim)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be float16 or bfloat16")
     if out is None:
         # zeros where no request reads: nothing is launched for an empty problem
         make = torch.empty if n and cache[0].shape[1] else torch.zeros
-        out = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
-    kp = _flat(out[0], dtype, "out[0]", *shape)
-    vp = _flat(out[1], dtype, "out[1]", *shape)
-    _check("cider_kv_read",
-           _load().cider_kv_read(c, -1 if layer is None else layer, tp, table.shape[1], sp, op, n,
-                                 tokens, kp, vp, _DTYPES[dtype], _raw_stream(dev)))
+        place = cache[0].device
+        k, v = out = make(shape, dtype=dtype, device=place), make(shape, dtype=dtype, device=place)
+        kp, vp = k.data_ptr(), v.data_ptr()
+    else:
+        kp = _flat(out[0], dtype, "out[0]", shape, dev)
+        vp = _flat(out[1], dtype, "out[1]", shape, dev)
+    st = (_lib or _load()).cider_kv_read(c, -1 if layer is None else layer, tp, width, sp, op, n, tokens,
+                                         kp, vp, _DTYPES[dtype], _raw_stream(dev))
+    if st:
+        _check("cider_kv_read", st)
     return out
 
 
@@ -515,14 +546,14 @@ def cider_kv_compact(cache, table, starts, path, kept) -> None:
     """In every layer, move request b's row at position starts[b] + path[b, i]
     to starts[b] + i for i < kept[b]."""
     c, dev, _, _, _ = _cache_args(cache)
-    n = starts.shape[0]
-    tp = _flat(table, torch.int32, "table", n, None)
-    sp = _flat(starts, torch.int32, "starts", n)
-    pp = _flat(path, torch.int32, "path", n, None)
-    kp = _flat(kept, torch.int32, "kept", n)
-    _check("cider_kv_compact",
-           _load().cider_kv_compact(c, tp, table.shape[1], sp, pp, path.shape[1], kp, n,
-                                    _raw_stream(dev)))
+    n, width, most = starts.shape[0], _width(table, "table"), _width(path, "path")
+    tp = _flat(table, _I32, "table", (n, width), dev)
+    sp = _flat(starts, _I32, "starts", (n,), dev)
+    pp = _flat(path, _I32, "path", (n, most), dev)
+    kp = _flat(kept, _I32, "kept", (n,), dev)
+    st = (_lib or _load()).cider_kv_compact(c, tp, width, sp, pp, most, kp, n, _raw_stream(dev))
+    if st:
+        _check("cider_kv_compact", st)
 
 
 def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree=None, scale=None,
@@ -532,21 +563,24 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
     tree int64 [tokens]: which of its request's new tokens a token sees (None:
     itself and the earlier ones).  -> out [tokens, q_heads, D] of q's type."""
     c, dev, heads, dim, _ = _cache_args(cache)
-    dt, qs = _rows(q, "q", None, dim)
-    n, hq, _ = q.shape
-    b = lengths.shape[0]
-    tp = _flat(table, torch.int32, "table", b, None)
-    lp = _flat(lengths, torch.int32, "lengths", b)
-    op = _flat(offsets, torch.int32, "offsets", b + 1)
-    mp = _flat(tree, torch.int64, "tree", n) if tree is not None else None
+    dt, qs = _rows(q, "q", None, dim, dev)
+    shape = q.shape
+    n, b, width = shape[0], lengths.shape[0], _width(table, "table")
+    tp = _flat(table, _I32, "table", (b, width), dev)
+    lp = _flat(lengths, _I32, "lengths", (b,), dev)
+    op = _flat(offsets, _I32, "offsets", (b + 1,), dev)
+    mp = None if tree is None else _flat(tree, _I64, "tree", (n,), dev)
     if out is None:
-        out = torch.empty((n, hq, dim), dtype=q.dtype, device=dev)
-    yp = _flat(out, q.dtype, "out", n, hq, dim)
-    _check("cider_tree_attention",
-           _load().cider_tree_attention(c, layer, q.data_ptr(), qs, dt, n, hq, tp, table.shape[1],
-                                        lp, op, b, max_nodes, mp,
-                                        1.0 / math.sqrt(dim) if scale is None else scale, yp,
-                                        _raw_stream(dev)))
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        yp = out.data_ptr()
+    else:
+        yp = _flat(out, q.dtype, "out", shape, dev)
+    st = (_lib or _load()).cider_tree_attention(c, layer, q.data_ptr(), qs, dt, n, shape[1], tp, width, lp,
+                                                op, b, max_nodes, mp,
+                                                dim ** -0.5 if scale is None else scale, yp,
+                                                _raw_stream(dev))
+    if st:
+        _check("cider_tree_attention", st)
     return out
 
 
@@ -556,29 +590,32 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
     logits [nodes, vocab] (fp16 or bf16, any row stride), with the given random
     numbers.  -> (count int32 [requests], path int32 [requests, max_nodes],
     next int32 [requests])."""
-    if not logits.is_cuda:
+    dev = logits.get_device()
+    if dev < 0:
         raise TypeError("logits must be a CUDA tensor")
     if logits.dtype not in _DTYPES:
         raise TypeError("logits must be float16 or bfloat16")
-    if logits.dim() != 2 or logits.stride(1) != 1:
-        raise ValueError("logits must be [nodes, vocab] with contiguous rows")
-    n, vocab = logits.shape
+    vocab = _width(logits, "logits")
+    n = logits.shape[0]
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits must have contiguous rows")
     b = offsets.shape[0] - 1
-    dev = logits.device
-    tp = _flat(tokens, torch.int32, "tokens", n)
-    pp = _flat(parents, torch.int32, "parents", n)
-    op = _flat(offsets, torch.int32, "offsets", None)
-    up = _flat(uniforms, torch.float32, "uniforms", n)
-    np_ = _flat(noise, torch.float32, "noise", b, vocab)
-    dp = _flat(draft_probs, torch.float32, "draft_probs", n, vocab) if draft_probs is not None else None
-    wp = _flat(temperature, torch.float32, "temperature", b) if temperature is not None else None
-    # one allocation: path, count, next
-    out = torch.empty((b * (max_nodes + 2),), dtype=torch.int32, device=dev)
-    path, count, nxt = out.split((b * max_nodes, b, b))
-    at = out.data_ptr()
-    _check("cider_verify_drafts",
-           _load().cider_verify_drafts(logits.data_ptr(), logits.stride(0) if n > 1 else vocab,
-                                       _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes,
-                                       up, np_, dp, wp, at + 4 * b * max_nodes,
-                                       at + 0, at + 4 * b * (max_nodes + 1), _raw_stream(dev)))
-    return count, path.view(b, max_nodes), nxt
+    tp = _flat(tokens, _I32, "tokens", (n,), dev)
+    pp = _flat(parents, _I32, "parents", (n,), dev)
+    op = _flat(offsets, _I32, "offsets", (b + 1,), dev)
+    up = _flat(uniforms, _F32, "uniforms", (n,), dev)
+    ep = _flat(noise, _F32, "noise", (b, vocab), dev)
+    dp = None if draft_probs is None else _flat(draft_probs, _F32, "draft_probs", (n, vocab), dev)
+    wp = None if temperature is None else _flat(temperature, _F32, "temperature", (b,), dev)
+    place = logits.device
+    path = torch.empty((b, max_nodes), dtype=_I32, device=place)
+    count = torch.empty((b,), dtype=_I32, device=place)
+    nxt = torch.empty((b,), dtype=_I32, device=place)
+    st = (_lib or _load()).cider_verify_drafts(logits.data_ptr(), stride if n > 1 else vocab,
+                                               _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes, up,
+                                               ep, dp, wp, count.data_ptr(), path.data_ptr(), nxt.data_ptr(),
+                                               _raw_stream(dev))
+    if st:
+        _check("cider_verify_drafts", st)
+    return count, path, nxt
