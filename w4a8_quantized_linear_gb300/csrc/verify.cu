@@ -16,8 +16,16 @@
 // Temperature 0: a child is accepted if its token is the logits' first
 // maximum, which is also the next token.
 //
-// Only the nodes on the accepted path are read.  Sums and softmax statistics
-// are fp32, in an order that depends on the sizes alone.
+// Only the nodes on the accepted path are read: its rows of logits once from
+// HBM (again from L2 where a residual or the draw needs them), and the noise of
+// the one draw.  The walk is serial, so what bounds it is latency: a cluster of
+// up to 8 CTAs shares a request's vocabulary, each visited node costs one pass
+// over a CTA's share (softmax maximum and sum in one pass, 4 x 16 bytes per
+// lane in flight) and one exchange between the CTAs through distributed shared
+// memory; the noise, and the row of the child that is asked first, are
+// prefetched to L2 meanwhile.  Every CTA adds the shares' results in the order
+// of their ranks, so all take the same decisions and the same inputs give the
+// same path.  Sums and softmax statistics are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -26,12 +34,16 @@
 #include "cider_device.cuh"
 #include "cider_internal.h"
 #include "kv_common.cuh"
+#include "kv_parts.cuh"
 
 namespace cider {
 namespace {
 
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kBlock = 256;     // tokens that a warp takes at once: 8 per lane
+constexpr int kAtOnce = 4;      // blocks in flight
+constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
   const void* logits;
@@ -66,37 +78,64 @@ struct Rejected {
   int32_t keeps;               // nothing was left: r stayed as it was
 };
 
-struct Shared {
-  float fsum[kVerifyWarps];
-  uint64_t best[kVerifyWarps];
-  Rejected rejected[kMaxNodes];
+// What a thread, a warp or a CTA found in its share: sum counts from top.
+struct Found {
+  float top, sum;
+  uint64_t best;
 };
 
-__device__ __forceinline__ float block_sum(float v, Shared& sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.fsum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kVerifyWarps; ++i) s += sh.fsum[i];
-  return s;
+struct Shared {
+  Found warp[2][kVerifyWarps];   // by exchange
+  Found cta[2][kMaxCluster];
+  Rejected rejected[kMaxNodes];
+  int32_t parent[kMaxNodes], token[kMaxNodes];
+  float uniform[kMaxNodes];
+  float logit[kMaxNodes], drafted[kMaxNodes];   // of the current node's children's tokens
+};
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
-__device__ __forceinline__ uint64_t block_best(uint64_t v, Shared& sh) {
+// The largest top, the sums from it added in a fixed tree, and the largest
+// best, over N lanes (a power of two).  c: the softmax's factor.
+template <int N>
+__device__ __forceinline__ Found join_lanes(Found v, float c) {
+  float top = v.top;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
+  for (int o = N / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  v.sum *= top == -INFINITY ? 1.0f : exp2_approx((v.top - top) * c);
+  v.top = top;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+    const uint64_t w = __shfl_xor_sync(0xffffffffu, v.best, o);
+    v.best = w > v.best ? w : v.best;
   }
+  return v;
+}
+
+// The cluster's result from each thread's: all threads of all its CTAs get the
+// same, by the same additions.  Every second exchange writes the same buffers:
+// between the two lies a barrier that a reader of the older one has passed.
+__device__ __forceinline__ Found exchange(Found v, float c, Shared& sh, int ranks, int rank, int& parity) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = join_lanes<32>(v, c);
+  if (lane == 0) sh.warp[parity][warp] = v;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.best[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint64_t s = sh.best[0];
-#pragma unroll
-  for (int i = 1; i < kVerifyWarps; ++i) s = sh.best[i] > s ? sh.best[i] : s;
-  return s;
+  v = join_lanes<kVerifyWarps>(sh.warp[parity][lane % kVerifyWarps], c);
+  if (ranks > 1) {
+    if (threadIdx.x < ranks)
+      st_cluster_v4(mapa_shared(smem_u32(&sh.cta[parity][rank]), threadIdx.x), __float_as_uint(v.top),
+                    __float_as_uint(v.sum), static_cast<uint32_t>(v.best), static_cast<uint32_t>(v.best >> 32));
+    cluster_sync_all();
+    v = Found{sh.cta[parity][0].top, 0.0f, 0};   // of a rank that is not there
+    if ((lane & (kMaxCluster - 1)) < ranks) v = sh.cta[parity][lane & (kMaxCluster - 1)];
+    v = join_lanes<kMaxCluster>(v, c);
+  }
+  parity ^= 1;
+  return v;
 }
 
 // r(x) after the node's rejected children so far; q: the drafter's row's value at x.
@@ -115,58 +154,168 @@ __device__ __forceinline__ float residual(float p, float q, int x, bool sampled,
   return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
-  __shared__ Shared sh;
-  const int b = blockIdx.x;
+// Every row begins on 16 bytes and holds whole groups of 8: a lane takes 8
+// neighbouring tokens; else it takes every 32nd of the warp's block.
+template <bool VEC>
+__device__ __forceinline__ int token_of(int block, int lane, int j) {
+  return block * kBlock + (VEC ? lane * 8 + j : j * 32 + lane);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, int block, int lane, int vocab, float (&f)[8]) {
+  if constexpr (VEC) {
+    const int x = token_of<true>(block, lane, 0);
+    if (x < vocab) {
+      if constexpr (sizeof(T) == 2) {
+        widen8<T>(*reinterpret_cast<const uint4*>(row + x), f);
+      } else {
+        const float4 a = *reinterpret_cast<const float4*>(row + x), b = *reinterpret_cast<const float4*>(row + x + 4);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int x = token_of<false>(block, lane, j);
+      if constexpr (sizeof(T) == 2)
+        f[j] = x < vocab ? as_float(row[x]) : -INFINITY;
+      else
+        f[j] = x < vocab ? row[x] : -INFINITY;
+    }
+  }
+}
+
+__device__ __forceinline__ void prefetch_range(const void* begin, const void* end) {
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(begin) + 15) & ~uintptr_t{15};
+  const uintptr_t b = reinterpret_cast<uintptr_t>(end) & ~uintptr_t{15};
+  const uint64_t most = 1u << 20;
+  if (b > a)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a),
+                 "r"(static_cast<uint32_t>(b - a < most ? b - a : most))
+                 : "memory");
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a, int ranks) {
+  __shared__ __align__(16) Shared sh;
+  const int rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int b = blockIdx.x / ranks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t first = a.offsets[b];
   const int64_t end = a.offsets[b + 1];
   const bool bad = first < 0 || end > a.nodes || end - first > a.max_nodes || end < first;
   const int size = bad ? 0 : static_cast<int>(end - first);
-  if (bad && threadIdx.x == 0) atomicOr(a.err, kDevErrIndex);
-  for (int i = threadIdx.x; i < a.max_nodes; i += kVerifyThreads)
-    a.path[static_cast<int64_t>(b) * a.max_nodes + i] = size > 0 && i == 0 ? 0 : -1;
+  if (bad && rank == 0 && threadIdx.x == 0) atomicOr(a.err, kDevErrIndex);
+  if (rank == 0)
+    for (int i = threadIdx.x; i < a.max_nodes; i += kVerifyThreads)
+      a.path[static_cast<int64_t>(b) * a.max_nodes + i] = size > 0 && i == 0 ? 0 : -1;
   if (size == 0) {
-    if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
       a.count[b] = 0;
       a.next[b] = -1;
     }
-    return;
+    return;   // all CTAs of the cluster do
   }
+  if (threadIdx.x < size) {
+    sh.parent[threadIdx.x] = a.parents[first + threadIdx.x];
+    sh.token[threadIdx.x] = a.tokens[first + threadIdx.x];
+    sh.uniform[threadIdx.x] = a.uniforms[first + threadIdx.x];
+  }
+  __syncthreads();
+  // the other CTAs must be running before their shared memory is written
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  bool started = ranks == 1;
+  const int blocks = (a.vocab + kBlock - 1) / kBlock;
+  const int begin_block = static_cast<int>(static_cast<int64_t>(blocks) * rank / ranks);
+  const int end_block = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / ranks);
+  const int x0 = begin_block * kBlock, x1 = min(end_block * kBlock, a.vocab);
   const float temperature = a.temperature ? a.temperature[b] : 1.0f;
   const bool greedy = !(temperature > 0.0f);
-  const float inv_t = greedy ? 1.0f : 1.0f / temperature;
+  const float c = greedy ? 1.0f : 1.44269504f / temperature;   // softmax in powers of two
   const float* noise = a.noise + static_cast<int64_t>(b) * a.vocab;
-  int now = 0, count = 1;
+  const T* logits = static_cast<const T*>(a.logits);
+  if (threadIdx.x == 0 && !greedy && x0 < x1) prefetch_range(noise + x0, noise + x1);
+  int now = 0, count = 1, parity = 0;
   for (;;) {
-    const T* row = static_cast<const T*>(a.logits) + (first + now) * a.logits_stride;
+    const T* row = logits + (first + now) * a.logits_stride;
     const float* q = a.draft ? a.draft + (first + now) * a.vocab : nullptr;
-    uint64_t best = 0;
-    for (int x = threadIdx.x; x < a.vocab; x += kVerifyThreads) {
-      const uint64_t p = pack_best(as_float(row[x]), x);
-      best = p > best ? p : best;
+    // the children, in a word; what is asked of them below is fetched meanwhile
+    uint64_t children;
+    {
+      const int i0 = now + 1 + lane, i1 = i0 + 32;
+      const uint32_t lo = __ballot_sync(0xffffffffu, i0 < size && sh.parent[min(i0, kMaxNodes - 1)] == now);
+      const uint32_t hi = __ballot_sync(0xffffffffu, i1 < size && sh.parent[min(i1, kMaxNodes - 1)] == now);
+      children = static_cast<uint64_t>(hi) << 32 | lo;   // bit i: node now + 1 + i
     }
-    const int hot = static_cast<int>(best_index(block_best(best, sh)));
-    const float top = as_float(row[hot]);
-    float sum = 0.0f;
-    if (!greedy) {
-      for (int x = threadIdx.x; x < a.vocab; x += kVerifyThreads)
-        sum += __expf((as_float(row[x]) - top) * inv_t);
-      sum = block_sum(sum, sh);
+    if (children && threadIdx.x == 0 && x0 < x1) {
+      const T* next = logits + (first + now + __ffsll(static_cast<long long>(children))) * a.logits_stride;
+      prefetch_range(next + x0, next + x1);
     }
+    if (threadIdx.x > now && threadIdx.x < size && sh.parent[threadIdx.x] == now) {
+      const int x = sh.token[threadIdx.x];
+      if (x >= 0 && x < a.vocab) {
+        sh.logit[threadIdx.x] = as_float(row[x]);
+        if (q) sh.drafted[threadIdx.x] = q[x];
+      }
+    }
+    // ------------------------------------------------ maximum and sum, one pass
+    Found v{-INFINITY, 0.0f, 0};
+    for (int k = begin_block + warp; k < end_block; k += kVerifyWarps * kAtOnce) {
+      float f[kAtOnce][8];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (k + u * kVerifyWarps < end_block) {
+          load8<T, VEC>(row, k + u * kVerifyWarps, lane, a.vocab, f[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[u][j] = -INFINITY;
+        }
+      }
+      float top = v.top;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, f[u][j]);
+      if (greedy) {
+        if (top > v.top) {   // a later token with the same value is not the first maximum
+#pragma unroll
+          for (int u = kAtOnce - 1; u >= 0; --u)
+#pragma unroll
+            for (int j = 7; j >= 0; --j)
+              if (f[u][j] == top) v.best = pack_best(top, token_of<VEC>(k + u * kVerifyWarps, lane, j));
+          v.top = top;
+        }
+      } else {
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = v.sum * exp2_approx((v.top - base) * c);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum += exp2_approx((f[u][j] - base) * c);
+        v.top = top;
+        v.sum = sum;
+      }
+    }
+    if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    started = true;
+    v = exchange(v, c, sh, ranks, rank, parity);
+    // an all -inf row has no maximum of its own: its first token stands for it
+    const int hot = v.best ? static_cast<int>(best_index(v.best)) : 0;
+    const float top = v.top;
     // a row of -inf alone is no distribution: nothing is accepted
-    const float inv_sum = top == -INFINITY ? 0.0f : 1.0f / sum;
-    auto prob = [&](int x) {
-      const float l = as_float(row[x]);
-      return l == -INFINITY ? 0.0f : __expf((l - top) * inv_t) * inv_sum;
-    };
+    const float inv_sum = top == -INFINITY ? 0.0f : 1.0f / v.sum;
+    auto prob = [&](float l) { return l == -INFINITY ? 0.0f : exp2_approx((l - top) * c) * inv_sum; };
     float mass = 1.0f, drawn = 1.0f;
     int rejected = 0, accepted = -1;
-    for (int i = now + 1; i < size; ++i) {
-      if (a.parents[first + i] != now) continue;
-      const int x = a.tokens[first + i];
+    while (children) {
+      const int i = now + __ffsll(static_cast<long long>(children));
+      children &= children - 1;
+      const int x = sh.token[i];
       if (x < 0 || x >= a.vocab) {
-        if (threadIdx.x == 0) atomicOr(a.err, kDevErrIndex);
+        if (threadIdx.x == 0 && rank == 0) atomicOr(a.err, kDevErrIndex);
         continue;
       }
       if (greedy) {
@@ -176,9 +325,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
         }
         continue;
       }
-      const float u = a.uniforms[first + i];
-      float qx = q ? q[x] : 1.0f;
-      const float r = residual(prob(x), qx, x, q != nullptr, sh.rejected, rejected);
+      const float u = sh.uniform[i];
+      float qx = q ? sh.drafted[i] : 1.0f;
+      const float r = residual(prob(sh.logit[i]), qx, x, q != nullptr, sh.rejected, rejected);
       if (!q) {
         if (u * mass < r) {
           accepted = i;
@@ -201,40 +350,98 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
       if (threadIdx.x == 0) sh.rejected[rejected] = Rejected{1.0f / mass, 1.0f / drawn, x, 0};
       __syncthreads();
       ++rejected;
-      float rest = 0.0f;
-      for (int y = threadIdx.x; y < a.vocab; y += kVerifyThreads)
-        rest += residual(prob(y), q[y], y, true, sh.rejected, rejected);
-      rest = block_sum(rest, sh);
+      Found rest{0.0f, 0.0f, 0};
+      for (int k = begin_block + warp; k < end_block; k += kVerifyWarps) {
+        float f[8], g[8];
+        load8<T, VEC>(row, k, lane, a.vocab, f);
+        load8<float, VEC>(q, k, lane, a.vocab, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (token_of<VEC>(k, lane, j) < a.vocab)
+            rest.sum += residual(prob(f[j]), g[j], token_of<VEC>(k, lane, j), true, sh.rejected, rejected);
+      }
+      rest = exchange(rest, 0.0f, sh, ranks, rank, parity);
       drawn -= qx;
-      if (rest == 0.0f) {
+      if (rest.sum == 0.0f) {
         if (threadIdx.x == 0) sh.rejected[rejected - 1].keeps = 1;
         __syncthreads();
       } else {
-        mass = rest;
+        mass = rest.sum;
       }
     }
     if (accepted >= 0) {
-      if (threadIdx.x == 0) a.path[static_cast<int64_t>(b) * a.max_nodes + count] = accepted;
+      if (rank == 0 && threadIdx.x == 0) a.path[static_cast<int64_t>(b) * a.max_nodes + count] = accepted;
       ++count;
       now = accepted;
       continue;
     }
     int next = hot;
     if (!greedy) {
-      best = 0;
-      for (int x = threadIdx.x; x < a.vocab; x += kVerifyThreads) {
-        const float r = residual(prob(x), q ? q[x] : 0.0f, x, q != nullptr, sh.rejected, rejected);
-        const uint64_t p = pack_best(__fdiv_rn(r, noise[x]), x);
-        best = p > best ? p : best;
+      // the largest r / e at its lowest token; r's factor 1 / sum is left out
+      // where nothing is subtracted from it
+      const float base = top == -INFINITY ? 0.0f : top;
+      float high = -1.0f;
+      int at = 0;
+      for (int k = begin_block + warp; k < end_block; k += kVerifyWarps * 2) {
+        float f[2][8], e[2][8], g[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (k + u * kVerifyWarps < end_block) {
+            load8<T, VEC>(row, k + u * kVerifyWarps, lane, a.vocab, f[u]);
+            load8<float, VEC>(noise, k + u * kVerifyWarps, lane, a.vocab, e[u]);
+            if (q) load8<float, VEC>(q, k + u * kVerifyWarps, lane, a.vocab, g[u]);
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (k + u * kVerifyWarps < end_block)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int x = token_of<VEC>(k + u * kVerifyWarps, lane, j);
+              float r = exp2_approx((f[u][j] - base) * c);
+              if (q) r = residual(r * inv_sum, g[u][j], x, true, sh.rejected, rejected);
+              float inv;
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e[u][j]));
+              float key = r * inv;
+              if (key > high && x < a.vocab) {   // rare after the first tokens
+                if (!q && residual(1.0f, 0.0f, x, false, sh.rejected, rejected) == 0.0f) key = 0.0f;
+                if (key > high) {
+                  high = key;
+                  at = x;
+                }
+              }
+            }
       }
-      next = static_cast<int>(best_index(block_best(best, sh)));
+      const uint64_t mine = high < 0.0f ? 0 : pack_best(high, at);
+      next = static_cast<int>(best_index(exchange(Found{0.0f, 0.0f, mine}, 0.0f, sh, ranks, rank, parity).best));
     }
-    if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
       a.count[b] = count;
       a.next[b] = next;
     }
     return;
   }
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_typed(const VerifyArgs& a, int num_sms, cudaStream_t st) {
+  // two CTAs fit an SM: as many per request as fit at once, and have a block of
+  // tokens for each of their warps
+  int ranks = kMaxCluster;
+  while (ranks > 1 && (static_cast<int64_t>(a.requests) * ranks > 2 * num_sms ||
+                       (a.vocab + kBlock - 1) / kBlock < ranks * kVerifyWarps / 2))
+    ranks /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.requests) * ranks);
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, a, ranks);
 }
 
 }  // namespace
@@ -245,15 +452,14 @@ cudaError_t launch_verify(const void* logits, int64_t logits_stride, bool bf16,
                           const float* uniforms, const float* noise, const float* draft,
                           const float* temperature, int32_t* count, int32_t* path, int32_t* next,
                           int* err, int num_sms, cudaStream_t st) {
-  (void)num_sms;
   const VerifyArgs a{logits, logits_stride, tokens, parents, offsets, requests, nodes,
                      vocab,  max_nodes,     uniforms, noise, draft,   temperature, count,
                      path,   next,          err};
+  auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vec = vocab % 8 == 0 && logits_stride % 8 == 0 && on16(logits) && on16(noise) && on16(draft);
   if (bf16)
-    verify_kernel<__nv_bfloat16><<<requests, kVerifyThreads, 0, st>>>(a);
-  else
-    verify_kernel<__half><<<requests, kVerifyThreads, 0, st>>>(a);
-  return cudaGetLastError();
+    return vec ? launch_typed<__nv_bfloat16, true>(a, num_sms, st) : launch_typed<__nv_bfloat16, false>(a, num_sms, st);
+  return vec ? launch_typed<__half, true>(a, num_sms, st) : launch_typed<__half, false>(a, num_sms, st);
 }
 
 }  // namespace cider
