@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cider_device.cuh"
 #include "cider_internal.h"
 #include "kv_common.cuh"
@@ -42,7 +44,7 @@ namespace {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kBlock = 256;     // tokens that a warp takes at once: 8 per lane
-constexpr int kAtOnce = 4;      // blocks in flight
+constexpr int kAtOnce = 8;      // blocks in flight
 constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
@@ -87,15 +89,23 @@ struct Found {
 struct Shared {
   Found warp[2][kVerifyWarps];   // by exchange
   Found cta[2][kMaxCluster];
+  uint64_t bar[2];               // the ranks' results of an exchange have arrived
+  uint32_t abort;
   Rejected rejected[kMaxNodes];
   int32_t parent[kMaxNodes], token[kMaxNodes];
   float uniform[kMaxNodes];
   float logit[kMaxNodes], drafted[kMaxNodes];   // of the current node's children's tokens
 };
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
+// 16 bytes to another CTA's shared memory, counted on its mbarrier when they
+// are there.  (A cluster barrier with its release costs ~1500 cycles on GB300,
+// an exchange by it took 3000.)
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                            uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+      : "memory");
 }
 
 // The largest top, the sums from it added in a fixed tree, and the largest
@@ -117,39 +127,41 @@ __device__ __forceinline__ Found join_lanes(Found v, float c) {
 }
 
 // The cluster's result from each thread's: all threads of all its CTAs get the
-// same, by the same additions.  Every second exchange writes the same buffers:
-// between the two lies a barrier that a reader of the older one has passed.
-__device__ __forceinline__ Found exchange(Found v, float c, Shared& sh, int ranks, int rank, int& parity) {
+// same, by the same additions.  Every second exchange uses the same buffers: a
+// rank sends for the one after the next only when it has this CTA's results of
+// the next, which are sent when all threads here have read the present ones.
+__device__ __forceinline__ Found exchange(Found v, float c, Shared& sh, int ranks, int rank, uint32_t& count,
+                                          int* err) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t parity = count & 1, phase = count >> 1 & 1;
   v = join_lanes<32>(v, c);
   if (lane == 0) sh.warp[parity][warp] = v;
   __syncthreads();
   v = join_lanes<kVerifyWarps>(sh.warp[parity][lane % kVerifyWarps], c);
   if (ranks > 1) {
-    if (threadIdx.x < ranks)
-      st_cluster_v4(mapa_shared(smem_u32(&sh.cta[parity][rank]), threadIdx.x), __float_as_uint(v.top),
-                    __float_as_uint(v.sum), static_cast<uint32_t>(v.best), static_cast<uint32_t>(v.best >> 32));
-    cluster_sync_all();
+    volatile uint32_t* abort_flag = &sh.abort;
+    const uint32_t bar = smem_u32(&sh.bar[parity]);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, ranks * 16u);
+    if (threadIdx.x < ranks && !*abort_flag)
+      st_async_v4(mapa_shared(smem_u32(&sh.cta[parity][rank]), threadIdx.x), __float_as_uint(v.top),
+                  __float_as_uint(v.sum), static_cast<uint32_t>(v.best), static_cast<uint32_t>(v.best >> 32),
+                  mapa_shared(bar, threadIdx.x));
+    mbar_wait_bounded(bar, phase, abort_flag, err, kKernelWaitTimeoutNs);
     v = Found{sh.cta[parity][0].top, 0.0f, 0};   // of a rank that is not there
     if ((lane & (kMaxCluster - 1)) < ranks) v = sh.cta[parity][lane & (kMaxCluster - 1)];
     v = join_lanes<kMaxCluster>(v, c);
   }
-  parity ^= 1;
+  ++count;
   return v;
 }
 
-// r(x) after the node's rejected children so far; q: the drafter's row's value at x.
-__device__ __forceinline__ float residual(float p, float q, int x, bool sampled,
-                                          const Rejected* rejected, int n) {
-  float r = p;
+// r(x) of sampled drafts after the node's rejected children so far; q: the
+// drafter's row's value at x.
+__device__ __forceinline__ float residual(float r, float q, int x, const Rejected* rejected, int n) {
   for (int j = 0; j < n; ++j) {
     const Rejected& e = rejected[j];
-    if (sampled) {
-      if (!e.keeps) r = fmaxf(r * e.inv_mass - q * e.inv_drawn, 0.0f);
-      if (x == e.token) q = 0.0f;
-    } else if (x == e.token) {
-      r = 0.0f;
-    }
+    if (!e.keeps) r = fmaxf(r * e.inv_mass - q * e.inv_drawn, 0.0f);
+    if (x == e.token) q = 0.0f;
   }
   return r;
 }
@@ -188,6 +200,43 @@ __device__ __forceinline__ void load8(const T* row, int block, int lane, int voc
   }
 }
 
+// The same as packed 16-bit values; tokens past the end are -inf.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_raw(const T* row, int block, int lane, int vocab) {
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;
+  uint4 r = make_uint4(kInf << 16 | kInf, kInf << 16 | kInf, kInf << 16 | kInf, kInf << 16 | kInf);
+  if constexpr (VEC) {
+    const int x = token_of<true>(block, lane, 0);
+    if (x < vocab) r = *reinterpret_cast<const uint4*>(row + x);
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int x = token_of<false>(block, lane, 2 * j), y = token_of<false>(block, lane, 2 * j + 1);
+      w[j] = (x < vocab ? p[x] : kInf) | static_cast<uint32_t>(y < vocab ? p[y] : kInf) << 16;
+    }
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = __hmax2(x, y);
+    memcpy(&a, &x, 4);
+  } else {
+    __nv_bfloat162 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = __hmax2(x, y);
+    memcpy(&a, &x, 4);
+  }
+  return a;
+}
+
 __device__ __forceinline__ void prefetch_range(const void* begin, const void* end) {
   const uintptr_t a = (reinterpret_cast<uintptr_t>(begin) + 15) & ~uintptr_t{15};
   const uintptr_t b = reinterpret_cast<uintptr_t>(end) & ~uintptr_t{15};
@@ -224,8 +273,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     sh.token[threadIdx.x] = a.tokens[first + threadIdx.x];
     sh.uniform[threadIdx.x] = a.uniforms[first + threadIdx.x];
   }
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    mbar_init(smem_u32(&sh.bar[0]), 1);
+    mbar_init(smem_u32(&sh.bar[1]), 1);
+    fence_mbar_init();
+  }
   __syncthreads();
-  // the other CTAs must be running before their shared memory is written
+  // the other CTAs' barriers must be there before they are sent anything
   if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   bool started = ranks == 1;
   const int blocks = (a.vocab + kBlock - 1) / kBlock;
@@ -238,7 +293,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
   const float* noise = a.noise + static_cast<int64_t>(b) * a.vocab;
   const T* logits = static_cast<const T*>(a.logits);
   if (threadIdx.x == 0 && !greedy && x0 < x1) prefetch_range(noise + x0, noise + x1);
-  int now = 0, count = 1, parity = 0;
+  int now = 0, count = 1;
+  uint32_t exchanges = 0;
   for (;;) {
     const T* row = logits + (first + now) * a.logits_stride;
     const float* q = a.draft ? a.draft + (first + now) * a.vocab : nullptr;
@@ -264,44 +320,43 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     // ------------------------------------------------ maximum and sum, one pass
     Found v{-INFINITY, 0.0f, 0};
     for (int k = begin_block + warp; k < end_block; k += kVerifyWarps * kAtOnce) {
-      float f[kAtOnce][8];
+      uint4 raw[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        if (k + u * kVerifyWarps < end_block) {
-          load8<T, VEC>(row, k + u * kVerifyWarps, lane, a.vocab, f[u]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[u][j] = -INFINITY;
-        }
-      }
-      float top = v.top;
+      for (int u = 0; u < kAtOnce; ++u)   // past the share: past the vocabulary
+        raw[u] = load_raw<T, VEC>(row, k + u * kVerifyWarps, lane, k + u * kVerifyWarps < end_block ? a.vocab : 0);
+      uint32_t high = raw[0].x;
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, f[u][j]);
+        high = max2<T>(max2<T>(high, max2<T>(raw[u].x, raw[u].y)), max2<T>(raw[u].z, raw[u].w));
+      float f[8];
+      widen8<T>(make_uint4(high, high, high, high), f);
+      const float top = fmaxf(v.top, fmaxf(f[0], f[1]));
       if (greedy) {
         if (top > v.top) {   // a later token with the same value is not the first maximum
 #pragma unroll
-          for (int u = kAtOnce - 1; u >= 0; --u)
+          for (int u = kAtOnce - 1; u >= 0; --u) {
+            widen8<T>(raw[u], f);
 #pragma unroll
             for (int j = 7; j >= 0; --j)
-              if (f[u][j] == top) v.best = pack_best(top, token_of<VEC>(k + u * kVerifyWarps, lane, j));
-          v.top = top;
+              if (f[j] == top) v.best = pack_best(top, token_of<VEC>(k + u * kVerifyWarps, lane, j));
+          }
         }
       } else {
         const float base = top == -INFINITY ? 0.0f : top;
         float sum = v.sum * exp2_approx((v.top - base) * c);
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
+        for (int u = 0; u < kAtOnce; ++u) {
+          widen8<T>(raw[u], f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum += exp2_approx((f[u][j] - base) * c);
-        v.top = top;
+          for (int j = 0; j < 8; ++j) sum += exp2_approx((f[j] - base) * c);
+        }
         v.sum = sum;
       }
+      v.top = top;
     }
     if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     started = true;
-    v = exchange(v, c, sh, ranks, rank, parity);
+    v = exchange(v, c, sh, ranks, rank, exchanges, a.err);
     // an all -inf row has no maximum of its own: its first token stands for it
     const int hot = v.best ? static_cast<int>(best_index(v.best)) : 0;
     const float top = v.top;
@@ -310,6 +365,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     auto prob = [&](float l) { return l == -INFINITY ? 0.0f : exp2_approx((l - top) * c) * inv_sum; };
     float mass = 1.0f, drawn = 1.0f;
     int rejected = 0, accepted = -1;
+    uint64_t refused = 0;   // certain drafts: the rejected children, by node
     while (children) {
       const int i = now + __ffsll(static_cast<long long>(children));
       children &= children - 1;
@@ -327,19 +383,19 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
       }
       const float u = sh.uniform[i];
       float qx = q ? sh.drafted[i] : 1.0f;
-      const float r = residual(prob(sh.logit[i]), qx, x, q != nullptr, sh.rejected, rejected);
+      float r = prob(sh.logit[i]);
       if (!q) {
+        for (uint64_t m = refused; m; m &= m - 1)
+          if (sh.token[__ffsll(static_cast<long long>(m)) - 1] == x) r = 0.0f;
         if (u * mass < r) {
           accepted = i;
           break;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) sh.rejected[rejected] = Rejected{0.0f, 0.0f, x, 0};
-        __syncthreads();
-        ++rejected;
+        refused |= uint64_t{1} << i;
         mass -= r;
         continue;
       }
+      r = residual(r, qx, x, sh.rejected, rejected);
       for (int j = 0; j < rejected; ++j)
         if (sh.rejected[j].token == x) qx = 0.0f;
       if (u * qx * mass < r * drawn) {
@@ -358,9 +414,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (token_of<VEC>(k, lane, j) < a.vocab)
-            rest.sum += residual(prob(f[j]), g[j], token_of<VEC>(k, lane, j), true, sh.rejected, rejected);
+            rest.sum += residual(prob(f[j]), g[j], token_of<VEC>(k, lane, j), sh.rejected, rejected);
       }
-      rest = exchange(rest, 0.0f, sh, ranks, rank, parity);
+      rest = exchange(rest, 0.0f, sh, ranks, rank, exchanges, a.err);
       drawn -= qx;
       if (rest.sum == 0.0f) {
         if (threadIdx.x == 0) sh.rejected[rejected - 1].keeps = 1;
@@ -384,6 +440,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
       int at = 0;
       for (int k = begin_block + warp; k < end_block; k += kVerifyWarps * 2) {
         float f[2][8], e[2][8], g[2][8];
+        uint64_t here[2] = {0, 0};   // rejected certain drafts among the block's tokens
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           if (k + u * kVerifyWarps < end_block) {
@@ -391,35 +448,47 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
             load8<float, VEC>(noise, k + u * kVerifyWarps, lane, a.vocab, e[u]);
             if (q) load8<float, VEC>(q, k + u * kVerifyWarps, lane, a.vocab, g[u]);
           }
+        for (uint64_t m = refused; m; m &= m - 1) {
+          const int i = __ffsll(static_cast<long long>(m)) - 1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (k + u * kVerifyWarps < end_block)
+          for (int u = 0; u < 2; ++u)
+            if (sh.token[i] / kBlock == k + u * kVerifyWarps) here[u] |= uint64_t{1} << i;
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int x = token_of<VEC>(k + u * kVerifyWarps, lane, j);
-              float r = exp2_approx((f[u][j] - base) * c);
-              if (q) r = residual(r * inv_sum, g[u][j], x, true, sh.rejected, rejected);
-              float inv;
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e[u][j]));
-              float key = r * inv;
-              if (key > high && x < a.vocab) {   // rare after the first tokens
-                if (!q && residual(1.0f, 0.0f, x, false, sh.rejected, rejected) == 0.0f) key = 0.0f;
-                if (key > high) {
-                  high = key;
-                  at = x;
-                }
-              }
+        for (int u = 0; u < 2; ++u) {
+          if (k + u * kVerifyWarps >= end_block) continue;
+          for (uint64_t m = here[u]; m; m &= m - 1) {
+            const int x = sh.token[__ffsll(static_cast<long long>(m)) - 1];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (token_of<VEC>(k + u * kVerifyWarps, lane, j) == x) f[u][j] = -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int x = token_of<VEC>(k + u * kVerifyWarps, lane, j);
+            float r = exp2_approx((f[u][j] - base) * c);
+            if (q) r = residual(r * inv_sum, g[u][j], x, sh.rejected, rejected);
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e[u][j]));
+            const float key = x < a.vocab ? r * inv : -1.0f;
+            if (key > high) {
+              high = key;
+              at = x;
             }
+          }
+        }
       }
       const uint64_t mine = high < 0.0f ? 0 : pack_best(high, at);
-      next = static_cast<int>(best_index(exchange(Found{0.0f, 0.0f, mine}, 0.0f, sh, ranks, rank, parity).best));
+      next = static_cast<int>(best_index(exchange(Found{0.0f, 0.0f, mine}, 0.0f, sh, ranks, rank, exchanges, a.err).best));
     }
     if (rank == 0 && threadIdx.x == 0) {
       a.count[b] = count;
       a.next[b] = next;
     }
-    return;
+    break;
   }
+  // after a wait that gave up a CTA may still be sent something
+  if (ranks > 1 && __syncthreads_or(sh.abort)) cluster_sync_all();
 }
 
 template <typename T, bool VEC>
