@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         float sum = v.sum * exp2_approx((v.top - base) * c);
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
+          if (u > 0 && k + u * kVerifyWarps >= end_block) break;
           widen8<T>(raw[u], f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) sum += exp2_approx((f[j] - base) * c);
