@@ -12,12 +12,15 @@
 //
 // What bounds these kernels is HBM traffic: every input byte is read once and
 // every output byte written once, eight values (16 bytes of fp16 / bf16) per
-// thread and access, key and value side by side so that each thread has two
-// independent loads in flight.
+// thread and access, several independent loads in flight per thread.  Issue
+// slots come second: at 4 instructions a clock the append has ~11 a value, so
+// the maximum is taken on packed pairs, the scale and the quotients by
+// corrected reciprocals, and the codes come out of float additions.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "cider_device.cuh"
@@ -31,7 +34,7 @@ constexpr int kRowThreads = 256;
 
 // ------------------------------------------------------------------ append
 // Eight values of a row -> their codes as bytes (INT8: 8 bytes) or packed
-// nibbles (INT4: 4 bytes in lo).  FAST: r = RN(1/s) and Markstein's corrected
+// nibbles (INT4: 4 bytes in x).  FAST: r = RN(1/s) and Markstein's corrected
 // quotient; it needs s normal and far from the ends of the exponent range.
 template <int BITS, bool FAST>
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float r) {
@@ -46,36 +49,53 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float r) 
       q = fminf(fmaxf(__fdiv_rn(f[i], s), -kTop), kTop);
     }
     // 1.5 * 2^23 puts the nearest whole number (ties to even) in the low
-    // mantissa bits, in two's complement
-    c[i] = __float_as_uint(__fadd_rn(q, 12582912.0f));
+    // mantissa bits: INT8 in two's complement, INT4 plus 8 (an even offset
+    // leaves the ties as they are)
+    c[i] = __float_as_uint(__fadd_rn(q, BITS == 8 ? 12582912.0f : 12582920.0f));
   }
   if constexpr (BITS == 8) {
     const uint32_t a = __byte_perm(c[0], c[1], 0x0040u), b = __byte_perm(c[2], c[3], 0x0040u);
     const uint32_t d = __byte_perm(c[4], c[5], 0x0040u), e = __byte_perm(c[6], c[7], 0x0040u);
     return make_uint2(__byte_perm(a, b, 0x5410u), __byte_perm(d, e, 0x5410u));
   } else {
-    uint32_t w = 0;
+    // sum of c_i 16^i: the nibbles side by side above the sum of the constant
+    // float bits, which is taken off; then plus 8 -> two's complement
+    uint32_t w = c[7];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= (c[i] & 0xFu) << (4 * i);
-    return make_uint2(w, 0u);
+    for (int i = 6; i >= 0; --i) w = w * 16u + c[i];
+    return make_uint2((w - 0x4B400000u * 0x11111111u) ^ 0x88888888u, 0u);
   }
+}
+
+// max |x| over two packed values each.
+template <typename T>
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+  using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  P x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = __hmax2(__habs2(x), __habs2(y));
+  memcpy(&a, &x, 4);
+  return a;
 }
 
 template <typename T, int D, int BITS>
 __device__ __forceinline__ void append_row(const uint4& in, uint8_t* codes, float* scale, int lane,
                                            bool write) {
   constexpr int kLanes = D / 8;
+  uint32_t m = amax2<T>(amax2<T>(in.x, in.y), amax2<T>(in.z, in.w));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = amax2<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
   float f[8];
-  widen8<T>(in, f);
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  widen8<T>(make_uint4(m, m, m, m), f);
+  const float a = fmaxf(f[0], f[1]);
   constexpr float kTop = BITS == 8 ? 127.0f : 7.0f;
-  const float s = a > 0.0f ? __fdiv_rn(a, kTop) : 1.0f;
-  // fp16 scales are always in this range; bf16 ones reach 2^-140
-  const bool fast = s > 1e-30f && s < 1e30f;
+  // corrected quotient by the constant's reciprocal while nothing underflows
+  // on the way (fp16 always; bf16 maxima reach 2^-133)
+  const bool fast = a > 1e-28f && a < 1e32f;
+  float s = div_rn_by(a, kTop, 1.0f / kTop);
+  if (!fast) s = a > 0.0f ? __fdiv_rn(a, kTop) : 1.0f;
+  widen8<T>(in, f);
   const uint2 c = fast ? encode8<BITS, true>(f, s, __frcp_rn(s)) : encode8<BITS, false>(f, s, 0.0f);
   if (!write) return;
   if constexpr (BITS == 8)
@@ -85,60 +105,74 @@ __device__ __forceinline__ void append_row(const uint4& in, uint8_t* codes, floa
   if (lane == 0) *scale = s;
 }
 
-// D / 8 neighbouring threads hold one (token, head) row of K and of V.
+// D / 8 neighbouring threads hold one (token, head) row of K and of V, and the
+// same of a second token.  Blocks of all heads of the same tokens run together.
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kRowThreads)
     kv_append_kernel(KvCache cache, const T* __restrict__ k, int64_t k_stride,
                      const T* __restrict__ v, int64_t v_stride, const int64_t* __restrict__ slots,
-                     uint32_t rows, int* err) {
-  constexpr int kLanes = D / 8;
-  const uint32_t row = (blockIdx.x * kRowThreads + threadIdx.x) / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  const bool have = row < rows;
-  const uint32_t token = have ? row / static_cast<uint32_t>(cache.heads) : 0;
-  const uint32_t head = have ? row - token * cache.heads : 0;
-  uint4 kin = make_uint4(0, 0, 0, 0), vin = make_uint4(0, 0, 0, 0);
-  int64_t slot = -1;
-  if (have) {
-    kin = ld_stream_v4(k + static_cast<int64_t>(token) * k_stride + head * D + lane * 8);
-    vin = ld_stream_v4(v + static_cast<int64_t>(token) * v_stride + head * D + lane * 8);
-    slot = slots[token];
+                     int tokens, int* err) {
+  constexpr int kLanes = D / 8, kGroups = kRowThreads / kLanes, kRowBytes = D * BITS / 8;
+  const int lane = threadIdx.x % kLanes, head = blockIdx.x;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * (2 * kGroups); t0 < tokens;
+       t0 += static_cast<int64_t>(gridDim.y) * (2 * kGroups)) {
+    uint4 kin[2], vin[2];
+    int64_t slot[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t token = t0 + u * kGroups + threadIdx.x / kLanes;
+      kin[u] = vin[u] = make_uint4(0, 0, 0, 0);
+      slot[u] = -1;
+      if (token < tokens) {
+        kin[u] = ld_stream_v4(k + token * k_stride + head * D + lane * 8);
+        vin[u] = ld_stream_v4(v + token * v_stride + head * D + lane * 8);
+        slot[u] = slots[token];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool inside = slot[u] >= 0 && slot[u] < cache.pages << cache.page_shift;
+      if (slot[u] >= 0 && !inside && lane == 0) atomicOr(err, kDevErrIndex);
+      const int page = inside ? static_cast<int>(slot[u] >> cache.page_shift) : 0;
+      const int at_page = static_cast<int>(slot[u]) & ((1 << cache.page_shift) - 1);
+      // 16-row blocks of a layer fit 32 bits
+      const int64_t at = (static_cast<int64_t>(page * cache.heads + head) << cache.page_shift) + at_page;
+      append_row<T, D, BITS>(kin[u], cache.k + at * kRowBytes, cache.k_scale + at, lane, inside);
+      append_row<T, D, BITS>(vin[u], cache.v + at * kRowBytes, cache.v_scale + at, lane, inside);
+    }
   }
-  const bool inside = slot >= 0 && slot < cache.pages << cache.page_shift;
-  if (slot >= 0 && !inside && lane == 0) atomicOr(err, kDevErrIndex);
-  const int64_t at =
-      inside ? cache.row(slot >> cache.page_shift, head,
-                         static_cast<int>(slot & ((1 << cache.page_shift) - 1)))
-             : 0;
-  constexpr int kRowBytes = D * BITS / 8;
-  append_row<T, D, BITS>(kin, cache.k + at * kRowBytes, cache.k_scale + at, lane, inside);
-  append_row<T, D, BITS>(vin, cache.v + at * kRowBytes, cache.v_scale + at, lane, inside);
 }
 
 // -------------------------------------------------------------------- read
+// Eight codes times s: each an exact float (its byte in the mantissa of 2^23,
+// the offset subtracted; a conversion instruction runs at a quarter of the
+// rate), the fp32 product rounded once to the output type.
 template <typename T, int BITS>
 __device__ __forceinline__ uint4 decode8(uint2 c, float s) {
-  uint4 out;
-  uint32_t* o = reinterpret_cast<uint32_t*>(&out);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    int lo, hi;
-    if constexpr (BITS == 8) {
-      const uint32_t w = j < 2 ? c.x : c.y;
-      lo = static_cast<int8_t>(w >> (16 * (j & 1)));
-      hi = static_cast<int8_t>(w >> (16 * (j & 1) + 8));
-    } else {
-      lo = static_cast<int>(c.x << (28 - 8 * j)) >> 28;
-      hi = static_cast<int>(c.x << (24 - 8 * j)) >> 28;
-    }
-    // the value is the fp32 product, rounded once to the output type
-    o[j] = y_bits2<std::is_same<T, __nv_bfloat16>::value>(__fmul_rn(static_cast<float>(lo), s),
-                                                         __fmul_rn(static_cast<float>(hi), s));
+  uint32_t even, odd;   // INT8: codes 0..3, 4..7 plus 128; INT4: even, odd ones plus 8
+  if constexpr (BITS == 8) {
+    even = c.x ^ 0x80808080u;
+    odd = c.y ^ 0x80808080u;
+  } else {
+    const uint32_t u = c.x ^ 0x88888888u;
+    even = u & 0x0F0F0F0Fu;
+    odd = u >> 4 & 0x0F0F0F0Fu;
   }
-  return out;
+  constexpr float kOff = 8388608.0f + (BITS == 8 ? 128.0f : 8.0f);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __byte_perm(even, 0x4B000000u, 0x7440u | i), b = __byte_perm(odd, 0x4B000000u, 0x7440u | i);
+    f[BITS == 8 ? i : 2 * i] = __fmul_rn(__uint_as_float(a) - kOff, s);
+    f[BITS == 8 ? i + 4 : 2 * i + 1] = __fmul_rn(__uint_as_float(b) - kOff, s);
+  }
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  return make_uint4(y_bits2<kBf16>(f[0], f[1]), y_bits2<kBf16>(f[2], f[3]), y_bits2<kBf16>(f[4], f[5]),
+                    y_bits2<kBf16>(f[6], f[7]));
 }
 
-// A CTA reads `tile` tokens (at most 32) of one layer, all heads.
+// A CTA reads `tile` tokens (at most 32) of one layer, all heads; a thread has
+// the codes and scales of four rows' K and V on their way at once.
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kRowThreads)
     kv_read_kernel(KvCache cache, const int32_t* __restrict__ table, int64_t table_width,
@@ -148,6 +182,7 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kRowThreads / kLanes;
   constexpr int kRowBytes = D * BITS / 8;
+  constexpr int kAtOnce = 4;
   __shared__ int64_t place[32];   // row of the cache for head 0, or -1
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile;
   const int here = static_cast<int>(min(static_cast<int64_t>(tile), tokens - t0));
@@ -155,115 +190,144 @@ __global__ void __launch_bounds__(kRowThreads)
     const int64_t i = t0 + threadIdx.x;
     const int b = find_request(offsets, requests, i);
     int64_t at = -1;
-    if (b >= 0) {
-      const int64_t pos = static_cast<int64_t>(starts[b]) + i - offsets[b];
-      const int64_t slot_page = pos >> cache.page_shift;
-      int64_t page = -1;
-      if (pos >= 0 && slot_page < table_width) page = table[b * table_width + slot_page];
-      if (page >= 0 && page < cache.pages)
-        at = cache.row(page, 0, static_cast<int>(pos & ((1 << cache.page_shift) - 1)));
-    }
+    if (b >= 0) at = cache_row_of(cache, table, table_width, b, static_cast<int64_t>(starts[b]) + i - offsets[b], 0);
     if (at < 0) atomicOr(err, kDevErrIndex);
     place[threadIdx.x] = at;
   }
   __syncthreads();
   const int lane = threadIdx.x % kLanes;
   const int64_t layer_rows = cache.layer_rows();
-  const uint8_t* ck = cache.k + blockIdx.y * layer_rows * kRowBytes;
-  const uint8_t* cv = cache.v + blockIdx.y * layer_rows * kRowBytes;
+  const uint8_t* ck = cache.k + blockIdx.y * layer_rows * kRowBytes + lane * BITS;
+  const uint8_t* cv = cache.v + blockIdx.y * layer_rows * kRowBytes + lane * BITS;
   const float* sk = cache.k_scale + blockIdx.y * layer_rows;
   const float* sv = cache.v_scale + blockIdx.y * layer_rows;
-  const int64_t out0 = (static_cast<int64_t>(blockIdx.y) * tokens + t0) * cache.heads;
+  const int64_t out0 = (static_cast<int64_t>(blockIdx.y) * tokens + t0) * cache.heads * D + lane * 8;
+  T* const ko = k + out0;
+  T* const vo = v + out0;
   const int rows = here * cache.heads;
-#pragma unroll 2
-  for (int r = threadIdx.x / kLanes; r < rows; r += kGroups) {
-    const int token = r / cache.heads, head = r - token * cache.heads;
-    const int64_t at = place[token];
-    uint4 ok = make_uint4(0, 0, 0, 0), ov = ok;
-    if (at >= 0) {
-      const int64_t row = at + (static_cast<int64_t>(head) << cache.page_shift);
-      uint2 a, b;
-      if constexpr (BITS == 8) {
-        a = *reinterpret_cast<const uint2*>(ck + row * kRowBytes + lane * 8);
-        b = *reinterpret_cast<const uint2*>(cv + row * kRowBytes + lane * 8);
-      } else {
-        a = make_uint2(*reinterpret_cast<const uint32_t*>(ck + row * kRowBytes + lane * 4), 0u);
-        b = make_uint2(*reinterpret_cast<const uint32_t*>(cv + row * kRowBytes + lane * 4), 0u);
+  // the rows of this group: one division, then steps with a carry
+  int r = threadIdx.x / kLanes;
+  int token = r / cache.heads, head = r - token * cache.heads;
+  const int step_token = kGroups / cache.heads, step_head = kGroups - step_token * cache.heads;
+  while (r < rows) {
+    uint2 a[kAtOnce], b[kAtOnce];
+    float s[kAtOnce], t[kAtOnce];
+    int at_row[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      a[u] = b[u] = make_uint2(0, 0);
+      s[u] = t[u] = 0.0f;
+      at_row[u] = r;
+      const int64_t at = r < rows ? place[token] : -1;
+      if (at >= 0) {
+        const int64_t row = at + (static_cast<int64_t>(head) << cache.page_shift);
+        if constexpr (BITS == 8) {
+          a[u] = *reinterpret_cast<const uint2*>(ck + row * kRowBytes);
+          b[u] = *reinterpret_cast<const uint2*>(cv + row * kRowBytes);
+        } else {
+          a[u].x = *reinterpret_cast<const uint32_t*>(ck + row * kRowBytes);
+          b[u].x = *reinterpret_cast<const uint32_t*>(cv + row * kRowBytes);
+        }
+        s[u] = sk[row];
+        t[u] = sv[row];
       }
-      ok = decode8<T, BITS>(a, sk[row]);
-      ov = decode8<T, BITS>(b, sv[row]);
+      r += kGroups;
+      token += step_token;
+      head += step_head;
+      if (head >= cache.heads) {
+        head -= cache.heads;
+        ++token;
+      }
     }
-    const int64_t o = (out0 + r) * D + lane * 8;
-    *reinterpret_cast<uint4*>(k + o) = ok;
-    *reinterpret_cast<uint4*>(v + o) = ov;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (at_row[u] < rows) {   // without a page: zeros
+        *reinterpret_cast<uint4*>(ko + static_cast<int64_t>(at_row[u]) * D) = decode8<T, BITS>(a[u], s[u]);
+        *reinterpret_cast<uint4*>(vo + static_cast<int64_t>(at_row[u]) * D) = decode8<T, BITS>(b[u], t[u]);
+      }
   }
 }
 
 // ----------------------------------------------------------------- compact
-// One CTA per (layer, request, head): row start + path[i] moves to start + i.
-// Every row is read before any is written, so a path may overlap its target.
-constexpr int kCompactThreads = 128;
+// Row start + path[i] moves to start + i, in every layer and head.  A thread
+// moves one 16-byte column of a (layer, head)'s rows (or its scales): the
+// columns do not depend on one another, so no barrier is needed, and the rows
+// are looked up once per CTA for all its columns.  (One CTA per layer, request
+// and head, with a barrier between reading and writing, spent its time on the
+// look-ups: 30 us for 26 MB.)  While the path only goes forward, as accepted
+// paths do, no target is a later source, and a thread moves 8 rows at a time;
+// else it reads all rows (64 at most, in local memory) before it writes.
+constexpr int kCompactThreads = 256;
+constexpr int kMoveAtOnce = 8;
+
+template <typename V>
+__device__ __forceinline__ void move_column(char* base, int64_t pitch, const int64_t* from, const int64_t* to,
+                                            int count, bool forward) {
+  if (forward) {
+    for (int i = 0; i < count; i += kMoveAtOnce) {
+      V hold[kMoveAtOnce];
+#pragma unroll
+      for (int j = 0; j < kMoveAtOnce; ++j)
+        if (i + j < count && from[i + j] >= 0) hold[j] = *reinterpret_cast<const V*>(base + from[i + j] * pitch);
+#pragma unroll
+      for (int j = 0; j < kMoveAtOnce; ++j)
+        if (i + j < count && from[i + j] >= 0) *reinterpret_cast<V*>(base + to[i + j] * pitch) = hold[j];
+    }
+  } else {
+    V hold[kMaxNodes];
+    for (int i = 0; i < count; ++i)
+      if (from[i] >= 0) hold[i] = *reinterpret_cast<const V*>(base + from[i] * pitch);
+    for (int i = 0; i < count; ++i)
+      if (from[i] >= 0) *reinterpret_cast<V*>(base + to[i] * pitch) = hold[i];
+  }
+}
 
 __global__ void __launch_bounds__(kCompactThreads)
-    kv_compact_kernel(KvCache cache, int row_bytes, const int32_t* __restrict__ table,
+    kv_compact_kernel(KvCache cache, int row_bytes, int units, const int32_t* __restrict__ table,
                       int64_t table_width, const int32_t* __restrict__ starts,
                       const int32_t* __restrict__ path, int path_width,
                       const int32_t* __restrict__ kept, int* err) {
-  __shared__ int64_t from[kMaxNodes], to[kMaxNodes];   // cache rows of this head, -1: nothing moves
-  const int b = blockIdx.x, head = blockIdx.y;
-  const int64_t layer = blockIdx.z;
+  __shared__ int64_t from[kMaxNodes], to[kMaxNodes];   // rows of layer 0, head 0; -1: nothing moves
+  const int b = blockIdx.y;
   const int n = kept[b];
   if (n <= 0) return;
-  const bool bad_count = n > path_width;
-  const int count = bad_count ? 0 : n;
-  if (bad_count && threadIdx.x == 0) atomicOr(err, kDevErrIndex);
-  if (threadIdx.x < count) {
+  if (n > path_width) {
+    if (threadIdx.x == 0) atomicOr(err, kDevErrIndex);
+    return;
+  }
+  bool forward = true;
+  if (threadIdx.x < n) {
     const int i = threadIdx.x;
-    const int src = path[static_cast<int64_t>(b) * path_width + i];
-    const int64_t f = src < 0 ? -1 : static_cast<int64_t>(starts[b]) + src;
-    const int64_t t = static_cast<int64_t>(starts[b]) + i;
-    const int64_t rf = cache_row_of(cache, table, table_width, b, f, head);
-    const int64_t rt = cache_row_of(cache, table, table_width, b, t, head);
+    const int32_t* p = path + static_cast<int64_t>(b) * path_width + i;
+    const int src = p[0];
+    forward = src >= i && (i == 0 || p[-1] < src);
+    const int64_t start = starts[b];
+    const int64_t rf = src < 0 ? -1 : cache_row_of(cache, table, table_width, b, start + src, 0);
+    const int64_t rt = cache_row_of(cache, table, table_width, b, start + i, 0);
     const bool ok = rf >= 0 && rt >= 0;
     if (!ok) atomicOr(err, kDevErrIndex);
-    const bool moves = ok && rf != rt;
-    from[i] = moves ? rf + layer * cache.layer_rows() : -1;
-    to[i] = moves ? rt + layer * cache.layer_rows() : -1;
+    from[i] = ok && rf != rt ? rf : -1;
+    to[i] = rt;
   }
-  __syncthreads();
-  // 64 rows x 128 bytes x (K, V) = 16 KiB at most: 8 chunks of 16 bytes a thread
-  const int chunks = row_bytes / 16;
-  constexpr int kMost = 2 * kMaxNodes * 8 / kCompactThreads;
-  uint4 hold[kMost];
-  float hs = 0.0f;
-  const int total = 2 * count * chunks;
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    const int c = j * kCompactThreads + threadIdx.x;
-    if (c < total) {
-      const int i = c / (2 * chunks), rest = c % (2 * chunks);
-      if (from[i] >= 0) {
-        const uint8_t* base = rest < chunks ? cache.k : cache.v;
-        hold[j] = *reinterpret_cast<const uint4*>(base + from[i] * row_bytes + (rest % chunks) * 16);
-      }
-    }
+  forward = __syncthreads_and(forward);
+  const int chunks = row_bytes / 16;   // of 16 bytes in a row
+  const int64_t columns = static_cast<int64_t>(units) * 2 * chunks, all = columns + 2 * units;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kCompactThreads + threadIdx.x;
+  if (id >= all) return;
+  const bool scales = id >= columns;
+  const int64_t rest = scales ? id - columns : id;
+  const int width = scales ? 2 : 2 * chunks;
+  const int unit = static_cast<int>(rest / width), column = static_cast<int>(rest - static_cast<int64_t>(unit) * width);
+  const int layer = unit / cache.heads, head = unit - layer * cache.heads;
+  const int64_t row0 = layer * cache.layer_rows() + (static_cast<int64_t>(head) << cache.page_shift);
+  if (scales) {
+    char* base = reinterpret_cast<char*>((column ? cache.v_scale : cache.k_scale) + row0);
+    move_column<float>(base, 4, from, to, n, forward);
+  } else {
+    char* base = reinterpret_cast<char*>((column < chunks ? cache.k : cache.v) + row0 * row_bytes) +
+                 (column < chunks ? column : column - chunks) * 16;
+    move_column<uint4>(base, row_bytes, from, to, n, forward);
   }
-  if (threadIdx.x < 2 * count && from[threadIdx.x >> 1] >= 0)
-    hs = (threadIdx.x & 1 ? cache.v_scale : cache.k_scale)[from[threadIdx.x >> 1]];
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    const int c = j * kCompactThreads + threadIdx.x;
-    if (c < total) {
-      const int i = c / (2 * chunks), rest = c % (2 * chunks);
-      if (to[i] >= 0) {
-        uint8_t* base = rest < chunks ? cache.k : cache.v;
-        *reinterpret_cast<uint4*>(base + to[i] * row_bytes + (rest % chunks) * 16) = hold[j];
-      }
-    }
-  }
-  if (threadIdx.x < 2 * count && to[threadIdx.x >> 1] >= 0)
-    (threadIdx.x & 1 ? cache.v_scale : cache.k_scale)[to[threadIdx.x >> 1]] = hs;
 }
 
 // Calls f(T*, head_dim constant, bits constant) for the run-time choice.
@@ -280,13 +344,13 @@ template <typename T>
 cudaError_t append_typed(const KvCache& c, const void* k, int64_t k_stride, const void* v,
                          int64_t v_stride, const int64_t* slots, int64_t tokens, int* err,
                          cudaStream_t st) {
-  const uint32_t rows = static_cast<uint32_t>(tokens * c.heads);
   return by_format<T>(c, [&](auto d, auto bits) {
-    constexpr int kPerCta = kRowThreads / (decltype(d)::value / 8);
-    kv_append_kernel<T, decltype(d)::value, decltype(bits)::value>
-        <<<(rows + kPerCta - 1) / kPerCta, kRowThreads, 0, st>>>(
-            c, static_cast<const T*>(k), k_stride, static_cast<const T*>(v), v_stride, slots, rows,
-            err);
+    constexpr int kPerCta = 2 * kRowThreads / (decltype(d)::value / 8);
+    const dim3 grid(static_cast<unsigned>(c.heads),
+                    static_cast<unsigned>(std::min<int64_t>((tokens + kPerCta - 1) / kPerCta, 65535)));
+    kv_append_kernel<T, decltype(d)::value, decltype(bits)::value><<<grid, kRowThreads, 0, st>>>(
+        c, static_cast<const T*>(k), k_stride, static_cast<const T*>(v), v_stride, slots,
+        static_cast<int>(tokens), err);
     return cudaGetLastError();
   });
 }
@@ -330,10 +394,16 @@ cudaError_t launch_kv_compact(const KvCache& c, int64_t layers, const int32_t* t
                               int64_t table_width, const int32_t* starts, const int32_t* path,
                               int path_width, const int32_t* kept, int requests, int* err,
                               cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(requests), static_cast<unsigned>(c.heads),
-                  static_cast<unsigned>(layers));
-  kv_compact_kernel<<<grid, kCompactThreads, 0, st>>>(c, c.head_dim * c.bits / 8, table, table_width,
-                                                      starts, path, path_width, kept, err);
+  const int row_bytes = c.head_dim * c.bits / 8;
+  const int64_t units = layers * c.heads;
+  const int64_t ctas = (units * (2 * (row_bytes / 16) + 2) + kCompactThreads - 1) / kCompactThreads;
+  // requests in runs that the grid's second dimension holds
+  for (int b = 0; b < requests; b += 65535) {
+    const int n = std::min(requests - b, 65535);
+    kv_compact_kernel<<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(n)), kCompactThreads, 0, st>>>(
+        c, row_bytes, static_cast<int>(units), table + b * table_width, table_width, starts + b,
+        path + static_cast<int64_t>(b) * path_width, path_width, kept + b, err);
+  }
   return cudaGetLastError();
 }
 
