@@ -33,26 +33,12 @@ namespace {
 constexpr int kRowThreads = 256;
 
 // ------------------------------------------------------------------ append
-// Eight values of a row -> their codes as bytes (INT8: 8 bytes) or packed
-// nibbles (INT4: 4 bytes in x).  FAST: r = RN(1/s) and Markstein's corrected
-// quotient; it needs s normal and far from the ends of the exponent range.
-template <int BITS, bool FAST>
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float r) {
-  constexpr float kTop = BITS == 8 ? 127.0f : 7.0f;
-  uint32_t c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q;
-    if constexpr (FAST) {
-      q = div_rn_by(f[i], s, r);
-    } else {
-      q = fminf(fmaxf(__fdiv_rn(f[i], s), -kTop), kTop);
-    }
-    // 1.5 * 2^23 puts the nearest whole number (ties to even) in the low
-    // mantissa bits: INT8 in two's complement, INT4 plus 8 (an even offset
-    // leaves the ties as they are)
-    c[i] = __float_as_uint(__fadd_rn(q, BITS == 8 ? 12582912.0f : 12582920.0f));
-  }
+// Eight rounded quotients plus 1.5 * 2^23 (the nearest whole number, ties to
+// even, in the low mantissa bits; INT8 in two's complement, INT4 with 8 more, an
+// even offset that leaves the ties as they are) -> codes as bytes (INT8: 8
+// bytes) or packed nibbles (INT4: 4 bytes in x).
+template <int BITS>
+__device__ __forceinline__ uint2 pack8(const uint32_t (&c)[8]) {
   if constexpr (BITS == 8) {
     const uint32_t a = __byte_perm(c[0], c[1], 0x0040u), b = __byte_perm(c[2], c[3], 0x0040u);
     const uint32_t d = __byte_perm(c[4], c[5], 0x0040u), e = __byte_perm(c[6], c[7], 0x0040u);
@@ -66,79 +52,123 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float r) 
     return make_uint2((w - 0x4B400000u * 0x11111111u) ^ 0x88888888u, 0u);
   }
 }
+template <int BITS>
+__device__ __forceinline__ float code_base() {
+  return BITS == 8 ? 12582912.0f : 12582920.0f;
+}
 
-// max |x| over two packed values each.
+// A row whose scale is near an end of the exponent range: plain divisions.
+template <int BITS>
+__device__ __noinline__ uint2 encode8_divide(const float* f, float s) {
+  constexpr float kTop = BITS == 8 ? 127.0f : 7.0f;
+  uint32_t c[8];
+  for (int i = 0; i < 8; ++i)
+    c[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(f[i], s), -kTop), kTop), code_base<BITS>()));
+  return pack8<BITS>(c);
+}
+
+// Eight packed 16-bit values -> fp32; bf16 values are the upper halves.
 template <typename T>
-__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ void spread8(const uint4& in, float (&f)[8]) {
+  if constexpr (std::is_same<T, __half>::value) {
+    widen8<T>(in, f);
+  } else {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+// The larger of two packed pairs without signs.
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
   P x, y;
   memcpy(&x, &a, 4);
   memcpy(&y, &b, 4);
-  x = __hmax2(__habs2(x), __habs2(y));
+  x = __hmax2(x, y);
   memcpy(&a, &x, 4);
   return a;
 }
 
+// Eight values of a row (with those of its D / 8 - 1 neighbours) -> their codes
+// and the row's scale.  Quotients by r = RN(1/s) and Markstein's correction,
+// the scale by the constant's reciprocal likewise; they hold while nothing
+// underflows on the way (fp16 always; bf16 maxima reach 2^-133): else `plain`
+// is set and s is the row's maximum.  r: one Newton step from the approximate reciprocal rounds correctly
+// but for an all-ones mantissa of s, which no s = RN(a / 127) or RN(a / 7) of
+// an 8- or 11-bit a has (a / 127 would have to be within 2^-23 of a power of 2).
 template <typename T, int D, int BITS>
-__device__ __forceinline__ void append_row(const uint4& in, uint8_t* codes, float* scale, int lane,
-                                           bool write) {
+__device__ __forceinline__ uint2 encode_row(const uint4& in, float& s, bool& plain) {
   constexpr int kLanes = D / 8;
-  uint32_t m = amax2<T>(amax2<T>(in.x, in.y), amax2<T>(in.z, in.w));
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = amax2<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float f[8];
-  widen8<T>(make_uint4(m, m, m, m), f);
-  const float a = fmaxf(f[0], f[1]);
   constexpr float kTop = BITS == 8 ? 127.0f : 7.0f;
-  // corrected quotient by the constant's reciprocal while nothing underflows
-  // on the way (fp16 always; bf16 maxima reach 2^-133)
-  const bool fast = a > 1e-28f && a < 1e32f;
-  float s = div_rn_by(a, kTop, 1.0f / kTop);
-  if (!fast) s = a > 0.0f ? __fdiv_rn(a, kTop) : 1.0f;
-  widen8<T>(in, f);
-  const uint2 c = fast ? encode8<BITS, true>(f, s, __frcp_rn(s)) : encode8<BITS, false>(f, s, 0.0f);
-  if (!write) return;
-  if constexpr (BITS == 8)
-    *reinterpret_cast<uint2*>(codes + lane * 8) = c;
-  else
-    *reinterpret_cast<uint32_t*>(codes + lane * 4) = c.x;
-  if (lane == 0) *scale = s;
+  uint32_t m = max2<T>(max2<T>(in.x & 0x7FFF7FFFu, in.y & 0x7FFF7FFFu),
+                       max2<T>(in.z & 0x7FFF7FFFu, in.w & 0x7FFF7FFFu));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max2<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = max2<T>(m, __byte_perm(m, m, 0x1032u));
+  float f[8];
+  spread8<T>(make_uint4(m, m, m, m), f);
+  const float a = f[0];
+  plain = !(a > 1e-28f && a < 1e32f) && a != 0.0f;
+  s = a == 0.0f ? 1.0f : plain ? a : div_rn_by(a, kTop, 1.0f / kTop);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = __fmaf_rn(r, __fmaf_rn(-s, r, 1.0f), r);
+  spread8<T>(in, f);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(__fadd_rn(div_rn_by(f[i], s, r), code_base<BITS>()));
+  return pack8<BITS>(c);
 }
 
-// D / 8 neighbouring threads hold one (token, head) row of K and of V, and the
-// same of a second token.  Blocks of all heads of the same tokens run together.
+// D / 8 neighbouring threads hold one (token, head) row of K and of V.  Blocks
+// of all heads of the same tokens run together.  (Two tokens per thread left
+// room for a third of the warps and took 56 us instead of 38 at 32768 tokens.)
 template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 6)
     kv_append_kernel(KvCache cache, const T* __restrict__ k, int64_t k_stride,
                      const T* __restrict__ v, int64_t v_stride, const int64_t* __restrict__ slots,
-                     int tokens, int* err) {
+                     int tokens, int64_t capacity, int* err) {
   constexpr int kLanes = D / 8, kGroups = kRowThreads / kLanes, kRowBytes = D * BITS / 8;
+  constexpr float kTop = BITS == 8 ? 127.0f : 7.0f;
   const int lane = threadIdx.x % kLanes, head = blockIdx.x;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * (2 * kGroups); t0 < tokens;
-       t0 += static_cast<int64_t>(gridDim.y) * (2 * kGroups)) {
-    uint4 kin[2], vin[2];
-    int64_t slot[2];
+  const int64_t token = (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * kGroups + threadIdx.x / kLanes;
+  uint4 in[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  int64_t slot = -1;
+  if (token < tokens) {
+    in[0] = ld_stream_v4(k + token * k_stride + head * D + lane * 8);
+    in[1] = ld_stream_v4(v + token * v_stride + head * D + lane * 8);
+    slot = slots[token];
+  }
+  const bool inside = slot >= 0 && slot < capacity;
+  if (slot >= 0 && !inside && lane == 0) atomicOr(err, kDevErrIndex);
+  // 16-row blocks of a layer fit 32 bits
+  const int page = static_cast<int>(slot >> cache.page_shift);
+  const int at = static_cast<int>(slot) & ((1 << cache.page_shift) - 1);
+  const int block = ((page * cache.heads + head) << (cache.page_shift - 4)) + (at >> 4);
+  const int64_t row = static_cast<int64_t>(block) * 16 + (at & 15);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t token = t0 + u * kGroups + threadIdx.x / kLanes;
-      kin[u] = vin[u] = make_uint4(0, 0, 0, 0);
-      slot[u] = -1;
-      if (token < tokens) {
-        kin[u] = ld_stream_v4(k + token * k_stride + head * D + lane * 8);
-        vin[u] = ld_stream_v4(v + token * v_stride + head * D + lane * 8);
-        slot[u] = slots[token];
-      }
+  for (int i = 0; i < 2; ++i) {
+    float s;
+    bool plain;
+    uint2 code = encode_row<T, D, BITS>(in[i], s, plain);
+    if (plain) {   // the same for all threads of a row: s is still the row's maximum
+      float f[8];
+      spread8<T>(in[i], f);
+      s = __fdiv_rn(s, kTop);
+      code = encode8_divide<BITS>(f, s);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool inside = slot[u] >= 0 && slot[u] < cache.pages << cache.page_shift;
-      if (slot[u] >= 0 && !inside && lane == 0) atomicOr(err, kDevErrIndex);
-      const int page = inside ? static_cast<int>(slot[u] >> cache.page_shift) : 0;
-      const int at_page = static_cast<int>(slot[u]) & ((1 << cache.page_shift) - 1);
-      // 16-row blocks of a layer fit 32 bits
-      const int64_t at = (static_cast<int64_t>(page * cache.heads + head) << cache.page_shift) + at_page;
-      append_row<T, D, BITS>(kin[u], cache.k + at * kRowBytes, cache.k_scale + at, lane, inside);
-      append_row<T, D, BITS>(vin[u], cache.v + at * kRowBytes, cache.v_scale + at, lane, inside);
+    if (inside) {
+      uint8_t* c = (i == 0 ? cache.k : cache.v) + row * kRowBytes + lane * BITS;
+      if constexpr (BITS == 8)
+        *reinterpret_cast<uint2*>(c) = code;
+      else
+        *reinterpret_cast<uint32_t*>(c) = code.x;
+      if (lane == 0) (i == 0 ? cache.k_scale : cache.v_scale)[row] = s;
     }
   }
 }
@@ -345,12 +375,14 @@ cudaError_t append_typed(const KvCache& c, const void* k, int64_t k_stride, cons
                          int64_t v_stride, const int64_t* slots, int64_t tokens, int* err,
                          cudaStream_t st) {
   return by_format<T>(c, [&](auto d, auto bits) {
-    constexpr int kPerCta = 2 * kRowThreads / (decltype(d)::value / 8);
-    const dim3 grid(static_cast<unsigned>(c.heads),
-                    static_cast<unsigned>(std::min<int64_t>((tokens + kPerCta - 1) / kPerCta, 65535)));
+    constexpr int kPerCta = kRowThreads / (decltype(d)::value / 8);
+    const int64_t blocks = (tokens + kPerCta - 1) / kPerCta;
+    const int64_t y = std::min<int64_t>(blocks, 32768);
+    const dim3 grid(static_cast<unsigned>(c.heads), static_cast<unsigned>(y),
+                    static_cast<unsigned>((blocks + y - 1) / y));
     kv_append_kernel<T, decltype(d)::value, decltype(bits)::value><<<grid, kRowThreads, 0, st>>>(
         c, static_cast<const T*>(k), k_stride, static_cast<const T*>(v), v_stride, slots,
-        static_cast<int>(tokens), err);
+        static_cast<int>(tokens), c.pages << c.page_shift, err);
     return cudaGetLastError();
   });
 }
