@@ -24,15 +24,18 @@ namespace cider {
 namespace {
 
 // Share c begins within a unit and the share before it began the unit: adds the
-// unit's parts in the order of the shares and writes its rows.  One CTA of D
-// threads per (share, row).  The shares' ends follow from the axis' length, so
-// the parts' statistics are loaded side by side; walking from share to share
-// cost a memory round trip each (18 us for 57 parts).
-__global__ void join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
-  extern __shared__ float2 weight[];   // per part: its factor
-  __shared__ float2 red[4];
+// unit's parts in the order of the shares and writes its rows.  One CTA per
+// (share, kJoinRows rows), a warp per row.  The shares' ends follow from the
+// axis' length, so the parts' statistics are loaded side by side; walking from
+// share to share cost a memory round trip each (18 us for 57 parts), and a CTA
+// per row repeated the 64-bit divisions too often (38 us for 152 x 128 rows).
+constexpr int kJoinRows = 16, kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
+  extern __shared__ float weights[];   // per warp and part: its factor
   pdl_wait();
-  const int c = blockIdx.x, row = blockIdx.y, d = threadIdx.x, dim = blockDim.x;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c == 0) return;
   const PartsArgs::Info i = parts.info[c];
   // the share before holds the unit's first tile unless it begins within it too
@@ -41,43 +44,59 @@ __global__ void join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
   const int group = a.q_heads / a.cache.heads;
   const int blocks = Axis::blocks_of(a, r, parts.rows);
   const int head = i.unit / blocks, block = i.unit - head * blocks;
-  const int at = block * parts.rows + row;
-  if (at >= r.nodes * group) return;
+  const int rows = min(parts.rows, r.nodes * group - block * parts.rows);
+  const int first_row = blockIdx.y * kJoinRows;
+  if (first_row >= rows) return;
   // parts: the last slot of the share before, then the first slot of every share that begins before the unit's end
   const int ctas = static_cast<int>(min(i.total, static_cast<int64_t>(gridDim.x)));
   int last = static_cast<int>(min(static_cast<int64_t>(ctas - 1), (i.end * ctas - 1) / i.total));
   while (last + 1 < ctas && i.total * (last + 1) / ctas < i.end) ++last;
   while (last > c && i.total * last / ctas >= i.end) --last;
   const int n = last - c + 2;
-  auto stat_of = [&](int j) { return (2 * static_cast<int64_t>(c - 1 + j) + (j == 0 ? 1 : 0)) * parts.rows + row; };
-  float top = -INFINITY, sum = 0.0f;
-  for (int j = d; j < n; j += dim) {
-    weight[j] = parts.stat[stat_of(j)];
-    top = fmaxf(top, weight[j].x);
-  }
+  float* weight = weights + warp * (static_cast<int>(gridDim.x) + 1);
+  const int64_t slot0 = 2 * static_cast<int64_t>(c - 1);   // part j: slot0 + 2 j, and one more for j = 0
+  for (int row = first_row + warp; row < min(rows, first_row + kJoinRows); row += kJoinWarps) {
+    float top = -INFINITY, sum = 0.0f;
+    for (int j = lane; j < n; j += 32) {
+      const float2 s = parts.stat[(slot0 + 2 * j + (j == 0 ? 1 : 0)) * parts.rows + row];
+      weight[j] = s.x;
+      top = fmaxf(top, s.x);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((d & 31) == 0) red[d >> 5].x = top;
-  __syncthreads();
-  for (int w = 0; w < dim / 32; ++w) top = fmaxf(top, red[w].x);
-  for (int j = d; j < n; j += dim) {
-    const float f = weight[j].x == -INFINITY ? 0.0f : exp2f(weight[j].x - top);
-    sum += weight[j].y * f;
-    weight[j].x = f;
-  }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int j = lane; j < n; j += 32) {
+      const float f = weight[j] == -INFINITY ? 0.0f : exp2f(weight[j] - top);
+      sum += parts.stat[(slot0 + 2 * j + (j == 0 ? 1 : 0)) * parts.rows + row].y * f;
+      weight[j] = f;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((d & 31) == 0) red[d >> 5].y = sum;
-  __syncthreads();
-  sum = 0.0f;
-  for (int w = 0; w < dim / 32; ++w) sum += red[w].y;
-  float o = 0.0f;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    constexpr int kPer = D / 32;
+    float v[kPer] = {};
 #pragma unroll 8
-  for (int j = 0; j < n; ++j) o += parts.out[stat_of(j) * dim + d] * weight[j].x;
-  const float v = sum > 0.0f ? o / sum : 0.0f;
-  const int node = at / group;
-  const int64_t dst = ((r.first + node) * a.q_heads + head * group + at - node * group) * dim + d;
-  static_cast<uint16_t*>(a.out)[dst] = bf16 ? y_bits<true>(v) : y_bits<false>(v);
+    for (int j = 0; j < n; ++j) {
+      const float* src = parts.out + ((slot0 + 2 * j + (j == 0 ? 1 : 0)) * parts.rows + row) * D + lane * kPer;
+      const float f = weight[j];
+      if constexpr (kPer == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] += x.x * f; v[1] += x.y * f; v[2] += x.z * f; v[3] += x.w * f;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] += x.x * f; v[1] += x.y * f;
+      }
+    }
+    const int at = block * parts.rows + row, node = at / group;
+    const int64_t dst = ((r.first + node) * a.q_heads + head * group + at - node * group) * D + lane * kPer;
+    const float scale = sum > 0.0f ? 1.0f / sum : 0.0f;
+    if constexpr (kPer == 4) {
+      store_out4(a.out, bf16, dst, make_float4(v[0], v[1], v[2], v[3]), scale);
+    } else {
+      const uint32_t u = bf16 ? y_bits2<true>(v[0] * scale, v[1] * scale) : y_bits2<false>(v[0] * scale, v[1] * scale);
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + dst) = u;
+    }
+    __syncwarp();   // the weights are written again
+  }
 }
 
 }  // namespace
@@ -85,16 +104,17 @@ __global__ void join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
 cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, int rows, bool bf16,
                         cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(static_cast<unsigned>(a.cache.head_dim));
-  cfg.dynamicSmemBytes = static_cast<size_t>(ctas + 1) * sizeof(float2);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = static_cast<size_t>(ctas + 1) * kJoinWarps * sizeof(float);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, a, parts, bf16);
+  return a.cache.head_dim == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<128>, a, parts, bf16)
+                                 : cudaLaunchKernelEx(&cfg, join_kernel<64>, a, parts, bf16);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
