@@ -29,7 +29,7 @@ namespace {
 // axis' length, so the parts' statistics are loaded side by side; walking from
 // share to share cost a memory round trip each (18 us for 57 parts), and a CTA
 // per row repeated the 64-bit divisions too often (38 us for 152 x 128 rows).
-constexpr int kJoinRows = 16, kJoinWarps = 4;
+constexpr int kJoinRows = 4, kJoinWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
@@ -38,13 +38,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, Par
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c == 0) return;
   const PartsArgs::Info i = parts.info[c];
+  const int64_t before = parts.info[c - 1].begin;
   // the share before holds the unit's first tile unless it begins within it too
-  if (i.begin < 0 || parts.info[c - 1].begin == i.begin) return;
-  const Request r = request_of(a, i.b, false);
+  if (i.begin < 0 || before == i.begin) return;
   const int group = a.q_heads / a.cache.heads;
-  const int blocks = Axis::blocks_of(a, r, parts.rows);
+  const int blocks = Axis::blocks_of(a, i.nodes, parts.rows);
   const int head = i.unit / blocks, block = i.unit - head * blocks;
-  const int rows = min(parts.rows, r.nodes * group - block * parts.rows);
+  const int rows = min(parts.rows, i.nodes * group - block * parts.rows);
   const int first_row = blockIdx.y * kJoinRows;
   if (first_row >= rows) return;
   // parts: the last slot of the share before, then the first slot of every share that begins before the unit's end
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, Par
     __syncwarp();
     constexpr int kPer = D / 32;
     float v[kPer] = {};
-#pragma unroll 8
+#pragma unroll 16
     for (int j = 0; j < n; ++j) {
       const float* src = parts.out + ((slot0 + 2 * j + (j == 0 ? 1 : 0)) * parts.rows + row) * D + lane * kPer;
       const float f = weight[j];
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, Par
       }
     }
     const int at = block * parts.rows + row, node = at / group;
-    const int64_t dst = ((r.first + node) * a.q_heads + head * group + at - node * group) * D + lane * kPer;
+    const int64_t dst = ((i.first + node) * a.q_heads + head * group + at - node * group) * D + lane * kPer;
     const float scale = sum > 0.0f ? 1.0f / sum : 0.0f;
     if constexpr (kPer == 4) {
       store_out4(a.out, bf16, dst, make_float4(v[0], v[1], v[2], v[3]), scale);

@@ -38,8 +38,11 @@ struct Axis {
     return r.nodes == 0 ? 0 : (r.length + tile - 1) / tile;
   }
   // Row blocks per head of a request.
+  __device__ static int blocks_of(const AttendArgs& a, int nodes, int block_rows) {
+    return (nodes * (a.q_heads / a.cache.heads) + block_rows - 1) / block_rows;
+  }
   __device__ static int blocks_of(const AttendArgs& a, const Request& r, int block_rows) {
-    return (r.nodes * (a.q_heads / a.cache.heads) + block_rows - 1) / block_rows;
+    return blocks_of(a, r.nodes, block_rows);
   }
   // Called by whole warps; block_rows: query rows of a unit at most.
   __device__ void begin(const AttendArgs& a, int tile, int lane, int block_rows) {
@@ -119,10 +122,11 @@ struct PartsArgs {
   float* out;       // [2 ctas][rows][D]
   float2* stat;     // [2 ctas][rows]: maximum (log2), sum
   // Of a share that begins within a unit: the unit's first and end tile on the
-  // axis, the axis' length, the request and the unit; else begin is -1.
+  // axis, the axis' length, the unit, and its request's first row and number of
+  // new tokens; else begin is -1.
   struct Info {
-    int64_t begin, end, total;
-    int b, unit;
+    int64_t begin, end, total, first;
+    int unit, nodes;
   };
   Info* info;       // [ctas]
   int rows;
@@ -141,8 +145,9 @@ struct PartsArgs {
   }
   __device__ void announce(const Axis& x) const {
     const bool mid = x.more() && x.continued;
-    info[blockIdx.x] = mid ? Info{x.unit_begin, x.unit_begin + x.unit_tiles, x.total, x.b, x.unit}
-                           : Info{-1, -1, 1, 0, 0};
+    info[blockIdx.x] = mid ? Info{x.unit_begin, x.unit_begin + x.unit_tiles, x.total, x.req.first, x.unit,
+                                  x.req.nodes}
+                           : Info{-1, -1, 1, 0, 0, 0};
   }
   __device__ void store(int slot, int row, int d_all, int d, const float4& v, float top,
                         float sum) const {

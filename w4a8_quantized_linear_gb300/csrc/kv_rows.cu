@@ -73,7 +73,7 @@ struct RowsCfg {
   static constexpr int kMaskBytes = kRows * 8;
   static constexpr int kScaleBytes = kWarps * kSub * 16;
   static constexpr int kRest = kQBytes + kOutBytes + kStatBytes + kMaskBytes + kScaleBytes;
-  static constexpr int kCtas = NB == 1 ? (D == 128 ? 3 : 4) : 2;   // per SM
+  static constexpr int kCtas = NB == 1 ? 3 : 2;   // per SM
   // as many stages as the resident CTAs' shared memory holds, at most 6
   static constexpr int kFit = (227 * 1024 / kCtas - 1024 - kRest) / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -166,23 +166,37 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t u) {
 // 2^15 and takes 128 2^-9 off, exactly (INT4 codes four bits up: 2^11).  Each
 // mask is then a single-constant operation: with the codes put under the
 // exponent of 1024 instead, a third of this loop was moves of constants.
+// (x & MASK) ^ flip in one operation.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t flip) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "n"(MASK), "r"(flip));
+  return r;
+}
+// A constant that is kept in a register: as a literal, beside the mask's, each
+// use of it would be a move and an operation.
+__device__ __forceinline__ uint32_t in_register(uint32_t c) {
+  asm volatile("" : "+r"(c));
+  return c;
+}
 template <int BITS>
-__device__ __forceinline__ void value_pairs(uint32_t wa, uint32_t wb, uint32_t* out) {
+__device__ __forceinline__ void value_pairs(uint32_t wa, uint32_t wb, uint32_t flip_lo, uint32_t flip_hi,
+                                            uint32_t* out) {
   const __half2 lift = bits_h2(0x78007800u);      // 2^15
   const __half2 lift_hi = bits_h2(0x68006800u);   // 2^11
   const __half2 off = bits_h2(BITS == 8 ? 0xB400B400u : 0xA400A400u);   // -128 2^-9, -8 2^-9
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const uint32_t x = __byte_perm(wa, wb, half == 0 ? 0x5410u : 0x7632u) ^ (BITS == 8 ? 0x80808080u : 0x88888888u);
+    const uint32_t x = __byte_perm(wa, wb, half == 0 ? 0x5410u : 0x7632u);
     const uint32_t y = x >> 8;
     if constexpr (BITS == 8) {
-      out[2 * half] = h2_bits(__hfma2(bits_h2(x & 0x00FF00FFu), lift, off));
-      out[2 * half + 1] = h2_bits(__hfma2(bits_h2(y & 0x00FF00FFu), lift, off));
+      out[2 * half] = h2_bits(__hfma2(bits_h2(pick<0x00FF00FFu>(x, flip_hi)), lift, off));
+      out[2 * half + 1] = h2_bits(__hfma2(bits_h2(pick<0x00FF00FFu>(y, flip_hi)), lift, off));
     } else {
-      out[4 * half] = h2_bits(__hfma2(bits_h2(x & 0x000F000Fu), lift, off));
-      out[4 * half + 1] = h2_bits(__hfma2(bits_h2(x & 0x00F000F0u), lift_hi, off));
-      out[4 * half + 2] = h2_bits(__hfma2(bits_h2(y & 0x000F000Fu), lift, off));
-      out[4 * half + 3] = h2_bits(__hfma2(bits_h2(y & 0x00F000F0u), lift_hi, off));
+      out[4 * half] = h2_bits(__hfma2(bits_h2(pick<0x000F000Fu>(x, flip_lo)), lift, off));
+      out[4 * half + 1] = h2_bits(__hfma2(bits_h2(pick<0x00F000F0u>(x, flip_hi)), lift_hi, off));
+      out[4 * half + 2] = h2_bits(__hfma2(bits_h2(pick<0x000F000Fu>(y, flip_lo)), lift, off));
+      out[4 * half + 3] = h2_bits(__hfma2(bits_h2(pick<0x00F000F0u>(y, flip_hi)), lift_hi, off));
     }
   }
 }
@@ -264,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
   uint64_t* mask_smem = reinterpret_cast<uint64_t*>(rest + C::kScaleBytes + C::kQBytes +
                                                     C::kOutBytes + C::kStatBytes);
   const int group = a.q_heads / a.cache.heads;
+  // two's complement to offset codes, of nibbles in place and four bits up (or bytes)
+  const uint32_t flip_lo = in_register(0x00080008u), flip_hi = in_register(0x00800080u);
 
   Axis axis;
   axis.begin(a, C::kTile, lane, C::kRows);
@@ -336,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
     return static_cast<const uint16_t*>(a.q) + (axis.req.first + node) * a.q_stride +
            static_cast<int64_t>(axis.unit * group + (have ? r - node * group : 0)) * D;
   };
-  uint4 q_raw[C::kQInRegs ? D / 32 : 1];   // a single block of rows is loaded ahead too
+  uint4 q_raw[NB == 1 ? D / 32 : 1];   // a single block of rows is loaded ahead too
   auto start = [&]() {   // the loads of the axis' current piece
     const int64_t begin = axis.piece_begin * C::kTile + warp * C::kSub;
     const int64_t end = min(axis.piece_end * C::kTile, axis.req.length);
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
     table = a.table + axis.b * a.table_width;
     load_slot = 0;
     rows32 = load_rows16(lane);
-    if constexpr (C::kQInRegs) query_load<D, BITS>(q_row(g, g < axis.req.nodes * group), g < axis.req.nodes * group, t, q_raw);
+    if constexpr (NB == 1) query_load<D, BITS>(q_row(g, g < axis.req.nodes * group), g < axis.req.nodes * group, t, q_raw);
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) copy(s);
   };
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
       const int r = nb * 8 + g;
       uint4 w[D / 32];
       float f[D / 4];
-      if constexpr (C::kQInRegs) {
+      if constexpr (NB == 1) {
         query_values<D>(bf16, q_raw, f);
       } else {
         query_load<D, BITS>(q_row(r, r < rows), r < rows, t, w);
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
       const int r = nb * 8 + g;
       uint4 w[D / 32];
       float f[D / 4];
-      if constexpr (C::kQInRegs) {
+      if constexpr (NB == 1) {
         query_values<D>(bf16, q_raw, f);
       } else {
         query_load<D, BITS>(q_row(r, r < rows), r < rows, t, w);
@@ -479,10 +495,9 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
                   f[u][h] = v & 0x00FF00FFu;
                   f[u][h + 2] = __byte_perm(v, 0u, 0x4341u);
                 } else {
-                  const uint32_t x8 = w[u][h][i] ^ 0x88888888u;
-                  const uint32_t v = e ? x8 >> 8 : x8;
-                  f[u][h] = v & 0x000F000Fu;
-                  f[u][h + 2] = v & 0x00F000F0u;
+                  const uint32_t v = e ? w[u][h][i] >> 8 : w[u][h][i];
+                  f[u][h] = pick<0x000F000Fu>(v, flip_lo);
+                  f[u][h + 2] = pick<0x00F000F0u>(v, flip_hi);
                 }
               }
 #pragma unroll
@@ -602,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
 #pragma unroll
         for (int i = 0; i < kBytes / 4; ++i) {
           uint32_t lo[kCodes], hi[kCodes];
-          value_pairs<BITS>(w[0][i], w[1][i], lo);
-          value_pairs<BITS>(w[2][i], w[3][i], hi);
+          value_pairs<BITS>(w[0][i], w[1][i], flip_lo, flip_hi, lo);
+          value_pairs<BITS>(w[2][i], w[3][i], flip_lo, flip_hi, hi);
 #pragma unroll
           for (int j = 0; j < kCodes / 2; ++j) {
             const uint32_t f[4] = {lo[2 * j], lo[2 * j + 1], hi[2 * j], hi[2 * j + 1]};

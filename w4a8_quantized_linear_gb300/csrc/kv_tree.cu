@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* lift_max = reinterpret_cast<float*>(smem + C::kBarOffset + kBars * 8 + 16);   // 16 warps
   auto bar = [&](int i) { return sbase + C::kBarOffset + i * 8; };
   auto wait = [&](int i, uint32_t parity) {
-    return mbar_wait_bounded(bar(i), parity & 1, abort_flag, a.err, kWaitNs);
+    return mbar_sleep_bounded(bar(i), parity & 1, abort_flag, a.err, kWaitNs);
   };
 
   if (warp == 0) {
