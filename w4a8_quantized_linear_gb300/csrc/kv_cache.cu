@@ -127,9 +127,9 @@ __device__ __forceinline__ uint2 encode_row(const uint4& in, float& s, bool& pla
 
 // D / 8 neighbouring threads hold one (token, head) row of K and of V.  Blocks
 // of all heads of the same tokens run together.  (Two tokens per thread left
-// room for a third of the warps and took 56 us instead of 38 at 32768 tokens.)
+// room for a third of the warps and took 56 us instead of 40 at 32768 tokens INT4.)
 template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(kRowThreads, 6)
+__global__ void __launch_bounds__(kRowThreads, 8)
     kv_append_kernel(KvCache cache, const T* __restrict__ k, int64_t k_stride,
                      const T* __restrict__ v, int64_t v_stride, const int64_t* __restrict__ slots,
                      int tokens, int64_t capacity, int* err) {
