@@ -125,6 +125,18 @@ def test_head_layouts_of_trees(hq, heads, dim, bits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("nodes", [2, 3, 4, 5, 6, 7, 8, 9])
+def test_every_number_of_rows(nodes, bits, dim):
+    """8 .. 36 query rows per key/value head: each form of the kernels for few
+    rows, full and not, and the change to the one for many."""
+    cider = require_gpu()
+    rng = np.random.default_rng(nodes)
+    run(cider, rng, [300, 41, 1000], [nodes, 1, nodes], 8, 2, dim, 16, bits, "bf16")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bits,dtype", [(8, "fp16"), (4, "bf16")])
 @pytest.mark.parametrize("nodes", [1, 3, 40])
 def test_long_axis_and_many_requests(bits, dtype, nodes):

@@ -117,9 +117,15 @@ cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, i
                                  : cudaLaunchKernelEx(&cfg, join_kernel<64>, a, parts, bf16);
 }
 
+// By the query rows of a key/value head (new tokens x grouped heads).  At 32
+// requests of 4096 .. 16384 positions the many-row kernel takes the same time
+// for 1 to 128 rows, the other one grows with them: up to 32 rows (64 requests
+// of up to 8192, INT8: 229 us against 304) it is ahead.
+constexpr int kFewRows = 32;
+
 cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {
-  return a.max_nodes * (a.q_heads / a.cache.heads) <= 16 ? launch_attend_rows(a, bf16, num_sms, st)
-                                                         : launch_attend_tree(a, bf16, num_sms, st);
+  return a.max_nodes * (a.q_heads / a.cache.heads) <= kFewRows ? launch_attend_rows(a, bf16, num_sms, st)
+                                                               : launch_attend_tree(a, bf16, num_sms, st);
 }
 
 }  // namespace cider

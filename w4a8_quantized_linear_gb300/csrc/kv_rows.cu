@@ -736,6 +736,7 @@ template <int D, int BITS>
 cudaError_t by_rows(const AttendArgs& a, bool bf16, int rows, int num_sms, cudaStream_t st) {
   if (rows <= 8) return launch_rows<D, BITS, 1>(a, bf16, num_sms, st);
   if (rows <= 16) return launch_rows<D, BITS, 2>(a, bf16, num_sms, st);
+  if (rows <= 24) return launch_rows<D, BITS, 3>(a, bf16, num_sms, st);
   return launch_rows<D, BITS, 4>(a, bf16, num_sms, st);
 }
 

@@ -274,6 +274,19 @@ __device__ __forceinline__ uint4 convert_unit(const uint4& c, int h) {
   return r;
 }
 
+// One lane of a converged warp, the same one each time.  The compiler knows the
+// pattern: behind a comparison of the lane number it elects a lane again for
+// every MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // The MMAs of a tile in stage ST: S = Q K^T, and O (+)= P V.
 template <typename C, int ST>
 __device__ __forceinline__ void issue_s(uint32_t sbase) {
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kKFull + st, ph) && ok;
           ok = wait(kVEmpty + st, ph + 1) && ok;   // P(n - 2), in the same columns, is read
           tc_fence_after();
-          if (lane == 0 && ok) {
+          if (__all_sync(0xffffffffu, ok) && elect_one()) {
             // a constant stage keeps every operand a constant or uniform
             if (st == 0) issue_s<C, 0>(sbase); else issue_s<C, 1>(sbase);
             tc_commit(bar(kSFull + st));
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kVFull + st, ph) && ok;
           ok = wait(kPReady + st, ph) && ok;
           tc_fence_after();
-          if (lane == 0 && ok) {
+          if (__all_sync(0xffffffffu, ok) && elect_one()) {
             if (st == 0) issue_o<C, D, 0>(sbase, i > 0); else issue_o<C, D, 1>(sbase, i > 0);
             tc_commit(bar(kVEmpty + st));
             if (i == tiles - 1) tc_commit(bar(kOFull));
@@ -473,15 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           slot = slot + 2 >= C::kSlots ? slot + 2 - C::kSlots : slot + 2;
         }
       }
-      // no copy may be in flight when the CTA ends, also after an abort
-      volatile uint32_t keep_waiting = 0u;
-      const uint32_t end = side, begin = v ? 1u : 0u;
-      for (uint32_t j = end > C::kSlots + begin ? end - (C::kSlots & ~1u) : begin; j < end; j += 2)
-        mbar_wait_bounded(bar(kRawFull + j % C::kSlots), j / C::kSlots & 1, &keep_waiting, a.err, kWaitNs);
+      // the converters wait for every copy before the CTA ends; after a wait that
+      // gave up they may not have: what is in flight lands within microseconds
+      if (*abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000u) __nanosleep(1000);
+      }
     }
     // no MMA may be in flight when the tensor memory is freed, also after an abort
     if (warp < 2) {
-      if (lane == 0) {
+      if (elect_one()) {
         tc_commit(bar(kDone + warp));
         volatile uint32_t keep_waiting = 0u;
         mbar_wait_bounded(bar(kDone + warp), 0, &keep_waiting, a.err, kWaitNs);
