@@ -334,8 +334,9 @@ cider_status_t cider_kv_compact(const cider_kv_cache_t* cache, const int32_t* ta
  *   out      [tokens, q_heads, D] of dtype.  A token that sees no position gets
  *            zeros; rows of a request whose offsets or length contradict the
  *            call's sizes are not written.
- * Products and sums are fp32; the weights of the values are rounded to fp16 with
- * their sum taken before; the result is rounded once to dtype.  Scratch for the
+ * Products and sums are fp32; the weights of the values are rounded to fp16, their
+ * sum is taken before that; the result is rounded once to dtype.  Value scales
+ * below 2^-90 count as 2^-90.  The same call gives the same bits.  Scratch for the
  * joined parts of long requests comes from the library's pool. */
 cider_status_t cider_tree_attention(const cider_kv_cache_t* cache, int64_t layer, const void* q,
                                     int64_t q_stride, int dtype, int64_t tokens, int64_t q_heads,

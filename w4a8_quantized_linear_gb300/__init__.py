@@ -328,7 +328,8 @@ def cider_w4a8_accumulators(qa, qw_packed, group_size: int = 0):
 
 def cider_check_device_error(device=None) -> int:
     """Synchronize the current stream and return (and clear) the status of
-    the library's device error word: 0 (CIDER_OK) or 5 (CIDER_ERR_TIMEOUT)."""
+    the library's device error word: 0 (CIDER_OK), 5 (CIDER_ERR_TIMEOUT) or 6
+    (CIDER_ERR_INDEX: a page, slot, offset, count or token was out of range)."""
     s = torch.cuda.current_stream(device)
     return int(_load().cider_check_device_error(ctypes.c_void_p(s.cuda_stream)))
 

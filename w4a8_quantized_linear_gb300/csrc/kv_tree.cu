@@ -15,8 +15,17 @@
 // bandwidth; with Q and P in tensor memory it is half.
 //
 // Bound: HBM for INT8 up to 128 rows in theory (a tile is 33 KiB: ~1400 cycles
-// of an SM's share of HBM against 1024 of tensor work), the issue of the
-// conversion and softmax instructions in practice.
+// of an SM's share of HBM against 1024 of tensor work); in practice the softmax
+// of a tile (~1600 cycles with four warps per scheduler, ~6 a warp's
+// instruction) and the steps around it (waits, agreement, P's store, the issue
+// of eight MMAs at ~110 cycles each) follow one another, ~3700 cycles a tile.
+// 32 requests of 4096 .. 16384 positions, 16 .. 32 new tokens, 32 / 8 heads of
+// 128, INT8: 289 us (2.5 TB/s of codes, 488 TFLOP/s), whatever the number of
+// rows up to 128.  Measured and not kept: two groups of softmax warps on
+// alternate tiles, each with an S and an O of its own and Q in shared memory
+// (316 us: two warps per scheduler at a time leave the latencies open), the same
+// with one warp per quarter and tile (392 us), eight softmax warps of 64
+// positions each (318 us).
 //
 // Roles (896 threads, one CTA per SM, persistent over its share of the axis):
 //   warps 0, 1    one thread each issues the MMAs of S and of O

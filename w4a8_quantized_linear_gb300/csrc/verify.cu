@@ -20,12 +20,16 @@
 // HBM (again from L2 where a residual or the draw needs them), and the noise of
 // the one draw.  The walk is serial, so what bounds it is latency: a cluster of
 // up to 8 CTAs shares a request's vocabulary, each visited node costs one pass
-// over a CTA's share (softmax maximum and sum in one pass, 4 x 16 bytes per
-// lane in flight) and one exchange between the CTAs through distributed shared
-// memory; the noise, and the row of the child that is asked first, are
-// prefetched to L2 meanwhile.  Every CTA adds the shares' results in the order
-// of their ranks, so all take the same decisions and the same inputs give the
-// same path.  Sums and softmax statistics are fp32.
+// over a CTA's share (softmax maximum and sum in one pass, 8 x 16 bytes per
+// lane in flight; ~3500 cycles for 16000 tokens, most of it the loads' latency)
+// and one exchange between the CTAs through distributed shared memory (~2000
+// cycles with the wait for the slowest warp; 3000 by cluster barriers); the
+// noise, and the row of the child that is asked first, are prefetched to L2
+// meanwhile.  Measured: 48 trees of 16 .. 32 nodes over 128000 tokens 31 us (the
+// longest path has 8 nodes), two chains of 4 drafts over 32003 tokens 19 us.
+// Every CTA adds the shares' results in the order of their ranks, so all take the
+// same decisions and the same inputs give the same path.  Sums and softmax
+// statistics are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
