@@ -527,6 +527,9 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
     shape = (tokens, heads, dim) if layer is not None else (layers, tokens, heads, dim)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be float16 or bfloat16")
+    # the C entry reads -1 as all layers, for which `shape` has no room
+    if layer is not None and layer < 0:
+        raise ValueError(f"layer must be None (all layers) or at least 0, got {layer}")
     if out is None:
         # zeros where no request reads: nothing is launched for an empty problem
         make = torch.empty if n and cache[0].shape[1] else torch.zeros
