@@ -449,6 +449,20 @@ cider_status_t cider_check_device_error(void* stream);
  * cider_check_device_error. */
 cider_status_t cider_debug_wait_timeout(int64_t max_polls, void* stream);
 
+/* The same for the waits of cider_verify_drafts, whose CTAs exchange results: as
+ * that call, with a limit of wait_us (1 .. 100000) microseconds per wait, and CTA
+ * `silent` of each request sending nothing (-1, or beyond the CTAs in use: all
+ * send).  A request whose wait gave up has count 0, next -1 and a path of -1;
+ * cider_check_device_error reports CIDER_ERR_TIMEOUT. */
+cider_status_t cider_debug_verify_timeout(const void* logits, int64_t logits_stride, int dtype,
+                                          const int32_t* tokens, const int32_t* parents,
+                                          const int32_t* offsets, int64_t requests, int64_t nodes,
+                                          int64_t vocab, int64_t max_nodes, const float* uniforms,
+                                          const float* noise, const float* draft,
+                                          const float* temperature, int32_t* count, int32_t* path,
+                                          int32_t* next, int64_t wait_us, int32_t silent,
+                                          void* stream);
+
 /* K split of the small-M path (M <= 16), for inspection and the benchmark's
  * launch count: pure host arithmetic, no GPU needed.  For a linear with y
  * output on a GPU with num_sms SMs, writes the number of K slices the

@@ -81,6 +81,8 @@ def _declare(lib):
                                   ctypes.c_float, p, p], i32),
         "cider_verify_drafts": ([p, i64, i32, p, p, p, i64, i64, i64, i64, p, p, p, p, p, p, p, p],
                                 i32),
+        "cider_debug_verify_timeout": ([p, i64, i32, p, p, p, i64, i64, i64, i64, p, p, p, p, p, p, p,
+                                        i64, ctypes.c_int32, p], i32),
         "cider_debug_small_m_launch": ([i64, i64, i64, i32, i32, i32, i32, p], i32),
     }
     for name, (args, res) in sig.items():

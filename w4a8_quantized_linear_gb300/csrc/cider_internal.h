@@ -164,7 +164,8 @@ cudaError_t launch_verify(const void* logits, int64_t logits_stride, bool bf16,
                           int requests, int64_t nodes, int vocab, int max_nodes,
                           const float* uniforms, const float* noise, const float* draft,
                           const float* temperature, int32_t* count, int32_t* path, int32_t* next,
-                          int* err, int num_sms, cudaStream_t st);
+                          int* err, int num_sms, cudaStream_t st,
+                          uint64_t wait_ns = kKernelWaitTimeoutNs, int silent = -1);
 
 // ---------------------------------------------------------------- cider_api.cu
 // One linear / accumulator call, as the C entry points receive it.

@@ -76,6 +76,39 @@ cider_status_t device(int** err, int* num_sms) {
   return cuda_status(cider::device_error_word(err));
 }
 
+// A verification whose waits between CTAs end after wait_ns; rank `silent` of
+// each cluster sends nothing (-1: all send).
+cider_status_t verify(const void* logits, int64_t logits_stride, int dtype,
+                      const int32_t* tokens, const int32_t* parents,
+                      const int32_t* offsets, int64_t requests, int64_t nodes,
+                      int64_t vocab, int64_t max_nodes, const float* uniforms,
+                      const float* noise, const float* draft,
+                      const float* temperature, int32_t* count, int32_t* path,
+                      int32_t* next, void* stream, uint64_t wait_ns, int silent) {
+  return guarded([&]() -> cider_status_t {
+    if (requests == 0) return CIDER_OK;
+    // without a single node there is nothing behind the nodes' pointers
+    if ((nodes != 0 && (!logits || !tokens || !parents || !uniforms)) || !offsets || !noise ||
+        !count || !path || !next || !valid_dtype(dtype) || requests < 0 || requests > kMaxDim || nodes < 0 ||
+        nodes > kMaxDim || vocab < 1 || vocab > kMaxDim || max_nodes < 1 ||
+        max_nodes > cider::kMaxNodes || logits_stride < vocab)
+      return CIDER_ERR_INVALID_ARGUMENT;
+    if (!aligned(logits, 2) || !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(offsets, 4) ||
+        !aligned(uniforms, 4) || !aligned(noise, 4) || !aligned(draft, 4) ||
+        !aligned(temperature, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(next, 4))
+      return CIDER_ERR_MISALIGNED;
+    int* err = nullptr;
+    int sms = 0;
+    cider_status_t s = device(&err, &sms);
+    if (s != CIDER_OK) return s;
+    return cuda_status(cider::launch_verify(
+        logits, logits_stride, dtype == CIDER_BF16, tokens, parents, offsets,
+        static_cast<int>(requests), nodes, static_cast<int>(vocab), static_cast<int>(max_nodes),
+        uniforms, noise, draft, temperature, count, path, next, err, sms,
+        static_cast<cudaStream_t>(stream), wait_ns, silent));
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -206,28 +239,23 @@ cider_status_t cider_verify_drafts(const void* logits, int64_t logits_stride, in
                                    const float* noise, const float* draft,
                                    const float* temperature, int32_t* count, int32_t* path,
                                    int32_t* next, void* stream) {
-  return guarded([&]() -> cider_status_t {
-    if (requests == 0) return CIDER_OK;
-    // without a single node there is nothing behind the nodes' pointers
-    if ((nodes != 0 && (!logits || !tokens || !parents || !uniforms)) || !offsets || !noise ||
-        !count || !path || !next || !valid_dtype(dtype) || requests < 0 || requests > kMaxDim || nodes < 0 ||
-        nodes > kMaxDim || vocab < 1 || vocab > kMaxDim || max_nodes < 1 ||
-        max_nodes > cider::kMaxNodes || logits_stride < vocab)
-      return CIDER_ERR_INVALID_ARGUMENT;
-    if (!aligned(logits, 2) || !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(offsets, 4) ||
-        !aligned(uniforms, 4) || !aligned(noise, 4) || !aligned(draft, 4) ||
-        !aligned(temperature, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(next, 4))
-      return CIDER_ERR_MISALIGNED;
-    int* err = nullptr;
-    int sms = 0;
-    cider_status_t s = device(&err, &sms);
-    if (s != CIDER_OK) return s;
-    return cuda_status(cider::launch_verify(
-        logits, logits_stride, dtype == CIDER_BF16, tokens, parents, offsets,
-        static_cast<int>(requests), nodes, static_cast<int>(vocab), static_cast<int>(max_nodes),
-        uniforms, noise, draft, temperature, count, path, next, err, sms,
-        static_cast<cudaStream_t>(stream)));
-  });
+  return verify(logits, logits_stride, dtype, tokens, parents, offsets, requests, nodes, vocab,
+                max_nodes, uniforms, noise, draft, temperature, count, path, next, stream,
+                cider::kKernelWaitTimeoutNs, -1);
+}
+
+cider_status_t cider_debug_verify_timeout(const void* logits, int64_t logits_stride, int dtype,
+                                          const int32_t* tokens, const int32_t* parents,
+                                          const int32_t* offsets, int64_t requests, int64_t nodes,
+                                          int64_t vocab, int64_t max_nodes, const float* uniforms,
+                                          const float* noise, const float* draft,
+                                          const float* temperature, int32_t* count, int32_t* path,
+                                          int32_t* next, int64_t wait_us, int32_t silent,
+                                          void* stream) {
+  if (wait_us < 1 || wait_us > 100000 || silent < -1) return CIDER_ERR_INVALID_ARGUMENT;
+  return verify(logits, logits_stride, dtype, tokens, parents, offsets, requests, nodes, vocab,
+                max_nodes, uniforms, noise, draft, temperature, count, path, next, stream,
+                static_cast<uint64_t>(wait_us) * 1000, silent);
 }
 
 }  // extern "C"

@@ -61,6 +61,8 @@ struct VerifyArgs {
   const float *uniforms, *noise, *draft, *temperature;
   int32_t *count, *path, *next;
   int* err;
+  uint64_t wait_ns;   // limit of a wait for the other ranks
+  int silent;         // this rank sends nothing (-1: all send); for tests of that limit
 };
 
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
@@ -130,12 +132,16 @@ __device__ __forceinline__ Found join_lanes(Found v, float c) {
   return v;
 }
 
-// The cluster's result from each thread's: all threads of all its CTAs get the
-// same, by the same additions.  Every second exchange uses the same buffers: a
-// rank sends for the one after the next only when it has this CTA's results of
-// the next, which are sent when all threads here have read the present ones.
-__device__ __forceinline__ Found exchange(Found v, float c, Shared& sh, int ranks, int rank, uint32_t& count,
-                                          int* err) {
+// The cluster's result from each thread's, into v: all threads of all its CTAs
+// get the same, by the same additions.  Every second exchange uses the same
+// buffers: a rank sends for the one after the next only when it has this CTA's
+// results of the next, which are sent when all threads here have read the
+// present ones.  False, for all threads of a CTA alike, when the wait for the
+// other ranks gave up: v is then worth nothing, and the CTA has to leave
+// (nothing more may be expected of a barrier whose phase is open, and threads
+// that went on with different results could wait at different barriers).
+__device__ __forceinline__ bool exchange(Found& v, float c, Shared& sh, int ranks, int rank, uint32_t& count,
+                                         const VerifyArgs& a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t parity = count & 1, phase = count >> 1 & 1;
   v = join_lanes<32>(v, c);
@@ -146,17 +152,18 @@ __device__ __forceinline__ Found exchange(Found v, float c, Shared& sh, int rank
     volatile uint32_t* abort_flag = &sh.abort;
     const uint32_t bar = smem_u32(&sh.bar[parity]);
     if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, ranks * 16u);
-    if (threadIdx.x < ranks && !*abort_flag)
+    if (threadIdx.x < ranks && rank != a.silent)
       st_async_v4(mapa_shared(smem_u32(&sh.cta[parity][rank]), threadIdx.x), __float_as_uint(v.top),
                   __float_as_uint(v.sum), static_cast<uint32_t>(v.best), static_cast<uint32_t>(v.best >> 32),
                   mapa_shared(bar, threadIdx.x));
-    mbar_wait_bounded(bar, phase, abort_flag, err, kKernelWaitTimeoutNs);
+    const bool here = mbar_wait_bounded(bar, phase, abort_flag, a.err, a.wait_ns);
+    if (!__syncthreads_and(here)) return false;
     v = Found{sh.cta[parity][0].top, 0.0f, 0};   // of a rank that is not there
     if ((lane & (kMaxCluster - 1)) < ranks) v = sh.cta[parity][lane & (kMaxCluster - 1)];
     v = join_lanes<kMaxCluster>(v, c);
   }
   ++count;
-  return v;
+  return true;
 }
 
 // r(x) of sampled drafts after the node's rejected children so far; q: the
@@ -299,6 +306,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
   if (threadIdx.x == 0 && !greedy && x0 < x1) prefetch_range(noise + x0, noise + x1);
   int now = 0, count = 1;
   uint32_t exchanges = 0;
+  bool lost = false;   // a wait for the other ranks gave up
   for (;;) {
     const T* row = logits + (first + now) * a.logits_stride;
     const float* q = a.draft ? a.draft + (first + now) * a.vocab : nullptr;
@@ -361,7 +369,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     }
     if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     started = true;
-    v = exchange(v, c, sh, ranks, rank, exchanges, a.err);
+    lost = !exchange(v, c, sh, ranks, rank, exchanges, a);
+    if (lost) break;
     // an all -inf row has no maximum of its own: its first token stands for it
     const int hot = v.best ? static_cast<int>(best_index(v.best)) : 0;
     const float top = v.top;
@@ -421,7 +430,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
           if (token_of<VEC>(k, lane, j) < a.vocab)
             rest.sum += residual(prob(f[j]), g[j], token_of<VEC>(k, lane, j), sh.rejected, rejected);
       }
-      rest = exchange(rest, 0.0f, sh, ranks, rank, exchanges, a.err);
+      lost = !exchange(rest, 0.0f, sh, ranks, rank, exchanges, a);
+      if (lost) break;
       drawn -= qx;
       if (rest.sum == 0.0f) {
         if (threadIdx.x == 0) sh.rejected[rejected - 1].keeps = 1;
@@ -430,6 +440,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         mass = rest.sum;
       }
     }
+    if (lost) break;
     if (accepted >= 0) {
       if (rank == 0 && threadIdx.x == 0) a.path[static_cast<int64_t>(b) * a.max_nodes + count] = accepted;
       ++count;
@@ -483,8 +494,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
           }
         }
       }
-      const uint64_t mine = high < 0.0f ? 0 : pack_best(high, at);
-      next = static_cast<int>(best_index(exchange(Found{0.0f, 0.0f, mine}, 0.0f, sh, ranks, rank, exchanges, a.err).best));
+      Found drawn_token{0.0f, 0.0f, high < 0.0f ? 0 : pack_best(high, at)};
+      lost = !exchange(drawn_token, 0.0f, sh, ranks, rank, exchanges, a);
+      if (lost) break;
+      next = static_cast<int>(best_index(drawn_token.best));
     }
     if (rank == 0 && threadIdx.x == 0) {
       a.count[b] = count;
@@ -492,8 +505,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     }
     break;
   }
-  // after a wait that gave up a CTA may still be sent something
-  if (ranks > 1 && __syncthreads_or(sh.abort)) cluster_sync_all();
+  if (lost) {
+    // no walk to speak of: as a request without nodes
+    if (rank == 0) {
+      for (int i = threadIdx.x; i < a.max_nodes; i += kVerifyThreads)
+        a.path[static_cast<int64_t>(b) * a.max_nodes + i] = -1;
+      if (threadIdx.x == 0) {
+        a.count[b] = 0;
+        a.next[b] = -1;
+      }
+    }
+    // The others may still send to this CTA: until they have given up too or
+    // are through (each of their waits has its limit), and for as long as what
+    // they sent last is on its way, microseconds.
+    cluster_sync_all();
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000u) __nanosleep(1000);
+  }
 }
 
 template <typename T, bool VEC>
@@ -525,10 +553,10 @@ cudaError_t launch_verify(const void* logits, int64_t logits_stride, bool bf16,
                           int requests, int64_t nodes, int vocab, int max_nodes,
                           const float* uniforms, const float* noise, const float* draft,
                           const float* temperature, int32_t* count, int32_t* path, int32_t* next,
-                          int* err, int num_sms, cudaStream_t st) {
+                          int* err, int num_sms, cudaStream_t st, uint64_t wait_ns, int silent) {
   const VerifyArgs a{logits, logits_stride, tokens, parents, offsets, requests, nodes,
                      vocab,  max_nodes,     uniforms, noise, draft,   temperature, count,
-                     path,   next,          err};
+                     path,   next,          err,      wait_ns, silent};
   auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const bool vec = vocab % 8 == 0 && logits_stride % 8 == 0 && on16(logits) && on16(noise) && on16(draft);
   if (bf16)
