@@ -366,10 +366,13 @@ cider_status_t cider_tree_attention(const cider_kv_cache_t* cache, int64_t layer
  *   next     int32 [requests]: the token that follows the path (-1 without nodes)
  * The current node's children are asked in increasing order.  With draft: the
  * residual r starts as softmax(logits / temperature), Z = 1, Q = 1; a child with
- * token x is accepted if u q(x) Z < r(x) Q; else r <- max(r / Z - q / Q, 0),
- * Z <- sum r (both stay if that is 0), Q <- Q - q(x), q(x) <- 0.  Without: accepted
- * if u Z < r(x); else Z <- Z - r(x), r(x) <- 0.  With no accepted child the next
- * token is the lowest index of the largest r(x) / noise(x). */
+ * token x is accepted if u q(x) / Q Z < r(x); else r <- max(r / Z - q / Q, 0),
+ * Z <- sum r (both stay if nothing is left of that), q(x) <- 0, Q <- sum q; with
+ * nothing left of Q the remaining children are refused (a sum below 2^-126 is
+ * nothing).  Without: accepted if u Z < r(x); else Z <- Z - r(x), r(x) <- 0.  With
+ * no accepted child the next token is the lowest index of the largest
+ * r(x) / noise(x).  Probabilities and sums are fp32, 2^x and 1 / noise the
+ * hardware's approximations (2 ulp): decisions nearer to a tie may fall either way. */
 cider_status_t cider_verify_drafts(const void* logits, int64_t logits_stride, int dtype,
                                    const int32_t* tokens, const int32_t* parents,
                                    const int32_t* offsets, int64_t requests, int64_t nodes,

@@ -6,8 +6,12 @@
 // current node's children are asked in increasing order.
 //   Drafts drawn from a distribution q without replacement: with the residual
 //   r (first p, mass Z = 1) and the rest of q (mass Q = 1), a child with token
-//   x is accepted if u q(x) Z < r(x) Q; otherwise r <- max(r / Z - q / Q, 0),
-//   Z <- sum r (r and Z stay when nothing is left), Q <- Q - q(x), q(x) <- 0.
+//   x is accepted if u q(x) / Q Z < r(x); otherwise r <- max(r / Z - q / Q, 0),
+//   Z <- sum r (r and Z stay when nothing is left), q(x) <- 0, Q <- sum q.
+//   Q is added up anew each time: as 1 - q(x1) - q(x2) - ... it would be rounding
+//   noise, of either sign, once a peaked drafter's first tokens are refused.
+//   Nothing is left of a sum below 2^-126 (its reciprocal may overflow).  With
+//   nothing left of q no later child can have been drawn: all are refused.
 //   Certain drafts (no q): accepted if u Z < r(x); otherwise Z <- Z - r(x),
 //   r(x) <- 0.
 // An accepted child becomes the current node.  When no child is accepted, or
@@ -81,16 +85,18 @@ __device__ __forceinline__ uint32_t best_index(uint64_t p) {
 
 // One rejected child of the current node.
 struct Rejected {
-  float inv_mass, inv_drawn;   // 1 / Z and 1 / Q when it was asked
+  float inv_mass, inv_rest;    // 1 / Z and 1 / Q when it was asked
   int32_t token;
   int32_t keeps;               // nothing was left: r stayed as it was
 };
 
-// What a thread, a warp or a CTA found in its share: sum counts from top.
+// What a thread, a warp or a CTA found in its share: sum counts from top.  Of a
+// pair of plain sums, `top` is the second one.
 struct Found {
   float top, sum;
   uint64_t best;
 };
+constexpr float kLeast = 0x1p-126f;   // nothing is left of a smaller sum
 
 struct Shared {
   Found warp[2][kVerifyWarps];   // by exchange
@@ -115,9 +121,18 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
 }
 
 // The largest top, the sums from it added in a fixed tree, and the largest
-// best, over N lanes (a power of two).  c: the softmax's factor.
-template <int N>
+// best, over N lanes (a power of two).  c: the softmax's factor.  SUMS: two plain
+// sums instead, in the same tree.
+template <int N, bool SUMS>
 __device__ __forceinline__ Found join_lanes(Found v, float c) {
+  if constexpr (SUMS) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+      v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+      v.top += __shfl_xor_sync(0xffffffffu, v.top, o);
+    }
+    return v;
+  }
   float top = v.top;
 #pragma unroll
   for (int o = N / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -140,14 +155,15 @@ __device__ __forceinline__ Found join_lanes(Found v, float c) {
 // other ranks gave up: v is then worth nothing, and the CTA has to leave
 // (nothing more may be expected of a barrier whose phase is open, and threads
 // that went on with different results could wait at different barriers).
+template <bool SUMS>
 __device__ __forceinline__ bool exchange(Found& v, float c, Shared& sh, int ranks, int rank, uint32_t& count,
                                          const VerifyArgs& a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t parity = count & 1, phase = count >> 1 & 1;
-  v = join_lanes<32>(v, c);
+  v = join_lanes<32, SUMS>(v, c);
   if (lane == 0) sh.warp[parity][warp] = v;
   __syncthreads();
-  v = join_lanes<kVerifyWarps>(sh.warp[parity][lane % kVerifyWarps], c);
+  v = join_lanes<kVerifyWarps, SUMS>(sh.warp[parity][lane % kVerifyWarps], c);
   if (ranks > 1) {
     volatile uint32_t* abort_flag = &sh.abort;
     const uint32_t bar = smem_u32(&sh.bar[parity]);
@@ -158,20 +174,20 @@ __device__ __forceinline__ bool exchange(Found& v, float c, Shared& sh, int rank
                   mapa_shared(bar, threadIdx.x));
     const bool here = mbar_wait_bounded(bar, phase, abort_flag, a.err, a.wait_ns);
     if (!__syncthreads_and(here)) return false;
-    v = Found{sh.cta[parity][0].top, 0.0f, 0};   // of a rank that is not there
+    v = Found{SUMS ? 0.0f : sh.cta[parity][0].top, 0.0f, 0};   // of a rank that is not there
     if ((lane & (kMaxCluster - 1)) < ranks) v = sh.cta[parity][lane & (kMaxCluster - 1)];
-    v = join_lanes<kMaxCluster>(v, c);
+    v = join_lanes<kMaxCluster, SUMS>(v, c);
   }
   ++count;
   return true;
 }
 
 // r(x) of sampled drafts after the node's rejected children so far; q: the
-// drafter's row's value at x.
-__device__ __forceinline__ float residual(float r, float q, int x, const Rejected* rejected, int n) {
+// drafter's row's value at x, afterwards what is left of it.
+__device__ __forceinline__ float residual(float r, float& q, int x, const Rejected* rejected, int n) {
   for (int j = 0; j < n; ++j) {
     const Rejected& e = rejected[j];
-    if (!e.keeps) r = fmaxf(r * e.inv_mass - q * e.inv_drawn, 0.0f);
+    if (!e.keeps) r = fmaxf(r * e.inv_mass - q * e.inv_rest, 0.0f);
     if (x == e.token) q = 0.0f;
   }
   return r;
@@ -258,7 +274,10 @@ __device__ __forceinline__ void prefetch_range(const void* begin, const void* en
                  : "memory");
 }
 
-template <typename T, bool VEC>
+// DRAFT: the drafts were drawn from `draft`; else they are certain.  (As a choice
+// at run time the sums of q's rest, which certain drafts do not need, cost them
+// spills: 48 trees 34 us instead of 29.)
+template <typename T, bool VEC, bool DRAFT>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a, int ranks) {
   __shared__ __align__(16) Shared sh;
   const int rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
   bool lost = false;   // a wait for the other ranks gave up
   for (;;) {
     const T* row = logits + (first + now) * a.logits_stride;
-    const float* q = a.draft ? a.draft + (first + now) * a.vocab : nullptr;
+    const float* q = DRAFT ? a.draft + (first + now) * a.vocab : nullptr;
     // the children, in a word; what is asked of them below is fetched meanwhile
     uint64_t children;
     {
@@ -326,7 +345,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
       const int x = sh.token[threadIdx.x];
       if (x >= 0 && x < a.vocab) {
         sh.logit[threadIdx.x] = as_float(row[x]);
-        if (q) sh.drafted[threadIdx.x] = q[x];
+        if (DRAFT) sh.drafted[threadIdx.x] = q[x];
       }
     }
     // ------------------------------------------------ maximum and sum, one pass
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     }
     if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     started = true;
-    lost = !exchange(v, c, sh, ranks, rank, exchanges, a);
+    lost = !exchange<false>(v, c, sh, ranks, rank, exchanges, a);
     if (lost) break;
     // an all -inf row has no maximum of its own: its first token stands for it
     const int hot = v.best ? static_cast<int>(best_index(v.best)) : 0;
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
     // a row of -inf alone is no distribution: nothing is accepted
     const float inv_sum = top == -INFINITY ? 0.0f : 1.0f / v.sum;
     auto prob = [&](float l) { return l == -INFINITY ? 0.0f : exp2_approx((l - top) * c) * inv_sum; };
-    float mass = 1.0f, drawn = 1.0f;
+    float mass = 1.0f, q_rest = 1.0f;   // Z and Q
     int rejected = 0, accepted = -1;
     uint64_t refused = 0;   // certain drafts: the rejected children, by node
     while (children) {
@@ -395,10 +414,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         }
         continue;
       }
+      if (DRAFT && q_rest < kLeast) continue;
       const float u = sh.uniform[i];
-      float qx = q ? sh.drafted[i] : 1.0f;
+      float qx = DRAFT ? sh.drafted[i] : 1.0f;
       float r = prob(sh.logit[i]);
-      if (!q) {
+      if (!DRAFT) {
         for (uint64_t m = refused; m; m &= m - 1)
           if (sh.token[__ffsll(static_cast<long long>(m)) - 1] == x) r = 0.0f;
         if (u * mass < r) {
@@ -410,30 +430,31 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         continue;
       }
       r = residual(r, qx, x, sh.rejected, rejected);
-      for (int j = 0; j < rejected; ++j)
-        if (sh.rejected[j].token == x) qx = 0.0f;
-      if (u * qx * mass < r * drawn) {
+      const float inv_rest = 1.0f / q_rest;
+      if (u * (qx * inv_rest) * mass < r) {
         accepted = i;
         break;
       }
       __syncthreads();
-      if (threadIdx.x == 0) sh.rejected[rejected] = Rejected{1.0f / mass, 1.0f / drawn, x, 0};
+      if (threadIdx.x == 0) sh.rejected[rejected] = Rejected{1.0f / mass, inv_rest, x, 0};
       __syncthreads();
       ++rejected;
-      Found rest{0.0f, 0.0f, 0};
+      Found rest{0.0f, 0.0f, 0};   // sums: of r, and of q in `top`
       for (int k = begin_block + warp; k < end_block; k += kVerifyWarps) {
         float f[8], g[8];
         load8<T, VEC>(row, k, lane, a.vocab, f);
         load8<float, VEC>(q, k, lane, a.vocab, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (token_of<VEC>(k, lane, j) < a.vocab)
+          if (token_of<VEC>(k, lane, j) < a.vocab) {
             rest.sum += residual(prob(f[j]), g[j], token_of<VEC>(k, lane, j), sh.rejected, rejected);
+            rest.top += g[j];
+          }
       }
-      lost = !exchange(rest, 0.0f, sh, ranks, rank, exchanges, a);
+      lost = !exchange<true>(rest, 0.0f, sh, ranks, rank, exchanges, a);
       if (lost) break;
-      drawn -= qx;
-      if (rest.sum == 0.0f) {
+      q_rest = rest.top;
+      if (rest.sum < kLeast) {
         if (threadIdx.x == 0) sh.rejected[rejected - 1].keeps = 1;
         __syncthreads();
       } else {
@@ -462,7 +483,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
           if (k + u * kVerifyWarps < end_block) {
             load8<T, VEC>(row, k + u * kVerifyWarps, lane, a.vocab, f[u]);
             load8<float, VEC>(noise, k + u * kVerifyWarps, lane, a.vocab, e[u]);
-            if (q) load8<float, VEC>(q, k + u * kVerifyWarps, lane, a.vocab, g[u]);
+            if (DRAFT) load8<float, VEC>(q, k + u * kVerifyWarps, lane, a.vocab, g[u]);
           }
         for (uint64_t m = refused; m; m &= m - 1) {
           const int i = __ffsll(static_cast<long long>(m)) - 1;
@@ -483,7 +504,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
           for (int j = 0; j < 8; ++j) {
             const int x = token_of<VEC>(k + u * kVerifyWarps, lane, j);
             float r = exp2_approx((f[u][j] - base) * c);
-            if (q) r = residual(r * inv_sum, g[u][j], x, sh.rejected, rejected);
+            if (DRAFT) r = residual(r * inv_sum, g[u][j], x, sh.rejected, rejected);
             float inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e[u][j]));
             const float key = x < a.vocab ? r * inv : -1.0f;
@@ -495,7 +516,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         }
       }
       Found drawn_token{0.0f, 0.0f, high < 0.0f ? 0 : pack_best(high, at)};
-      lost = !exchange(drawn_token, 0.0f, sh, ranks, rank, exchanges, a);
+      lost = !exchange<false>(drawn_token, 0.0f, sh, ranks, rank, exchanges, a);
       if (lost) break;
       next = static_cast<int>(best_index(drawn_token.best));
     }
@@ -524,8 +545,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
   }
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_typed(const VerifyArgs& a, int num_sms, cudaStream_t st) {
+template <typename T, bool VEC, bool DRAFT>
+cudaError_t launch_as(const VerifyArgs& a, int num_sms, cudaStream_t st) {
   // two CTAs fit an SM: as many per request as fit at once, and have a block of
   // tokens for each of their warps
   int ranks = kMaxCluster;
@@ -543,7 +564,11 @@ cudaError_t launch_typed(const VerifyArgs& a, int num_sms, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, a, ranks);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC, DRAFT>, a, ranks);
+}
+template <typename T, bool VEC>
+cudaError_t launch_typed(const VerifyArgs& a, int num_sms, cudaStream_t st) {
+  return a.draft ? launch_as<T, VEC, true>(a, num_sms, st) : launch_as<T, VEC, false>(a, num_sms, st);
 }
 
 }  // namespace
