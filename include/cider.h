@@ -332,8 +332,10 @@ cider_status_t cider_kv_compact(const cider_kv_cache_t* cache, const int32_t* ta
  *            NULL: token t sees the new tokens 0 .. t (a chain, or one token)
  *   scale    of q . k before the softmax (finite)
  *   out      [tokens, q_heads, D] of dtype.  A token that sees no position gets
- *            zeros; rows of a request whose offsets or length contradict the
- *            call's sizes are not written.
+ *            zeros, and so does one that belongs to no request (before offsets[0]
+ *            or from offsets[requests] on), which is reported; rows of a request
+ *            whose offsets or length contradict the call's sizes are not written,
+ *            and reported.  An empty problem launches nothing and writes nothing.
  * Products and sums are fp32; the weights of the values are rounded to fp16, their
  * sum is taken before that; the result is rounded once to dtype.  Value scales
  * below 2^-90 count as 2^-90.  The same call gives the same bits.  Scratch for the

@@ -567,7 +567,8 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
     """Attention of each request's last tokens q [tokens, q_heads, D] over its
     cached positions (lengths int32 [requests], the new tokens included).
     tree int64 [tokens]: which of its request's new tokens a token sees (None:
-    itself and the earlier ones).  -> out [tokens, q_heads, D] of q's type."""
+    itself and the earlier ones).  -> out [tokens, q_heads, D] of q's type; rows
+    that no request owns are zeros."""
     c, dev, heads, dim, _ = _cache_args(cache)
     dt, qs = _rows(q, "q", None, dim, dev)
     shape = q.shape
@@ -581,6 +582,8 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
         yp = out.data_ptr()
     else:
         yp = _flat(out, q.dtype, "out", shape, dev)
+    if not b or not cache[0].numel():   # nothing is launched for an empty problem
+        return out.zero_()
     st = (_lib or _load()).cider_tree_attention(c, layer, q.data_ptr(), qs, dt, n, shape[1], tp, width, lp,
                                                 op, b, max_nodes, mp,
                                                 dim ** -0.5 if scale is None else scale, yp,

@@ -23,6 +23,22 @@
 namespace cider {
 namespace {
 
+// Zeros for the rows of the output that no request owns, before the first offset
+// and past the last, and their report.  The first launch of the call does not
+// touch them, and what ran before it is over: nothing is waited for.
+__device__ __forceinline__ void zero_unowned(const AttendArgs& a) {
+  const int64_t before = max(static_cast<int64_t>(a.offsets[0]), int64_t{0});
+  const int64_t past = max(static_cast<int64_t>(a.offsets[a.requests]), int64_t{0});
+  if (before == 0 && past >= a.rows) return;
+  if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, kDevErrIndex);
+  const int64_t chunks = static_cast<int64_t>(a.q_heads) * a.cache.head_dim / 8;   // 16 bytes each, of a row
+  uint4* const out = static_cast<uint4*>(a.out);
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x;
+  for (int64_t i = first; i < min(before, a.rows) * chunks; i += step) out[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = past * chunks + first; i < a.rows * chunks; i += step) out[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Share c begins within a unit and the share before it began the unit: adds the
 // unit's parts in the order of the shares and writes its rows.  One CTA per
 // (share, kJoinRows rows), a warp per row.  The shares' ends follow from the
@@ -34,9 +50,12 @@ constexpr int kJoinRows = 4, kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttendArgs a, PartsArgs parts, bool bf16) {
   extern __shared__ float weights[];   // per warp and part: its factor
-  pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (c == 0) return;
+  if (c == 0) {   // no share lies before this one: its CTAs see to the rows without a request
+    zero_unowned(a);
+    return;
+  }
+  pdl_wait();
   const PartsArgs::Info i = parts.info[c];
   const int64_t before = parts.info[c - 1].begin;
   // the share before holds the unit's first tile unless it begins within it too
