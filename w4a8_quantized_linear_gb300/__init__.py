@@ -533,7 +533,7 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
     if layer is not None and layer < 0:
         raise ValueError(f"layer must be None (all layers) or at least 0, got {layer}")
     if out is None:
-        # zeros where no request reads: nothing is launched for an empty problem
+        # zeros where nothing is launched, as below
         make = torch.empty if n and cache[0].shape[1] else torch.zeros
         place = cache[0].device
         k, v = out = make(shape, dtype=dtype, device=place), make(shape, dtype=dtype, device=place)
@@ -541,6 +541,9 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
     else:
         kp = _flat(out[0], dtype, "out[0]", shape, dev)
         vp = _flat(out[1], dtype, "out[1]", shape, dev)
+        if not n or not cache[0].numel():   # nothing is launched for an empty problem
+            out[0].zero_()
+            out[1].zero_()
     st = (_lib or _load()).cider_kv_read(c, -1 if layer is None else layer, tp, width, sp, op, n, tokens,
                                          kp, vp, _DTYPES[dtype], _raw_stream(dev))
     if st:
