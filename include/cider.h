@@ -338,7 +338,8 @@ cider_status_t cider_kv_compact(const cider_kv_cache_t* cache, const int32_t* ta
  *            and reported.  An empty problem launches nothing and writes nothing.
  * Products and sums are fp32; the weights of the values are rounded to fp16, their
  * sum is taken before that; the result is rounded once to dtype.  Value scales
- * below 2^-90 count as 2^-90.  The same call gives the same bits.  Scratch for the
+ * below 2^-90 count as 2^-90; a row of zeros adds its weight to the sum alone,
+ * whatever its scale of 1.  The same call gives the same bits.  Scratch for the
  * joined parts of long requests comes from the library's pool. */
 cider_status_t cider_tree_attention(const cider_kv_cache_t* cache, int64_t layer, const void* q,
                                     int64_t q_stride, int dtype, int64_t tokens, int64_t q_heads,

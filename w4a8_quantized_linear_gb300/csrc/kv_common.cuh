@@ -19,6 +19,14 @@ namespace cider {
 // is skipped and this bit of the device error word set.
 constexpr int kDevErrIndex = 2;
 
+// A value row of zeros has scale 1.  It adds nothing to an output however large
+// its weight, so its scale must not set the maximum that the other weights are
+// rounded against: the attention takes it as 2^-60, far below the scales of
+// ordinary values (fp16's lie in 2^-31 .. 2^9) and far enough above fp32's least
+// number that its weight still counts in the sum (down to 2^-63 of the others'
+// for scales of 2^9).  Only rows of scale 1 are looked at.
+constexpr float kZeroRowScale = 0x1p-60f;
+
 constexpr int kMaxNodes = 64;   // new tokens of one request: a mask is 64 bits
 
 struct KvCache {

@@ -12,7 +12,9 @@
 // exceeds it by 8 (p' stays below 2^14 with the shift of 6; fp16 goes to 2^16),
 // so the outputs are rarely rescaled.  Scales below 2^-90 count as 2^-90: a
 // value's error is then at most 127 * 2^-90.  A scale of 0 marks a position
-// that is not there (a page out of range is filled with zeros).
+// that is not there (a page out of range is filled with zeros).  A row of zeros
+// (scale 1) counts as one of scale 2^-60, so that its weight, which nothing is
+// multiplied by, does not set m_i.
 //
 // q . ck on the fp16 pipe: a code plus 128 (INT4: plus 8), as the bits of an
 // fp16 subnormal, is (code + 128) 2^-24 exactly, one mask per two codes; the
@@ -472,7 +474,16 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
       if (C::kSub == 32 || lane < C::kSub) {
         const float sk = reinterpret_cast<const float*>(st + 2 * C::kSide)[lane];
         const float sv = reinterpret_cast<const float*>(st + 2 * C::kSide)[C::kSub + lane];
-        const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        if (sv == 1.0f) {   // rarely any other than a row of zeros
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int i = 0; i < RB; i += 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(st + C::kSide + swz_v<RB>(lane * RB + i));
+            any |= w.x | w.y | w.z | w.w;
+          }
+          if (any == 0) kept = kZeroRowScale;
+        }
         scale_smem[lane] = make_float4(sk * mul, log2_approx(kept),
                                        kept > 0.0f && kept < INFINITY ? rcp_approx(kept) : 0.0f, 0.0f);
       }

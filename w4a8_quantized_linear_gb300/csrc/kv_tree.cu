@@ -573,7 +573,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sk = in[0], sv = in[kTilePos];
         float* f = reinterpret_cast<float*>(smem + C::kScaleOffset + (n & 3) * C::kScaleStage);
         const int pair = token_s >> 1, e = token_s & 1;
-        const float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        float kept = sv > 0.0f && sv < 0x1p-90f ? 0x1p-90f : sv;
+        if (sv == 1.0f) {   // a row of zeros does not set the maximum; the codes came with the scales
+          const uint8_t* codes = smem + C::kRingOffset + (slot + 1 == C::kSlots ? 0 : slot + 1) * C::kRingSlot +
+                                 token_s * C::kRowBytes;
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int i = 0; i < C::kRowBytes; i += 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + i);
+            any |= w.x | w.y | w.z | w.w;
+          }
+          if (any == 0) kept = kZeroRowScale;
+        }
         float lg, inv;
         asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(kept));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(kept));
