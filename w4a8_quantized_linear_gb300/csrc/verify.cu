@@ -73,9 +73,9 @@ __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // A float's order as an unsigned number, above the index's reversed order:
-// the largest packed value is the largest float, at its lowest index.
+// the largest packed value is the largest float, at its lowest index.  -0 is +0.
 __device__ __forceinline__ uint64_t pack_best(float v, uint32_t i) {
-  uint32_t b = __float_as_uint(v);
+  uint32_t b = __float_as_uint(v + 0.0f);
   b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
   return static_cast<uint64_t>(b) << 32 | (0xFFFFFFFFu - i);
 }
