@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kCompactThreads)
   __shared__ int64_t from[kMaxNodes], to[kMaxNodes];   // rows of layer 0, head 0; -1: nothing moves
   const int b = blockIdx.y;
   const int n = kept[b];
-  if (n <= 0) return;
-  if (n > path_width) {
+  if (n == 0) return;
+  if (n < 0 || n > path_width) {
     if (threadIdx.x == 0) atomicOr(err, kDevErrIndex);
     return;
   }
