@@ -426,7 +426,10 @@ def cider_kv_cache(layers: int, pages: int, heads: int, head_dim: int, page_size
 # microseconds: each tensor is passed by one chained condition, and only a
 # tensor that fails it goes through the function that says what is wrong.
 _I32, _I64, _F32, _I8, _U8 = torch.int32, torch.int64, torch.float32, torch.int8, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index
+# The current stream's handle, of a device index.  The function behind
+# current_stream() saves a few microseconds a call; a PyTorch without CUDA lacks it.
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _refuse_cache(cache):
