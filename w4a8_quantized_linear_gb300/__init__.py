@@ -451,12 +451,15 @@ def _refuse_cache(cache):
 def _cache_args(cache):
     """-> (cider_kv_cache_t as bytes, device index, heads, head_dim, layers)."""
     k, ks, v, vs = cache
-    shape, kind, dev = k.shape, k.dtype, k.get_device()
-    if not (len(shape) == 5 and (kind is _I8 or kind is _U8) and v.dtype is kind and ks.dtype is _F32
-            and vs.dtype is _F32 and v.shape == shape and dev >= 0 and ks.get_device() == dev
-            and v.get_device() == dev and vs.get_device() == dev and k.is_contiguous()
-            and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
-            and ks.shape == shape[:4] and vs.shape == shape[:4]):
+    try:
+        shape, kind, dev = k.shape, k.dtype, k.get_device()
+        if not (len(shape) == 5 and (kind is _I8 or kind is _U8) and v.dtype is kind and ks.dtype is _F32
+                and vs.dtype is _F32 and v.shape == shape and dev >= 0 and ks.get_device() == dev
+                and v.get_device() == dev and vs.get_device() == dev and k.is_contiguous()
+                and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+                and ks.shape == shape[:4] and vs.shape == shape[:4]):
+            _refuse_cache(cache)
+    except AttributeError:   # not all are tensors
         _refuse_cache(cache)
     layers, pages, heads, page, width = shape
     bits, dim = (8, width) if kind is _I8 else (4, 2 * width)
@@ -466,7 +469,7 @@ def _cache_args(cache):
 
 def _rows(t, name, heads, dim, dev):
     """dtype and token stride of a [tokens, heads, dim] tensor with dense heads."""
-    if not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
@@ -484,9 +487,12 @@ def _rows(t, name, heads, dim, dev):
 
 def _flat(t, dtype, name, shape, dev):
     """A contiguous tensor of this type and shape on this device -> its pointer."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if not t.is_cuda or t.dtype != dtype:
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:   # not a tensor
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -495,12 +501,14 @@ def _flat(t, dtype, name, shape, dev):
     raise ValueError(f"{name} is on another device")
 
 
-def _width(t, name):
-    """The columns of a matrix."""
+def _size(t, name, dims):
+    """The last dimension of a vector (dims 1) or a matrix (2)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
     shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
-    return shape[1]
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimension{'s' * (dims > 1)}, got {tuple(shape)}")
+    return shape[-1]
 
 
 def cider_kv_append(k, v, slots, cache, layer: int = 0) -> None:
@@ -525,7 +533,7 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
     layer None): request b's positions starts[b], starts[b] + 1, ... for its
     output rows offsets[b] .. offsets[b + 1]."""
     c, dev, heads, dim, layers = _cache_args(cache)
-    n, width = starts.shape[0], _width(table, "table")
+    n, width = _size(starts, "starts", 1), _size(table, "table", 2)
     tp = _flat(table, _I32, "table", (n, width), dev)
     sp = _flat(starts, _I32, "starts", (n,), dev)
     op = _flat(offsets, _I32, "offsets", (n + 1,), dev)
@@ -558,7 +566,7 @@ def cider_kv_compact(cache, table, starts, path, kept) -> None:
     """In every layer, move request b's row at position starts[b] + path[b, i]
     to starts[b] + i for i < kept[b]."""
     c, dev, _, _, _ = _cache_args(cache)
-    n, width, most = starts.shape[0], _width(table, "table"), _width(path, "path")
+    n, width, most = _size(starts, "starts", 1), _size(table, "table", 2), _size(path, "path", 2)
     tp = _flat(table, _I32, "table", (n, width), dev)
     sp = _flat(starts, _I32, "starts", (n,), dev)
     pp = _flat(path, _I32, "path", (n, most), dev)
@@ -578,7 +586,7 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
     c, dev, heads, dim, _ = _cache_args(cache)
     dt, qs = _rows(q, "q", None, dim, dev)
     shape = q.shape
-    n, b, width = shape[0], lengths.shape[0], _width(table, "table")
+    n, b, width = shape[0], _size(lengths, "lengths", 1), _size(table, "table", 2)
     tp = _flat(table, _I32, "table", (b, width), dev)
     lp = _flat(lengths, _I32, "lengths", (b,), dev)
     op = _flat(offsets, _I32, "offsets", (b + 1,), dev)
@@ -605,17 +613,17 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
     logits [nodes, vocab] (fp16 or bf16, any row stride), with the given random
     numbers.  -> (count int32 [requests], path int32 [requests, max_nodes],
     next int32 [requests])."""
-    dev = logits.get_device()
-    if dev < 0:
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
+    dev = logits.get_device()
     if logits.dtype not in _DTYPES:
         raise TypeError("logits must be float16 or bfloat16")
-    vocab = _width(logits, "logits")
+    vocab = _size(logits, "logits", 2)
     n = logits.shape[0]
     stride, one = logits.stride()
     if one != 1 and vocab > 1:
         raise ValueError("logits must have contiguous rows")
-    b = offsets.shape[0] - 1
+    b = _size(offsets, "offsets", 1) - 1
     tp = _flat(tokens, _I32, "tokens", (n,), dev)
     pp = _flat(parents, _I32, "parents", (n,), dev)
     op = _flat(offsets, _I32, "offsets", (b + 1,), dev)
