@@ -116,8 +116,25 @@ def _check(fn: str, status: int):
         raise CiderError(fn, status)
 
 
-def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+# The current stream's handle, of a device index, and the current device's index.
+# The functions behind current_stream() and current_device() save a few
+# microseconds a call; a PyTorch without CUDA lacks them.
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(fn: str, dev: int, *args):
+    """Call an entry point with the current stream of the device that its tensors
+    are on.  The library launches on the current device, so that is made current."""
+    call = getattr(_lib or _load(), fn)
+    if _current_device() == dev:
+        status = call(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, _raw_stream(dev))
+    if status:
+        _check(fn, status)
 
 
 def _ptr(t):
@@ -145,7 +162,7 @@ def _quantize_act(fn, x, dtype):
     M, K = x.shape
     qa = torch.empty((M, K), dtype=torch.int8, device=x.device)
     sa = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _check(fn, getattr(_load(), fn)(_ptr(x), M, K, _ptr(qa), _ptr(sa), _stream(x)))
+    _launch(fn, x.get_device(), _ptr(x), M, K, _ptr(qa), _ptr(sa))
     return qa, sa
 
 
@@ -167,9 +184,8 @@ def cider_int4_from_offset_binary(packed: torch.Tensor, out=None):
     if not packed.is_contiguous():
         raise ValueError("packed must be contiguous")
     dst = out if out is not None else torch.empty_like(packed)
-    _check("cider_int4_from_offset_binary",
-           _load().cider_int4_from_offset_binary(_ptr(packed), _ptr(dst), packed.numel(),
-                                                 _stream(packed)))
+    _launch("cider_int4_from_offset_binary", packed.get_device(), _ptr(packed), _ptr(dst),
+            packed.numel())
     return dst
 
 
@@ -182,14 +198,11 @@ def cider_quantize_weight_int8(w: torch.Tensor, group_size: int = 0, clip_percen
     qw = torch.empty((N, K), dtype=torch.int8, device=w.device)
     sw = torch.empty((N, G), dtype=torch.float32, device=w.device)
     if clip_percentile is None:
-        _check("cider_quantize_weight_int8",
-               _load().cider_quantize_weight_int8(_ptr(w), N, K, group_size, _ptr(qw), _ptr(sw),
-                                                  _stream(w)))
+        _launch("cider_quantize_weight_int8", w.get_device(), _ptr(w), N, K, group_size, _ptr(qw),
+                _ptr(sw))
     else:
-        _check("cider_quantize_weight_int8_clip",
-               _load().cider_quantize_weight_int8_clip(_ptr(w), N, K, group_size,
-                                                       float(clip_percentile), _ptr(qw), _ptr(sw),
-                                                       _stream(w)))
+        _launch("cider_quantize_weight_int8_clip", w.get_device(), _ptr(w), N, K, group_size,
+                float(clip_percentile), _ptr(qw), _ptr(sw))
     return qw, sw
 
 
@@ -202,14 +215,11 @@ def cider_quantize_weight_int4(w: torch.Tensor, group_size: int = 0, clip_percen
     qp = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     sw = torch.empty((N, G), dtype=torch.float32, device=w.device)
     if clip_percentile is None:
-        _check("cider_quantize_weight_int4",
-               _load().cider_quantize_weight_int4(_ptr(w), N, K, group_size, _ptr(qp), _ptr(sw),
-                                                  _stream(w)))
+        _launch("cider_quantize_weight_int4", w.get_device(), _ptr(w), N, K, group_size, _ptr(qp),
+                _ptr(sw))
     else:
-        _check("cider_quantize_weight_int4_clip",
-               _load().cider_quantize_weight_int4_clip(_ptr(w), N, K, group_size,
-                                                       float(clip_percentile), _ptr(qp), _ptr(sw),
-                                                       _stream(w)))
+        _launch("cider_quantize_weight_int4_clip", w.get_device(), _ptr(w), N, K, group_size,
+                float(clip_percentile), _ptr(qp), _ptr(sw))
     return qp, sw
 
 
@@ -227,8 +237,8 @@ def _linear(fn, x, qw, sw, group_size, int4, out=None, x_dtype=torch.float16):
     sw = sw.reshape(N, -1)
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    _check(fn, getattr(_load(), fn)(_ptr(x), M, N, K, _ptr(qw), _ptr(sw), _gran(group_size),
-                                    group_size, _ptr(y), _stream(x)))
+    _launch(fn, x.get_device(), _ptr(x), M, N, K, _ptr(qw), _ptr(sw), _gran(group_size), group_size,
+            _ptr(y))
     return y
 
 
@@ -267,9 +277,8 @@ def _linear_ex(fn, x, qw, sw, group_size, int4, y_dtype, out):
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=x.device)
     _need(y, y_dtype, "out", 2)
-    _check(fn, getattr(_load(), fn)(_ptr(x), _DTYPES[x.dtype], M, N, K, _ptr(qw), _ptr(sw),
-                                    _gran(group_size), group_size, _ptr(y), _DTYPES[y_dtype],
-                                    _stream(x)))
+    _launch(fn, x.get_device(), _ptr(x), _DTYPES[x.dtype], M, N, K, _ptr(qw), _ptr(sw),
+            _gran(group_size), group_size, _ptr(y), _DTYPES[y_dtype])
     return y
 
 
@@ -293,8 +302,8 @@ def _linear_prequant(fn, qa, sa, qw, sw, group_size, int4, out=None):
     sw = sw.reshape(N, -1)
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=qa.device)
-    _check(fn, getattr(_load(), fn)(_ptr(qa), _ptr(sa), M, N, K, _ptr(qw), _ptr(sw),
-                                    _gran(group_size), group_size, _ptr(y), _stream(qa)))
+    _launch(fn, qa.get_device(), _ptr(qa), _ptr(sa), M, N, K, _ptr(qw), _ptr(sw),
+            _gran(group_size), group_size, _ptr(y))
     return y
 
 
@@ -314,8 +323,7 @@ def _accumulators(fn, qa, qw, group_size, int4):
     N = qw.shape[0]
     G = K // group_size if group_size else 1
     acc = torch.empty((M, N, G), dtype=torch.int32, device=qa.device)
-    _check(fn, getattr(_load(), fn)(_ptr(qa), M, N, K, _ptr(qw), group_size, _ptr(acc),
-                                    _stream(qa)))
+    _launch(fn, qa.get_device(), _ptr(qa), M, N, K, _ptr(qw), group_size, _ptr(acc))
     return acc
 
 
@@ -332,21 +340,24 @@ def cider_check_device_error(device=None) -> int:
     """Synchronize the current stream and return (and clear) the status of
     the library's device error word: 0 (CIDER_OK), 5 (CIDER_ERR_TIMEOUT) or 6
     (CIDER_ERR_INDEX: a page, slot, offset, count or token was out of range)."""
-    s = torch.cuda.current_stream(device)
-    return int(_load().cider_check_device_error(ctypes.c_void_p(s.cuda_stream)))
+    with torch.cuda.device(device):   # the error word is the current device's; None: as it is
+        s = torch.cuda.current_stream()
+        return int(_load().cider_check_device_error(ctypes.c_void_p(s.cuda_stream)))
 
 
 def cider_trim_scratch_pool(keep_bytes: int = 0, device=None) -> None:
     """Return the library's pooled scratch memory beyond ``keep_bytes`` to the
     device (after the current stream's queued calls have run)."""
-    s = torch.cuda.current_stream(device)
-    _check("cider_trim_scratch_pool",
-           _load().cider_trim_scratch_pool(int(keep_bytes), ctypes.c_void_p(s.cuda_stream)))
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream()
+        _check("cider_trim_scratch_pool",
+               _load().cider_trim_scratch_pool(int(keep_bytes), ctypes.c_void_p(s.cuda_stream)))
 
 
 def cider_debug_wait_timeout(max_polls: int, device=None) -> int:
-    s = torch.cuda.current_stream(device)
-    return int(_load().cider_debug_wait_timeout(int(max_polls), ctypes.c_void_p(s.cuda_stream)))
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream()
+        return int(_load().cider_debug_wait_timeout(int(max_polls), ctypes.c_void_p(s.cuda_stream)))
 
 
 def cider_timing_begin(capacity: int) -> None:
@@ -426,10 +437,6 @@ def cider_kv_cache(layers: int, pages: int, heads: int, head_dim: int, page_size
 # microseconds: each tensor is passed by one chained condition, and only a
 # tensor that fails it goes through the function that says what is wrong.
 _I32, _I64, _F32, _I8, _U8 = torch.int32, torch.int64, torch.float32, torch.int8, torch.uint8
-# The current stream's handle, of a device index.  The function behind
-# current_stream() saves a few microseconds a call; a PyTorch without CUDA lacks it.
-_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
-               or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _refuse_cache(cache):
@@ -521,10 +528,7 @@ def cider_kv_append(k, v, slots, cache, layer: int = 0) -> None:
     if dv != dt or v.shape[0] != n:
         raise ValueError("k and v must have the same type and tokens")
     sp = _flat(slots, _I64, "slots", (n,), dev)
-    st = (_lib or _load()).cider_kv_append(c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n,
-                                           _raw_stream(dev))
-    if st:
-        _check("cider_kv_append", st)
+    _launch("cider_kv_append", dev, c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n)
 
 
 def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float16, layer=None,
@@ -555,10 +559,8 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
         if not n or not cache[0].numel():   # nothing is launched for an empty problem
             out[0].zero_()
             out[1].zero_()
-    st = (_lib or _load()).cider_kv_read(c, -1 if layer is None else layer, tp, width, sp, op, n, tokens,
-                                         kp, vp, _DTYPES[dtype], _raw_stream(dev))
-    if st:
-        _check("cider_kv_read", st)
+    _launch("cider_kv_read", dev, c, -1 if layer is None else layer, tp, width, sp, op, n, tokens,
+            kp, vp, _DTYPES[dtype])
     return out
 
 
@@ -571,9 +573,7 @@ def cider_kv_compact(cache, table, starts, path, kept) -> None:
     sp = _flat(starts, _I32, "starts", (n,), dev)
     pp = _flat(path, _I32, "path", (n, most), dev)
     kp = _flat(kept, _I32, "kept", (n,), dev)
-    st = (_lib or _load()).cider_kv_compact(c, tp, width, sp, pp, most, kp, n, _raw_stream(dev))
-    if st:
-        _check("cider_kv_compact", st)
+    _launch("cider_kv_compact", dev, c, tp, width, sp, pp, most, kp, n)
 
 
 def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree=None, scale=None,
@@ -598,12 +598,8 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
         yp = _flat(out, q.dtype, "out", shape, dev)
     if not b or not cache[0].numel():   # nothing is launched for an empty problem
         return out.zero_()
-    st = (_lib or _load()).cider_tree_attention(c, layer, q.data_ptr(), qs, dt, n, shape[1], tp, width, lp,
-                                                op, b, max_nodes, mp,
-                                                dim ** -0.5 if scale is None else scale, yp,
-                                                _raw_stream(dev))
-    if st:
-        _check("cider_tree_attention", st)
+    _launch("cider_tree_attention", dev, c, layer, q.data_ptr(), qs, dt, n, shape[1], tp, width, lp,
+            op, b, max_nodes, mp, dim ** -0.5 if scale is None else scale, yp)
     return out
 
 
@@ -635,10 +631,7 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
     path = torch.empty((b, max_nodes), dtype=_I32, device=place)
     count = torch.empty((b,), dtype=_I32, device=place)
     nxt = torch.empty((b,), dtype=_I32, device=place)
-    st = (_lib or _load()).cider_verify_drafts(logits.data_ptr(), stride if n > 1 else vocab,
-                                               _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes, up,
-                                               ep, dp, wp, count.data_ptr(), path.data_ptr(), nxt.data_ptr(),
-                                               _raw_stream(dev))
-    if st:
-        _check("cider_verify_drafts", st)
+    _launch("cider_verify_drafts", dev, logits.data_ptr(), stride if n > 1 else vocab,
+            _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes, up, ep, dp, wp,
+            count.data_ptr(), path.data_ptr(), nxt.data_ptr())
     return count, path, nxt
