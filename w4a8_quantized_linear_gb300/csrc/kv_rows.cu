@@ -18,10 +18,13 @@
 //
 // q . ck on the fp16 pipe: a code plus 128 (INT4: plus 8), as the bits of an
 // fp16 subnormal, is (code + 128) 2^-24 exactly, one mask per two codes; the
-// accumulator starts at -128 sum_d q_d 2^-24, which takes the offset out again
-// (magnitudes stay within 4x of the result's, in fp32).  Odd INT4 codes are
-// taken four bits up, 16 times as large, against q / 16.  q is first scaled by
-// a power of two so that it fits fp16 (bf16 reaches further).  For
+// accumulator starts at -128 sum_d q_d 2^-24, which takes the offset out again.
+// What is added up is at most 255 sum_d |q_d| (INT4: 15), not bounded by the
+// result: for a q of one sign and D = 128 about 50 times the size of a typical
+// q . ck.  The error is fp32's rounding of that in D / 16 + 1 steps, at most 2^-23
+// each: 5e-5 of a typical score of such a q at worst, more of one that cancels.
+// Odd INT4 codes are taken four bits up, 16 times as large, against q / 16.  q is
+// first scaled by a power of two so that it fits fp16 (bf16 reaches further).  For
 // p' . cv the offset would not stay small (it grows with the sum of the
 // weights while the values average out), so the value codes are centred, exactly.
 //
@@ -394,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, BITS, NB>::kCtas)
         m = a.tree ? static_cast<uint64_t>(a.tree[req.first + node]) : ~0ull >> (63 - node);
       mask_smem[threadIdx.x] = m;
     }
-    // one power of two for all rows puts the largest value in [2^13, 2^14):
-    // what a smaller row loses is 2^-38 of it, absolutely
+    // one power of two for all rows puts the largest value in [2^13, 2^14): what
+    // a smaller one loses is at most 2^-39 of it, absolutely (half of fp16's
+    // smallest step; 2^-35 for q / 16 of INT4's odd codes)
     float top = 0.0f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
