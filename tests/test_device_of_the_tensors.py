@@ -19,17 +19,21 @@ def test_launch_on_the_tensors_device(monkeypatch):
         yield
         now[0] = before
 
-    fake = types.SimpleNamespace(cider_kv_append=lambda *a: seen.append((now[0], a)) or 0,
-                                 cider_status_string=lambda s: b"refused", cider_kv_read=lambda *a: 2)
-    monkeypatch.setattr(pkg, "_lib", fake)
+    def cider_kv_append(*a):
+        seen.append((now[0], a))
+        return 0
+
+    def cider_kv_read(*a):
+        return 2
+
+    monkeypatch.setattr(pkg, "_lib", types.SimpleNamespace(cider_status_string=lambda s: b"refused"))
     monkeypatch.setattr(pkg, "_current_device", lambda: now[0])
-    monkeypatch.setattr(pkg, "_raw_stream", lambda d: 100 + d)
     monkeypatch.setattr(torch.cuda, "device", device)
-    pkg._launch("cider_kv_append", 0, 1, 2)
-    pkg._launch("cider_kv_append", 3, 1, 2)
-    assert seen == [(0, (1, 2, 100)), (3, (1, 2, 103))] and now == [0]
-    with pytest.raises(pkg.CiderError):
-        pkg._launch("cider_kv_read", 3)
+    pkg._launch(cider_kv_append, 0, (1, 2))
+    pkg._launch(cider_kv_append, 3, (1, 2))
+    assert seen == [(0, (1, 2)), (3, (1, 2))] and now == [0]
+    with pytest.raises(pkg.CiderError, match="cider_kv_read"):
+        pkg._launch(cider_kv_read, 3, ())
     assert now == [0]
 
 

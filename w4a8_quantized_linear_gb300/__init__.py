@@ -124,17 +124,23 @@ _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _launch(fn: str, dev: int, *args):
-    """Call an entry point with the current stream of the device that its tensors
-    are on.  The library launches on the current device, so that is made current."""
-    call = getattr(_lib or _load(), fn)
+def _launch(call, dev: int, args: tuple):
+    """Call an entry point of the library with `args`, the last of them a stream of
+    the device that its tensors are on.  The library launches on the current
+    device, so that one is made current."""
     if _current_device() == dev:
-        status = call(*args, _raw_stream(dev))
+        status = call(*args)
     else:
         with torch.cuda.device(dev):
-            status = call(*args, _raw_stream(dev))
+            status = call(*args)
     if status:
-        _check(fn, status)
+        _check(call.__name__, status)
+
+
+def _call(fn: str, t: torch.Tensor, *args):
+    """_launch with the current stream of t's device."""
+    dev = t.get_device()
+    _launch(getattr(_lib or _load(), fn), dev, args + (_raw_stream(dev),))
 
 
 def _ptr(t):
@@ -162,7 +168,7 @@ def _quantize_act(fn, x, dtype):
     M, K = x.shape
     qa = torch.empty((M, K), dtype=torch.int8, device=x.device)
     sa = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _launch(fn, x.get_device(), _ptr(x), M, K, _ptr(qa), _ptr(sa))
+    _call(fn, x, _ptr(x), M, K, _ptr(qa), _ptr(sa))
     return qa, sa
 
 
@@ -184,8 +190,7 @@ def cider_int4_from_offset_binary(packed: torch.Tensor, out=None):
     if not packed.is_contiguous():
         raise ValueError("packed must be contiguous")
     dst = out if out is not None else torch.empty_like(packed)
-    _launch("cider_int4_from_offset_binary", packed.get_device(), _ptr(packed), _ptr(dst),
-            packed.numel())
+    _call("cider_int4_from_offset_binary", packed, _ptr(packed), _ptr(dst), packed.numel())
     return dst
 
 
@@ -198,11 +203,10 @@ def cider_quantize_weight_int8(w: torch.Tensor, group_size: int = 0, clip_percen
     qw = torch.empty((N, K), dtype=torch.int8, device=w.device)
     sw = torch.empty((N, G), dtype=torch.float32, device=w.device)
     if clip_percentile is None:
-        _launch("cider_quantize_weight_int8", w.get_device(), _ptr(w), N, K, group_size, _ptr(qw),
-                _ptr(sw))
+        _call("cider_quantize_weight_int8", w, _ptr(w), N, K, group_size, _ptr(qw), _ptr(sw))
     else:
-        _launch("cider_quantize_weight_int8_clip", w.get_device(), _ptr(w), N, K, group_size,
-                float(clip_percentile), _ptr(qw), _ptr(sw))
+        _call("cider_quantize_weight_int8_clip", w, _ptr(w), N, K, group_size,
+              float(clip_percentile), _ptr(qw), _ptr(sw))
     return qw, sw
 
 
@@ -215,11 +219,10 @@ def cider_quantize_weight_int4(w: torch.Tensor, group_size: int = 0, clip_percen
     qp = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     sw = torch.empty((N, G), dtype=torch.float32, device=w.device)
     if clip_percentile is None:
-        _launch("cider_quantize_weight_int4", w.get_device(), _ptr(w), N, K, group_size, _ptr(qp),
-                _ptr(sw))
+        _call("cider_quantize_weight_int4", w, _ptr(w), N, K, group_size, _ptr(qp), _ptr(sw))
     else:
-        _launch("cider_quantize_weight_int4_clip", w.get_device(), _ptr(w), N, K, group_size,
-                float(clip_percentile), _ptr(qp), _ptr(sw))
+        _call("cider_quantize_weight_int4_clip", w, _ptr(w), N, K, group_size,
+              float(clip_percentile), _ptr(qp), _ptr(sw))
     return qp, sw
 
 
@@ -237,8 +240,7 @@ def _linear(fn, x, qw, sw, group_size, int4, out=None, x_dtype=torch.float16):
     sw = sw.reshape(N, -1)
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    _launch(fn, x.get_device(), _ptr(x), M, N, K, _ptr(qw), _ptr(sw), _gran(group_size), group_size,
-            _ptr(y))
+    _call(fn, x, _ptr(x), M, N, K, _ptr(qw), _ptr(sw), _gran(group_size), group_size, _ptr(y))
     return y
 
 
@@ -277,8 +279,8 @@ def _linear_ex(fn, x, qw, sw, group_size, int4, y_dtype, out):
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=x.device)
     _need(y, y_dtype, "out", 2)
-    _launch(fn, x.get_device(), _ptr(x), _DTYPES[x.dtype], M, N, K, _ptr(qw), _ptr(sw),
-            _gran(group_size), group_size, _ptr(y), _DTYPES[y_dtype])
+    _call(fn, x, _ptr(x), _DTYPES[x.dtype], M, N, K, _ptr(qw), _ptr(sw), _gran(group_size),
+          group_size, _ptr(y), _DTYPES[y_dtype])
     return y
 
 
@@ -302,8 +304,8 @@ def _linear_prequant(fn, qa, sa, qw, sw, group_size, int4, out=None):
     sw = sw.reshape(N, -1)
     _need(sw, torch.float32, "sw", 2)
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=qa.device)
-    _launch(fn, qa.get_device(), _ptr(qa), _ptr(sa), M, N, K, _ptr(qw), _ptr(sw),
-            _gran(group_size), group_size, _ptr(y))
+    _call(fn, qa, _ptr(qa), _ptr(sa), M, N, K, _ptr(qw), _ptr(sw), _gran(group_size), group_size,
+          _ptr(y))
     return y
 
 
@@ -323,7 +325,7 @@ def _accumulators(fn, qa, qw, group_size, int4):
     N = qw.shape[0]
     G = K // group_size if group_size else 1
     acc = torch.empty((M, N, G), dtype=torch.int32, device=qa.device)
-    _launch(fn, qa.get_device(), _ptr(qa), M, N, K, _ptr(qw), group_size, _ptr(acc))
+    _call(fn, qa, _ptr(qa), M, N, K, _ptr(qw), group_size, _ptr(acc))
     return acc
 
 
@@ -476,7 +478,7 @@ def _cache_args(cache):
 
 def _rows(t, name, heads, dim, dev):
     """dtype and token stride of a [tokens, heads, dim] tensor with dense heads."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
@@ -510,9 +512,10 @@ def _flat(t, dtype, name, shape, dev):
 
 def _size(t, name, dims):
     """The last dimension of a vector (dims 1) or a matrix (2)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    shape = t.shape
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a CUDA tensor") from None
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimension{'s' * (dims > 1)}, got {tuple(shape)}")
     return shape[-1]
@@ -528,7 +531,8 @@ def cider_kv_append(k, v, slots, cache, layer: int = 0) -> None:
     if dv != dt or v.shape[0] != n:
         raise ValueError("k and v must have the same type and tokens")
     sp = _flat(slots, _I64, "slots", (n,), dev)
-    _launch("cider_kv_append", dev, c, layer, k.data_ptr(), ks, v.data_ptr(), vs, dt, sp, n)
+    _launch((_lib or _load()).cider_kv_append, dev, (c, layer, k.data_ptr(), ks, v.data_ptr(), vs,
+            dt, sp, n, _raw_stream(dev)))
 
 
 def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float16, layer=None,
@@ -559,8 +563,8 @@ def cider_kv_read(cache, table, starts, offsets, tokens: int, dtype=torch.float1
         if not n or not cache[0].numel():   # nothing is launched for an empty problem
             out[0].zero_()
             out[1].zero_()
-    _launch("cider_kv_read", dev, c, -1 if layer is None else layer, tp, width, sp, op, n, tokens,
-            kp, vp, _DTYPES[dtype])
+    _launch((_lib or _load()).cider_kv_read, dev, (c, -1 if layer is None else layer, tp, width, sp,
+            op, n, tokens, kp, vp, _DTYPES[dtype], _raw_stream(dev)))
     return out
 
 
@@ -573,7 +577,8 @@ def cider_kv_compact(cache, table, starts, path, kept) -> None:
     sp = _flat(starts, _I32, "starts", (n,), dev)
     pp = _flat(path, _I32, "path", (n, most), dev)
     kp = _flat(kept, _I32, "kept", (n,), dev)
-    _launch("cider_kv_compact", dev, c, tp, width, sp, pp, most, kp, n)
+    _launch((_lib or _load()).cider_kv_compact, dev, (c, tp, width, sp, pp, most, kp, n,
+            _raw_stream(dev)))
 
 
 def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree=None, scale=None,
@@ -598,8 +603,9 @@ def cider_tree_attention(q, cache, table, lengths, offsets, max_nodes: int, tree
         yp = _flat(out, q.dtype, "out", shape, dev)
     if not b or not cache[0].numel():   # nothing is launched for an empty problem
         return out.zero_()
-    _launch("cider_tree_attention", dev, c, layer, q.data_ptr(), qs, dt, n, shape[1], tp, width, lp,
-            op, b, max_nodes, mp, dim ** -0.5 if scale is None else scale, yp)
+    _launch((_lib or _load()).cider_tree_attention, dev, (c, layer, q.data_ptr(), qs, dt, n,
+            shape[1], tp, width, lp, op, b, max_nodes, mp, dim ** -0.5 if scale is None else scale,
+            yp, _raw_stream(dev)))
     return out
 
 
@@ -609,7 +615,7 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
     logits [nodes, vocab] (fp16 or bf16, any row stride), with the given random
     numbers.  -> (count int32 [requests], path int32 [requests, max_nodes],
     next int32 [requests])."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+    if not getattr(logits, "is_cuda", False):
         raise TypeError("logits must be a CUDA tensor")
     dev = logits.get_device()
     if logits.dtype not in _DTYPES:
@@ -631,7 +637,7 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
     path = torch.empty((b, max_nodes), dtype=_I32, device=place)
     count = torch.empty((b,), dtype=_I32, device=place)
     nxt = torch.empty((b,), dtype=_I32, device=place)
-    _launch("cider_verify_drafts", dev, logits.data_ptr(), stride if n > 1 else vocab,
-            _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes, up, ep, dp, wp,
-            count.data_ptr(), path.data_ptr(), nxt.data_ptr())
+    _launch((_lib or _load()).cider_verify_drafts, dev, (logits.data_ptr(),
+            stride if n > 1 else vocab, _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes,
+            up, ep, dp, wp, count.data_ptr(), path.data_ptr(), nxt.data_ptr(), _raw_stream(dev)))
     return count, path, nxt
