@@ -336,7 +336,8 @@ cider_status_t cider_kv_compact(const cider_kv_cache_t* cache, const int32_t* ta
  *            or from offsets[requests] on), which is reported; rows of a request
  *            whose offsets or length contradict the call's sizes are not written,
  *            and reported.  An empty problem launches nothing and writes nothing.
- * Products and sums are fp32; the weights of the values are rounded to fp16, their
+ * Products and sums are fp32, 2^x, log2 and reciprocals the hardware's
+ * approximations (2 ulp); the weights of the values are rounded to fp16, their
  * sum is taken before that; the result is rounded once to dtype.  Value scales
  * below 2^-90 count as 2^-90; a row of zeros adds its weight to the sum alone,
  * whatever its scale of 1.  The same call gives the same bits.  Scratch for the

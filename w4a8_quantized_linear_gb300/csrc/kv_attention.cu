@@ -139,7 +139,7 @@ cudaError_t launch_join(const AttendArgs& a, const PartsArgs& parts, int ctas, i
 // By the query rows of a key/value head (new tokens x grouped heads).  At 32
 // requests of 4096 .. 16384 positions the many-row kernel takes the same time
 // for 1 to 128 rows, the other one grows with them: up to 32 rows (64 requests
-// of up to 8192, INT8: 229 us against 304) it is ahead.
+// of up to 8192, INT8: 224 us against 304) it is ahead.
 constexpr int kFewRows = 32;
 
 cudaError_t launch_attend(const AttendArgs& a, bool bf16, int num_sms, cudaStream_t st) {

@@ -18,7 +18,9 @@
 // of an SM's share of HBM against 1024 of tensor work); in practice the softmax
 // of a tile (~1600 cycles with four warps per scheduler, ~6 a warp's
 // instruction) and the steps around it (waits, agreement, P's store, the issue
-// of eight MMAs at ~110 cycles each) follow one another, ~3700 cycles a tile.
+// of eight MMAs at ~110 cycles each) follow one another, ~3700 cycles a tile: the
+// tensor pipe is active 26 % of the time.  The softmax warps' 80 registers do not
+// hold a tile's scores and weights beside the rest: 396 .. 420 bytes are spilled.
 // 32 requests of 4096 .. 16384 positions, 16 .. 32 new tokens, 32 / 8 heads of
 // 128, INT8: 289 us (2.5 TB/s of codes, 488 TFLOP/s), whatever the number of
 // rows up to 128.  Measured and not kept: two groups of softmax warps on
