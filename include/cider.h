@@ -73,8 +73,9 @@ typedef enum { CIDER_PER_CHANNEL = 0, CIDER_PER_GROUP = 1 } cider_granularity_t;
 
 /* Element type of an activation or output matrix (the Cider README's roadmap,
  * "auto dtype float16/bfloat16"): IEEE binary16, or bfloat16 (the upper half
- * of an IEEE binary32). */
-typedef enum { CIDER_F16 = 0, CIDER_BF16 = 1 } cider_dtype_t;
+ * of an IEEE binary32).  CIDER_F32 (IEEE binary32) is taken only where an entry
+ * point says so. */
+typedef enum { CIDER_F16 = 0, CIDER_BF16 = 1, CIDER_F32 = 2 } cider_dtype_t;
 
 /* 1 when the current CUDA device is an sm_103 GPU this library was built
  * for, else 0 (the Cider README's is_available(), "Conditional compilation").
@@ -384,6 +385,103 @@ cider_status_t cider_verify_drafts(const void* logits, int64_t logits_stride, in
                                    const float* noise, const float* draft,
                                    const float* temperature, int32_t* count, int32_t* path,
                                    int32_t* next, void* stream);
+
+/* ------------------------------------- microscaled 4-bit floating point
+ *
+ * Linears whose weights and activations are both 4-bit floating point with a
+ * scale per block of a row, multiplied on the block-scaled tensor cores.  The
+ * Cider README has no counterpart: its modes are W8A8 and W4A8.
+ *
+ * A value is an E2M1 number (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives: sign
+ * in bit 3) times its block's scale times its row's:
+ *   block_size 32  scale E8M0 (byte e + 127 is 2^e; 255 is NaN), no row scale of
+ *                  the quantizer's own
+ *   block_size 16  scale E4M3 (the byte of an 8-bit float, at most 448), and an
+ *                  fp32 scale for the row
+ * Two codes share a byte, element 2j in the low nibble, as in the INT4 weights.
+ *   codes      uint8 [rows, cols / 2]
+ *   scales     uint8 [ceil(rows / 128), ceil(cols / (4 block_size)), 512]: tiles
+ *              of 128 rows x 4 blocks, as the tensor cores read them.  Row r's
+ *              block j is byte 16 (r % 32) + 4 (r % 128 / 32) + j % 4 of tile
+ *              (r / 128, j / 4).  Bytes of blocks behind the last one are zero;
+ *              bytes of rows behind the last one reach no output
+ *   row_scale  fp32 [rows], or NULL: 1.  A factor of the row's values
+ * cols is a multiple of 32, at most 131072.
+ *
+ * Checks on the host, in this order: no rows or outputs returns CIDER_OK; null
+ * pointers, sizes, strides, types that do not fit each other give
+ * CIDER_ERR_INVALID_ARGUMENT; alignment (16 bytes; row_scale 4)
+ * CIDER_ERR_MISALIGNED; the device CIDER_ERR_UNSUPPORTED_DEVICE. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_scale;
+  int64_t rows, cols;
+  int32_t block_size;
+} cider_fp4_t;
+
+typedef enum { CIDER_SILU = 0, CIDER_GELU = 1 } cider_activation_t;
+
+/* Quantizes a matrix (activations, or weights once when a model is loaded).
+ *   x  [rows, cols] of x_dtype (CIDER_F16, CIDER_BF16 or CIDER_F32), x_stride
+ *      elements between rows: at least cols, whole units of 16 bytes
+ *   q  all of it is written, the padding of scales included; row_scale for block
+ *      size 16, and must be NULL for 32
+ * All roundings are to the nearest, ties to even.
+ *   block_size 32: s = the smallest power of two (at least 2^-127) with max|x| <=
+ *     6 s over the block, 1 for a block of zeros; code = E2M1(x / s).
+ *   block_size 16: r = the smallest power of two (at least 2^-126) with max|x| <=
+ *     2688 r over the row, 1 for a row of zeros; b = E4M3(max|x| / r / 6) over the
+ *     block; code = E2M1(x / r / b), at most 6, and 0 where b is 0.  The quotients
+ *     by 6 and by b are fp32.
+ * An infinity or NaN makes its block NaN (block size 32), or its row (16). */
+cider_status_t cider_quantize_fp4(const void* x, int x_dtype, int64_t x_stride, const cider_fp4_t* q,
+                                  void* stream);
+
+/* The values that a quantized matrix stands for, code * scale * row scale in
+ * fp32, rounded once to x_dtype (CIDER_F16, CIDER_BF16 or CIDER_F32).
+ *   x  [rows, cols], dense, output */
+cider_status_t cider_dequantize_fp4(const cider_fp4_t* q, void* x, int x_dtype, void* stream);
+
+/* W4A4 linear: y = x w^T with the rows of x quantized by the call, in w's block
+ * size.
+ *   x  [M, K] of x_dtype (CIDER_F16 or CIDER_BF16), x_stride elements between rows
+ *      (as for cider_quantize_fp4);  w  [N, K], N % 8 == 0;  y  [M, N] of y_dtype
+ * Products of codes and block scales are summed in fp32 in the tensor cores, the
+ * sum is multiplied by x's row scale and then w's, and rounded once to y_dtype.
+ * The same call gives the same bits. */
+cider_status_t cider_w4a4_linear(const void* x, int x_dtype, int64_t x_stride, int64_t M,
+                                 const cider_fp4_t* w, void* y, int y_dtype, void* stream);
+
+/* The same for rows that are quantized already (x's block size is w's): several
+ * projections of one input share its quantization. */
+cider_status_t cider_w4a4_linear_prequant(const cider_fp4_t* x, const cider_fp4_t* w, void* y,
+                                          int y_dtype, void* stream);
+
+/* First half of a gated feed-forward block: h = act(x gate^T) * (x up^T), both
+ * products, the activation and the product of the two in one kernel.
+ *   gate, up    [F, K] of one block size, F % 8 == 0
+ *   activation  CIDER_SILU: g / (1 + e^-g); CIDER_GELU: g (1 + tanh(sqrt(2 / pi)
+ *               (g + 0.044715 g^3))) / 2
+ *   h           [M, F] of h_dtype
+ * Both sums are fp32 and are not rounded before the activation; e^x and the
+ * reciprocal are the hardware's approximations (2 ulp); one rounding to h_dtype. */
+cider_status_t cider_w4a4_gated_linear(const void* x, int x_dtype, int64_t x_stride, int64_t M,
+                                       const cider_fp4_t* gate, const cider_fp4_t* up, int activation,
+                                       void* h, int h_dtype, void* stream);
+cider_status_t cider_w4a4_gated_linear_prequant(const cider_fp4_t* x, const cider_fp4_t* gate,
+                                                const cider_fp4_t* up, int activation, void* h,
+                                                int h_dtype, void* stream);
+
+/* The whole block: y = h down^T for h = act(x gate^T) * (x up^T) rounded to x's
+ * type and quantized in the weights' block size: the same bits as
+ * cider_w4a4_gated_linear with h_dtype = x_dtype, then cider_w4a4_linear.
+ *   down  [N, F], F % 32 == 0, N % 8 == 0;  y  [M, N] of y_dtype
+ * The hidden values are scratch of the library's pool. */
+cider_status_t cider_w4a4_feed_forward(const void* x, int x_dtype, int64_t x_stride, int64_t M,
+                                       const cider_fp4_t* gate, const cider_fp4_t* up,
+                                       const cider_fp4_t* down, int activation, void* y, int y_dtype,
+                                       void* stream);
 
 /* Size of the fixed scratch array used by cider_w8a8_linear_noalloc: 32 MiB
  * of device global memory per GPU on which the library has been used. */

@@ -28,6 +28,7 @@ CIDER_PER_CHANNEL = 0
 CIDER_PER_GROUP = 1
 CIDER_F16 = 0
 CIDER_BF16 = 1
+CIDER_F32 = 2
 _DTYPES = {torch.float16: CIDER_F16, torch.bfloat16: CIDER_BF16}
 STATUS_NAMES = {0: "CIDER_OK", 1: "CIDER_ERR_INVALID_ARGUMENT", 2: "CIDER_ERR_MISALIGNED",
                 3: "CIDER_ERR_UNSUPPORTED_DEVICE", 4: "CIDER_ERR_CUDA", 5: "CIDER_ERR_TIMEOUT",
@@ -83,6 +84,13 @@ def _declare(lib):
                                 i32),
         "cider_debug_verify_timeout": ([p, i64, i32, p, p, p, i64, i64, i64, i64, p, p, p, p, p, p, p,
                                         i64, ctypes.c_int32, p], i32),
+        "cider_quantize_fp4": ([p, i32, i64, p, p], i32),
+        "cider_dequantize_fp4": ([p, p, i32, p], i32),
+        "cider_w4a4_linear": ([p, i32, i64, i64, p, p, i32, p], i32),
+        "cider_w4a4_linear_prequant": ([p, p, p, i32, p], i32),
+        "cider_w4a4_gated_linear": ([p, i32, i64, i64, p, p, i32, p, i32, p], i32),
+        "cider_w4a4_gated_linear_prequant": ([p, p, p, i32, p, i32, p], i32),
+        "cider_w4a4_feed_forward": ([p, i32, i64, i64, p, p, p, i32, p, i32, p], i32),
         "cider_debug_small_m_launch": ([i64, i64, i64, i32, i32, i32, i32, p], i32),
     }
     for name, (args, res) in sig.items():
@@ -641,3 +649,196 @@ def cider_verify_drafts(logits, tokens, parents, offsets, uniforms, noise, max_n
             stride if n > 1 else vocab, _DTYPES[logits.dtype], tp, pp, op, b, n, vocab, max_nodes,
             up, ep, dp, wp, count.data_ptr(), path.data_ptr(), nxt.data_ptr(), _raw_stream(dev)))
     return count, path, nxt
+
+
+# ------------------------------------------ microscaled 4-bit floating point
+_FP4 = struct.Struct("@PPPqqi4x")   # cider_fp4_t
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
+_WIDE = {torch.float16: CIDER_F16, torch.bfloat16: CIDER_BF16, torch.float32: CIDER_F32}
+
+
+def _refuse_fp4(q, block_size, name):
+    if not isinstance(q, (tuple, list)) or len(q) != 3:
+        raise TypeError(f"{name} must be (codes, scales, row_scale)")
+    codes, scales, row = q
+    for t, part in ((codes, "codes"), (scales, "scales")) + (((row, "row_scale"),) if row is not None else ()):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}'s {part} must be a CUDA tensor")
+    if codes.dtype != _U8 or scales.dtype != _U8:
+        raise TypeError(f"{name}'s codes and scales must be uint8")
+    if row is not None and row.dtype != _F32:
+        raise TypeError(f"{name}'s row_scale must be float32")
+    if codes.dim() != 2:
+        raise ValueError(f"{name}'s codes must have 2 dimensions, got shape {tuple(codes.shape)}")
+    if not all(t is None or t.is_contiguous() for t in q):
+        raise ValueError(f"{name} must be contiguous")
+    if any(t is not None and t.get_device() != codes.get_device() for t in q):
+        raise ValueError(f"{name}'s tensors are on different devices")
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    raise ValueError(f"{name}: codes {tuple(codes.shape)} of block size {block_size} need scales "
+                     f"{_scale_shape(rows, cols, block_size)} and row_scale {(rows,)} (or None), got "
+                     f"{tuple(scales.shape)} and {None if row is None else tuple(row.shape)}")
+
+
+def _scale_shape(rows, cols, block_size):
+    return (rows + 127) // 128, -(-cols // (4 * block_size)), 512
+
+
+def _block(block_size):
+    if block_size not in (16, 32):
+        raise ValueError(f"block_size must be 16 or 32, got {block_size}")
+
+
+def _fp4_args(q, block_size, name, dev=None):
+    """-> (cider_fp4_t as bytes, device index, rows, cols)."""
+    try:
+        codes, scales, row = q
+        half, place = codes.shape, codes.get_device()
+        rows, cols = half[0], 2 * half[1]
+        if not (len(half) == 2 and codes.dtype is _U8 and scales.dtype is _U8 and place >= 0
+                and scales.get_device() == place and codes.is_contiguous() and scales.is_contiguous()
+                and scales.shape == _scale_shape(rows, cols, block_size)
+                and (row is None or (row.dtype is _F32 and row.shape == (rows,) and row.get_device() == place
+                                     and row.is_contiguous()))):
+            _refuse_fp4(q, block_size, name)
+    except (AttributeError, TypeError, ValueError, IndexError):   # not a triple of tensors
+        _refuse_fp4(q, block_size, name)
+    if dev is not None and place != dev:
+        raise ValueError(f"{name} is on another device")
+    return (_FP4.pack(codes.data_ptr(), scales.data_ptr(), 0 if row is None else row.data_ptr(), rows, cols,
+                      block_size), place, rows, cols)
+
+
+def _wide_rows(x, cols, kinds, dev=None):
+    """Type, row stride and rows of a matrix [rows, cols] with dense rows."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    if x.dtype not in kinds:
+        raise TypeError(f"x must be one of {', '.join(str(k) for k in kinds)}, got {x.dtype}")
+    if x.dim() != 2 or (cols is not None and x.shape[1] != cols):
+        raise ValueError(f"x must have shape [rows, {'cols' if cols is None else cols}], got {tuple(x.shape)}")
+    n, k = x.shape
+    stride, one = x.stride()
+    if one != 1 and k > 1:
+        raise ValueError("x must have contiguous rows")
+    if dev is not None and x.get_device() != dev:
+        raise ValueError("x is on another device")
+    return kinds[x.dtype], stride if n > 1 else k, n
+
+
+def _result(out, shape, dtype, dev, name):
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name}'s type must be float16 or bfloat16")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return out, out.data_ptr()
+    return out, _flat(out, dtype, name, shape, dev)
+
+
+def cider_quantize_fp4(x: torch.Tensor, block_size: int = 32):
+    """x fp16, bf16 or fp32 [rows, cols] (any row stride) -> (codes uint8 [rows, cols / 2],
+    scales uint8 [ceil(rows / 128), ceil(cols / (4 block_size)), 512], row_scale):
+    4-bit floating point (E2M1) with an E8M0 scale per 32 values (row_scale None),
+    or an E4M3 scale per 16 values and row_scale fp32 [rows]."""
+    _block(block_size)
+    kind, stride, rows = _wide_rows(x, None, _WIDE)
+    cols, place = x.shape[1], x.device
+    q = (torch.empty((rows, cols // 2), dtype=_U8, device=place),
+         torch.empty(_scale_shape(rows, cols, block_size), dtype=_U8, device=place),
+         torch.empty((rows,), dtype=_F32, device=place) if block_size == 16 else None)
+    c = _FP4.pack(q[0].data_ptr(), q[1].data_ptr(), 0 if q[2] is None else q[2].data_ptr(), rows, cols, block_size)
+    dev = x.get_device()
+    _launch((_lib or _load()).cider_quantize_fp4, dev, (x.data_ptr(), kind, stride, c, _raw_stream(dev)))
+    return q
+
+
+def cider_dequantize_fp4(q, block_size: int = 32, dtype=torch.float16, out=None):
+    """The values of a quantized matrix (codes, scales, row_scale) -> [rows, cols] of
+    `dtype` (fp16, bf16 or fp32)."""
+    _block(block_size)
+    c, dev, rows, cols = _fp4_args(q, block_size, "q")
+    if dtype not in _WIDE:
+        raise TypeError("dtype must be float16, bfloat16 or float32")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=q[0].device)
+        xp = out.data_ptr()
+    else:
+        xp = _flat(out, dtype, "out", (rows, cols), dev)
+    _launch((_lib or _load()).cider_dequantize_fp4, dev, (c, xp, _WIDE[dtype], _raw_stream(dev)))
+    return out
+
+
+def cider_w4a4_linear(x, w, block_size: int = 32, y_dtype=None, out=None):
+    """y [M, N] of y_dtype (None: x's) = x w^T for x fp16 or bf16 [M, K] (any row
+    stride), quantized by the call, and w = cider_quantize_fp4(weights [N, K])."""
+    _block(block_size)
+    c, dev, n, k = _fp4_args(w, block_size, "w")
+    kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
+    y_dtype = x.dtype if y_dtype is None else y_dtype
+    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    _launch((_lib or _load()).cider_w4a4_linear, dev, (x.data_ptr(), kind, stride, m, c, yp, _DTYPES[y_dtype],
+            _raw_stream(dev)))
+    return y
+
+
+def cider_w4a4_linear_prequant(qx, w, block_size: int = 32, y_dtype=torch.float16, out=None):
+    """As cider_w4a4_linear for rows that cider_quantize_fp4 has quantized already."""
+    _block(block_size)
+    c, dev, n, k = _fp4_args(w, block_size, "w")
+    a, _, m, kx = _fp4_args(qx, block_size, "qx", dev)
+    if kx != k:
+        raise ValueError(f"qx has {kx} columns, w {k}")
+    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    _launch((_lib or _load()).cider_w4a4_linear_prequant, dev, (a, c, yp, _DTYPES[y_dtype], _raw_stream(dev)))
+    return y
+
+
+def _gate_up(gate, up, block_size, activation):
+    _block(block_size)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
+    g, dev, f, k = _fp4_args(gate, block_size, "gate")
+    u, _, fu, ku = _fp4_args(up, block_size, "up", dev)
+    if (fu, ku) != (f, k):
+        raise ValueError(f"gate is {f} x {k}, up {fu} x {ku}")
+    return g, u, dev, f, k, _ACTIVATIONS[activation]
+
+
+def cider_w4a4_gated_linear(x, gate, up, block_size: int = 32, activation="silu", h_dtype=None, out=None):
+    """h [M, F] of h_dtype (None: x's) = act(x gate^T) * (x up^T): the first half of a
+    gated feed-forward block.  activation: "silu", or "gelu" (by its tanh form)."""
+    g, u, dev, f, k, act = _gate_up(gate, up, block_size, activation)
+    kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
+    h_dtype = x.dtype if h_dtype is None else h_dtype
+    h, hp = _result(out, (m, f), h_dtype, dev, "out")
+    _launch((_lib or _load()).cider_w4a4_gated_linear, dev, (x.data_ptr(), kind, stride, m, g, u, act, hp,
+            _DTYPES[h_dtype], _raw_stream(dev)))
+    return h
+
+
+def cider_w4a4_gated_linear_prequant(qx, gate, up, block_size: int = 32, activation="silu",
+                                     h_dtype=torch.float16, out=None):
+    """As cider_w4a4_gated_linear for rows that cider_quantize_fp4 has quantized already."""
+    g, u, dev, f, k, act = _gate_up(gate, up, block_size, activation)
+    a, _, m, kx = _fp4_args(qx, block_size, "qx", dev)
+    if kx != k:
+        raise ValueError(f"qx has {kx} columns, gate {k}")
+    h, hp = _result(out, (m, f), h_dtype, dev, "out")
+    _launch((_lib or _load()).cider_w4a4_gated_linear_prequant, dev, (a, g, u, act, hp, _DTYPES[h_dtype],
+            _raw_stream(dev)))
+    return h
+
+
+def cider_w4a4_feed_forward(x, gate, up, down, block_size: int = 32, activation="silu", y_dtype=None, out=None):
+    """y [M, N] of y_dtype (None: x's) = h down^T, h = act(x gate^T) * (x up^T) rounded
+    to x's type and quantized: a whole gated feed-forward block."""
+    g, u, dev, f, k, act = _gate_up(gate, up, block_size, activation)
+    d, _, n, fd = _fp4_args(down, block_size, "down", dev)
+    if fd != f:
+        raise ValueError(f"down has {fd} columns, gate {f} rows")
+    kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
+    y_dtype = x.dtype if y_dtype is None else y_dtype
+    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    _launch((_lib or _load()).cider_w4a4_feed_forward, dev, (x.data_ptr(), kind, stride, m, g, u, d, act, yp,
+            _DTYPES[y_dtype], _raw_stream(dev)))
+    return y

@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libcider.so")
 SOURCES = ["cider_api.cu", "quant.cu", "gemv.cu", "gemm_tc.cu", "gemm_pair.cu", "gemm_pg.cu", "noalloc.cu",
-           "kv_api.cu", "kv_cache.cu", "kv_attention.cu", "kv_rows.cu", "kv_tree.cu", "verify.cu"]
-HEADERS = ["cider_device.cuh", "cider_internal.h", "kv_common.cuh", "kv_parts.cuh"]
+           "kv_api.cu", "kv_cache.cu", "kv_attention.cu", "kv_rows.cu", "kv_tree.cu", "verify.cu",
+           "fp4_api.cu", "fp4.cu", "fp4_rows.cu", "fp4_pair.cu"]
+HEADERS = ["cider_device.cuh", "cider_internal.h", "kv_common.cuh", "kv_parts.cuh", "fp4_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,129 @@
+// fp4_common.cuh -- what the kernels of microscaled 4-bit floating point share:
+// the matrix as the host passes it, the block-scaled tcgen05 product and the
+// copies of its scales into tensor memory, the activations.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cider_device.cuh"
+#include "cider_internal.h"
+
+namespace cider {
+
+constexpr int kFpTileRows = 128;    // rows of a tile of block scales
+constexpr int kFpTileBytes = 512;   // a tile: 128 rows x 4 blocks
+constexpr int kFpStageK = 256;      // K of a pipeline stage: rows of 128 bytes, one swizzle span
+constexpr int kFpStepK = 64;        // K of one MMA
+constexpr int kFpSteps = kFpStageK / kFpStepK;
+constexpr uint64_t kFpWaitNs = 2000000000ull;
+
+// Tiles of block scales along K, and those of a stage (BS 16: one a step; 32: one for two steps).
+__host__ __device__ constexpr int fp4_tiles(int64_t K, int block) {
+  return static_cast<int>((K / block + 3) / 4);
+}
+template <int BS>
+struct FpBlock {
+  static constexpr int kTiles = kFpStageK / (4 * BS);         // scale tiles of a stage
+  static constexpr int kBytes = kTiles * kFpTileBytes;        // of 128 rows
+  static constexpr int kCols = kTiles * 4;                    // tensor-memory columns of 128 rows
+};
+
+// One side of a gated product's activation: t(g) of g * sigmoid(t(g)).
+enum FpAct : int { kActSilu = 0, kActGelu = 1 };
+
+#ifdef __CUDACC__
+// 16 * 8 bytes at a time: the scales of 32 rows x 4 blocks of 4 groups of rows,
+// copied to 4 columns of each of the four lane quarters.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8 rows x 16 bytes between groups of 8 rows
+  d |= static_cast<uint64_t>(1u) << 46;          // descriptor version for tcgen05; no swizzle
+  return d;
+}
+// The copy and the MMAs that follow it from the same thread run in the order they are issued in.
+template <int CG>
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4nvf4: E2M1 operands, both K-major, K = 64;
+// scales E4M3 (BS 16) or E8M0 (BS 32), of which `id` 0 or 2 names the two bytes of a step.
+template <int BS>
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, int id) {
+  return (static_cast<uint32_t>(id) << 4) | (1u << 7) | (1u << 10) |
+         (static_cast<uint32_t>(N >> 3) << 17) | ((BS == 32 ? 1u : 0u) << 23) |
+         (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(id) << 29);
+}
+
+// D (+)= (A * its scales) (B * its scales)^T, 64 of K.
+template <int CG, int BS>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+#define CIDER_FP4_MMA(CGS, VEC)                                                                   \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred p;\n\t"                                                                   \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                \
+      "tcgen05.mma.cta_group::" CGS ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                         \
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                            \
+      : "memory")
+  if constexpr (CG == 1 && BS == 16) CIDER_FP4_MMA("1", "4X");
+  if constexpr (CG == 1 && BS == 32) CIDER_FP4_MMA("1", "2X");
+  if constexpr (CG == 2 && BS == 16) CIDER_FP4_MMA("2", "4X");
+  if constexpr (CG == 2 && BS == 32) CIDER_FP4_MMA("2", "2X");
+#undef CIDER_FP4_MMA
+}
+
+// act(g) * u with act(g) = g / (1 + e^-t): t = g (SiLU), or t = 2 sqrt(2 / pi) (g + 0.044715 g^3),
+// for which g / (1 + e^-t) = g (1 + tanh(t / 2)) / 2 (GELU).  2^x and the reciprocal are the
+// hardware's approximations (2 ulp each), far below the 16-bit result's half step.
+__device__ __forceinline__ float gated(float g, float u, int act) {
+  const float t = act == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+#endif
+
+// A quantized matrix, as the host passes it on.
+struct FpMat {
+  const uint8_t* codes = nullptr;
+  const uint8_t* scales = nullptr;
+  const float* row = nullptr;
+  int64_t rows = 0;
+};
+
+// fp4.cu.  x of dtype (cider_dtype_t), x_stride elements between rows.  pad: the scales of the rows
+// behind the last one in its tile are written too, as zeros (a product does not need them: they
+// reach only outputs that it does not store).  release: as in quant.cu.
+cudaError_t launch_quantize_fp4(const void* x, int dtype, int64_t x_stride, int64_t rows, int64_t K,
+                                int block, uint8_t* codes, uint8_t* scales, float* row, bool pad,
+                                cudaStream_t st, bool release);
+cudaError_t launch_dequantize_fp4(const FpMat& q, int64_t K, int block, void* x, int dtype,
+                                  cudaStream_t st);
+
+// One product: y = x w^T, or with `up` h = act(x w^T) (x up^T).
+struct FpProduct {
+  FpMat x, w, up;
+  int64_t M = 0, N = 0, K = 0;
+  int block = 0;
+  bool is_gated = false;
+  int act = kActSilu;
+  void* y = nullptr;
+  bool y_bf16 = false;
+  bool after_launch = false;   // the launch just before is this call's own: overlap with its end
+  int num_sms = 0;
+  cudaStream_t st = nullptr;
+};
+// fp4_rows.cu: 128 rows of weights against all (up to 256) tokens, K split over a cluster.
+cudaError_t launch_fp4_rows(const FpProduct& p);
+// fp4_pair.cu: 256 tokens x 256 weight rows on a CTA pair.
+cudaError_t launch_fp4_pair(const FpProduct& p);
+
+}  // namespace cider
