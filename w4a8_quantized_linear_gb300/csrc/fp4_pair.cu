@@ -81,7 +81,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + C::kBars + 8 * C::kNumBars + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = blockIdx.x & 1;   // of the pair; known to be the same for all threads
   const int cid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -146,42 +146,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (rank == 0 && lane == 0) {
-      int it = 0, n = 0;
+    if (rank == 0) {
+      int n = 0, s = 0;
+      uint32_t phase = 0;
       bool go = true;
       for (int tile = cid; tile < p.tiles && go; tile += pairs, ++n) {
         const uint32_t d = tmem + ((n & 1) ? C::kAcc1 : 0);
         // the tile before has given up the columns that its accumulator shares with this one's
         // (and, earlier, everything of the tile before that)
-        if (n > 0 && !mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)) break;
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const int s = it % S;
-          if (!mbar_wait_bounded(full_bar(s), (it / S) & 1, abort_flag, p.err, kFpWaitNs)) {
+        if (n > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)))
+          break;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs))) {
             go = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = base + s * C::kStage;
-#pragma unroll
-          for (int a = 0; a < B::kTiles; ++a) {
-            tc_cp_scales<2>(tmem + C::kColX + 4 * a, smem_desc_scales(at + C::kSfx + a * kFpTileBytes));
-            tc_cp_scales<2>(tmem + C::kColW + 8 * a, smem_desc_scales(at + C::kSfw + a * kFpTileBytes));
-            tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, smem_desc_scales(at + C::kSfw + B::kBytes + a * kFpTileBytes));
-          }
           const int steps = min(kFpSteps, p.nsteps - kb * kFpSteps);
-          const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
+          if (elect_one()) {
+            const uint32_t at = base + s * C::kStage;
+            const uint64_t dx = smem_desc_scales(at + C::kSfx), dw = smem_desc_scales(at + C::kSfw);
 #pragma unroll
-          for (int j = 0; j < kFpSteps; ++j) {
-            if (j >= steps) break;
-            const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
-            tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, 256, id), tmem + C::kColX + 4 * a,
-                              tmem + C::kColW + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
+            for (int a = 0; a < B::kTiles; ++a) {
+              tc_cp_scales<2>(tmem + C::kColX + 4 * a, dx + a * (kFpTileBytes >> 4));
+              tc_cp_scales<2>(tmem + C::kColW + 8 * a, dw + a * (kFpTileBytes >> 4));
+              tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
+            }
+            const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
+#pragma unroll
+            for (int j = 0; j < kFpSteps; ++j) {
+              if (j >= steps) break;
+              const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
+              tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, 256, id), tmem + C::kColX + 4 * a,
+                                tmem + C::kColW + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
+            }
+            tc_commit_pair_mc(empty_bar(s), 0x3);
+            if (kb == p.nkb - 1) tc_commit_pair_mc(accf_bar0 + 8u * (n & 1), 0x3);
           }
-          tc_commit_pair_mc(empty_bar(s), 0x3);
+          __syncwarp();
+          if (++s == S) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
-        if (go) tc_commit_pair_mc(accf_bar0 + 8u * (n & 1), 0x3);
       }
-      tc_commit_pair_mc(done_bar, 0x3);
+      if (elect_one()) tc_commit_pair_mc(done_bar, 0x3);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue

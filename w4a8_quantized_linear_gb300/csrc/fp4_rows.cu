@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + ring + 8 * kRBars + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  // the rank in the cluster; of blockIdx, so that the compiler knows it to be the same for all threads
+  const int rank = static_cast<int>(blockIdx.x) % p.splits;
   const int unit = blockIdx.x / p.splits;
   const int mt = unit % p.m_tiles, nt = unit / p.m_tiles;
   const int m0 = mt * p.tn;
@@ -129,25 +130,30 @@ __global__ void __launch_bounds__(kRThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t sfw = tmem + acc_cols, sfu = sfw + B::kCols, sft = sfw + (GATED ? 2 : 1) * B::kCols;
-      const int tcols = 4 * p.tok_tiles;   // columns of the tokens' scales of one tile of K
-      for (int i = 0; kb0 + i < kb1; ++i) {
-        const int s = i % p.stages;
-        if (!mbar_wait_bounded(full_bar(s), (i / p.stages) & 1, abort_flag, p.err, kFpWaitNs)) break;
-        tc_fence_after();
+    const uint32_t sfw = tmem + acc_cols, sfu = sfw + B::kCols, sft = sfw + (GATED ? 2 : 1) * B::kCols;
+    const uint32_t tcols = 4 * p.tok_tiles;   // columns of the tokens' scales of one tile of K
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < kb1 - kb0; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs))) break;
+      tc_fence_after();
+      const int steps = min(kFpSteps, p.nsteps - (kb0 + i) * kFpSteps);
+      if (elect_one()) {
         const uint32_t at = base + s * p.stage_bytes;
+        const uint64_t dw = smem_desc_scales(at + p.sfw_offset), du = smem_desc_scales(at + p.sfu_offset),
+                       dt = smem_desc_scales(at + p.sft_offset);
+#pragma unroll
         for (int a = 0; a < B::kTiles; ++a) {
-          tc_cp_scales<1>(sfw + 4 * a, smem_desc_scales(at + p.sfw_offset + a * kFpTileBytes));
-          if (GATED) tc_cp_scales<1>(sfu + 4 * a, smem_desc_scales(at + p.sfu_offset + a * kFpTileBytes));
-          for (int t = 0; t < p.tok_tiles; ++t)
-            tc_cp_scales<1>(sft + tcols * a + 4 * t,
-                            smem_desc_scales(at + p.sft_offset + t * B::kBytes + a * kFpTileBytes));
+          tc_cp_scales<1>(sfw + 4 * a, dw + a * (kFpTileBytes >> 4));
+          if (GATED) tc_cp_scales<1>(sfu + 4 * a, du + a * (kFpTileBytes >> 4));
+          tc_cp_scales<1>(sft + tcols * a, dt + a * (kFpTileBytes >> 4));
+          if (p.tok_tiles == 2) tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         }
-        const int steps = min(kFpSteps, p.nsteps - (kb0 + i) * kFpSteps);
         const uint64_t wd = smem_desc_k_sw128(at), ud = smem_desc_k_sw128(at + kROperand),
                        td = smem_desc_k_sw128(at + p.tok_offset);
-        for (int j = 0; j < steps; ++j) {
+#pragma unroll
+        for (int j = 0; j < kFpSteps; ++j) {
+          if (j >= steps) break;
           const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
           const uint32_t idesc = idesc_fp4<BS>(128, p.tn, id);
           const uint32_t acc = (i > 0 || j > 0) ? 1u : 0u;
@@ -156,8 +162,13 @@ __global__ void __launch_bounds__(kRThreads, 1)
         }
         tc_commit(empty_bar(s));
       }
-      tc_commit(acc_bar);
+      __syncwarp();
+      if (++s == p.stages) {
+        s = 0;
+        phase ^= 1u;
+      }
     }
+    if (elect_one()) tc_commit(acc_bar);
     __syncwarp();
   }
   // ---------------------------------------------------------------- sums

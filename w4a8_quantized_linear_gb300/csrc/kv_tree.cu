@@ -285,19 +285,6 @@ __device__ __forceinline__ uint4 convert_unit(const uint4& c, int h) {
   return r;
 }
 
-// One lane of a converged warp, the same one each time.  The compiler knows the
-// pattern: behind a comparison of the lane number it elects a lane again for
-// every MMA.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
 // The MMAs of a tile in stage ST: S = Q K^T, and O (+)= P V.
 template <typename C, int ST>
 __device__ __forceinline__ void issue_s(uint32_t sbase) {
