@@ -105,45 +105,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   pdl_wait();   // codes and scales of x come from the launch just before
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kBars + 8 * C::kNumBars);
+  constexpr uint32_t tmem = 0;   // the CTA holds all columns
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(full_bar(0), 0);
-      int it = 0;
-      bool go = true;
-      for (int tile = cid; tile < p.tiles && go; tile += pairs) {
-        const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const int s = it % S;
-          if (!mbar_wait_bounded(empty_bar(s), ((it / S) & 1) ^ 1u, abort_flag, p.err, kFpWaitNs)) {
-            go = false;
-            break;
-          }
+    const uint32_t full0 = mapa_shared(full_bar(0), 0);
+    int s = 0, it = 0;
+    uint32_t phase = 1;
+    bool go = true;
+    for (int tile = cid; tile < p.tiles && go; tile += pairs) {
+      const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(s), phase, abort_flag, p.err, kFpWaitNs))) {
+          go = false;
+          break;
+        }
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kLoaded);
           const uint32_t at = base + s * C::kStage, bar = full0 + 8u * s;
           const int sk = kb * (B::kBytes / 8);
           tma_load_2d_pair(at, &tm_x, bar, kb * 128, mt * 256 + rank * 128);
+          if (GATED) {
+            if (rank == 0)
+              tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 128);
+            else
+              tma_load_2d_pair(at + kFOperand, &tm_u, bar, kb * 128, nt * 128);
+          } else {
+            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
+          }
           tma_load_2d_pair(at + C::kSfx, &tm_sx, bar, sk, mt * 2 + rank);
           if (GATED) {
-            tma_load_2d_pair(at + kFOperand, rank == 0 ? &tm_w : &tm_u, bar, kb * 128, nt * 128);
             tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt);
             tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_su, bar, sk, nt);
           } else {
-            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
             tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt * 2);
             tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, nt * 2 + 1);
           }
         }
-      }
-      // both CTAs' copies have landed before either leaves, also after a wait that gave up
-      if (rank == 0) {
-        volatile uint32_t keep_waiting = 0u;
-        for (int j = max(0, it - S); j < it; ++j)
-          mbar_wait_bounded(full_bar(j % S), (j / S) & 1, &keep_waiting, p.err, kFpWaitNs);
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
     }
+    // both CTAs' copies have landed before either leaves, also after a wait that gave up
+    if (rank == 0) {
+      volatile uint32_t keep_waiting = 0u;
+      for (int j = max(0, it - S); j < it; ++j)
+        mbar_wait_bounded(full_bar(j % S), (j / S) & 1, &keep_waiting, p.err, kFpWaitNs);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
     if (rank == 0) {
