@@ -461,6 +461,12 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
 }
 
 // ---------------------------------------------------------------- outputs
+// 32 bytes to a 32-byte boundary of global memory.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // The bits of one output value: the fp32 result rounded once to fp16 or to
 // bf16 (round to nearest even either way).
 template <bool BF16>

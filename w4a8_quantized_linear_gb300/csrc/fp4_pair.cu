@@ -26,9 +26,7 @@ namespace cider {
 namespace {
 
 constexpr int kFThreads = 192;
-constexpr int kFStages = 5;
 constexpr int kFOperand = 128 * 128;             // bytes of 128 rows of a stage's codes
-constexpr int kFOut = 4 * 2 * 4096;              // 4 warps x 2 buffers x 32 rows x 128 bytes
 constexpr int kFTmemCols = 512;
 
 template <int BS>
@@ -38,10 +36,10 @@ struct FCfg {
   static constexpr int kSfw = kSfx + B::kBytes;                // both halves' weight scales
   static constexpr int kStage = (kSfw + 2 * B::kBytes + 1023) / 1024 * 1024;
   static constexpr int kLoaded = kSfw + 2 * B::kBytes;         // bytes that a CTA loads a stage
-  static constexpr int kOut = kFStages * kStage;
-  static constexpr int kRowScale = kOut + kFOut;               // 2 tiles x 256 fp32
+  static constexpr int kStages = 230000 / kStage;
+  static constexpr int kRowScale = kStages * kStage;           // 2 tiles x 256 fp32
   static constexpr int kBars = kRowScale + 2 * 256 * 4;
-  static constexpr int kNumBars = 2 * kFStages + 4;
+  static constexpr int kNumBars = 2 * kStages + 4;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;
   static constexpr int kColX = kFTmemCols - 3 * B::kCols;      // scales at the end of tensor memory
   static constexpr int kColW = kColX + B::kCols;
@@ -54,6 +52,8 @@ struct FPairArgs {
   int m_tiles, tiles;
   int nkb, nsteps;
   const float *sx, *sw, *su;
+  uint16_t* y;
+  int wide;          // rows of y start at 32-byte boundaries
   int y_bf16, act;
   int* err;
 };
@@ -63,10 +63,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_sx,
                     const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_su,
-                    const __grid_constant__ CUtensorMap tm_y, const FPairArgs p) {
+                    const FPairArgs p) {
   using C = FCfg<BS>;
   using B = FpBlock<BS>;
-  constexpr int S = kFStages;
+  constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     const uint32_t acce0 = mapa_shared(acce_bar, 0);
     float* scale = reinterpret_cast<float*>(gbase + C::kRowScale);
     constexpr int kCols = GATED ? 128 : 256;   // outputs of a tile's row
-    int n = 0, buf = 0;
+    int n = 0;
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
       const int m0 = mt * 256 + static_cast<int>(rank) * 128, m = m0 + row, n0 = nt * kCols;
@@ -261,25 +261,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           }
           h[j] = p.y_bf16 ? y_bits2<true>(a, b) : y_bits2<false>(a, b);
         }
-        // the buffer's store of two turns ago has read it
-        if (lane == 0) bulk_wait_group_read<1>();
-        __syncwarp();
-        const uint32_t out = base + C::kOut + (q * 2 + buf) * 4096;
+        if (m < p.M) {
+          uint16_t* out = p.y + static_cast<int64_t>(m) * p.N + n0 + c;
+          if (p.wide) {   // N % 16 == 0: sixteen outputs are all in or all out
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t x[4] = {h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]};
-          st_shared_v4(out + lane * 128 + ((j ^ (lane & 7)) << 4), x);
+            for (int j = 0; j < 4; ++j)
+              if (n0 + c + 16 * j < p.N) st_global_v8(out + 16 * j, h + 8 * j);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (n0 + c + 8 * j < p.N)
+                *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (m0 + q * 32 < p.M && n0 + c < p.N) tma_store_2d(&tm_y, out, n0 + c, m0 + q * 32);
-          bulk_commit_group();
-        }
-        buf ^= 1;
       }
     }
-    if (lane == 0) bulk_wait_group<0>();
   }
   __syncwarp();
   if (warp == 1) {
@@ -319,11 +315,13 @@ cudaError_t launch(const FpProduct& p) {
   a.sx = p.x.row;
   a.sw = p.w.row;
   a.su = p.up.row;
+  a.y = static_cast<uint16_t*>(p.y);
+  a.wide = reinterpret_cast<uintptr_t>(p.y) % 32 == 0 && p.N % 16 == 0;
   a.y_bf16 = p.y_bf16;
   a.act = p.act;
   e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
-  CUtensorMap mx, mw, mu, msx, msw, msu, my;
+  CUtensorMap mx, mw, mu, msx, msw, msu;
   auto codes = [&](CUtensorMap* m, const FpMat& q) {
     return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, 128,
                               CU_TENSOR_MAP_SWIZZLE_128B);
@@ -335,9 +333,7 @@ cudaError_t launch(const FpProduct& p) {
   };
   const FpMat& up = GATED ? p.up : p.w;
   if (!codes(&mx, p.x) || !codes(&mw, p.w) || !codes(&mu, up) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
-      !scales(&msu, up) ||
-      !make_tensor_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.y, p.N, p.M, p.N * 2, 64, 32,
-                          CU_TENSOR_MAP_SWIZZLE_128B))
+      !scales(&msu, up))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kFThreads, 1, 1);
@@ -366,7 +362,7 @@ cudaError_t launch(const FpProduct& p) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, mx, mw, mu, msx, msw, msu, my, a);
+  return cudaLaunchKernelEx(&cfg, kern, mx, mw, mu, msx, msw, msu, a);
 }
 
 }  // namespace
