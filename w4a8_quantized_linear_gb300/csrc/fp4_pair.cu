@@ -26,25 +26,34 @@ namespace cider {
 namespace {
 
 constexpr int kFThreads = 192;
-constexpr int kFOperand = 128 * 128;             // bytes of 128 rows of a stage's codes
+constexpr int kFOperand = 128 * 128;             // bytes of a stage's codes of 128 tokens
+constexpr int kFOut = 4 * 4096;                  // 4 warps x 32 rows x 128 bytes
 constexpr int kFTmemCols = 512;
 
-template <int BS>
+template <bool GATED, int BS>
 struct FCfg {
   using B = FpBlock<BS>;
-  static constexpr int kSfx = 2 * kFOperand;                   // tokens' scales
-  static constexpr int kSfw = kSfx + B::kBytes;                // both halves' weight scales
-  static constexpr int kStage = (kSfw + 2 * B::kBytes + 1023) / 1024 * 1024;
+  static constexpr int kTileN = GATED ? 256 : 192;             // the MMA's N
+  static constexpr int kOutN = GATED ? 128 : 192;              // outputs of a token in a tile
+  static constexpr int kRowsW = kTileN / 2;                    // weight rows that a CTA loads
+  static constexpr int kSfx = kFOperand + kRowsW * 128;        // tokens' scales
+  static constexpr int kSfw = kSfx + B::kBytes;                // the weights', two tiles
   static constexpr int kLoaded = kSfw + 2 * B::kBytes;         // bytes that a CTA loads a stage
-  static constexpr int kStages = 230000 / kStage;
-  static constexpr int kRowScale = kStages * kStage;           // 2 tiles x 256 fp32
+  static constexpr int kStage = (kLoaded + 1023) / 1024 * 1024;
+  static constexpr int kStages = (232448 - 1024 - 512 - kFOut - 2 * 256 * 4) / kStage;
+  static constexpr int kOut = kStages * kStage;
+  static constexpr int kRowScale = kOut + kFOut;               // 2 tiles x 256 fp32
   static constexpr int kBars = kRowScale + 2 * 256 * 4;
-  static constexpr int kNumBars = 2 * kStages + 4;
+  static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;
-  static constexpr int kColX = kFTmemCols - 3 * B::kCols;      // scales at the end of tensor memory
+  // tensor memory: two accumulators, at its end the scales.  Gated, the accumulators share columns.
+  static constexpr int kColX = kFTmemCols - 3 * B::kCols;
   static constexpr int kColW = kColX + B::kCols;
-  static constexpr int kAcc1 = kColX - 256;                    // the second accumulator
+  static constexpr bool kShared = 2 * kTileN > kColX;
+  static constexpr int kAcc1 = kShared ? kColX - kTileN : kTileN;
   static_assert(kSmem <= 232448, "shared memory budget");
+  // the shared columns are among the first 64 outputs that are drained
+  static_assert(!kShared || kTileN - kAcc1 <= 64, "shared columns");
 };
 
 struct FPairArgs {
@@ -52,8 +61,6 @@ struct FPairArgs {
   int m_tiles, tiles;
   int nkb, nsteps;
   const float *sx, *sw, *su;
-  uint16_t* y;
-  int wide;          // rows of y start at 32-byte boundaries
   int y_bf16, act;
   int* err;
 };
@@ -63,8 +70,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_sx,
                     const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_su,
-                    const FPairArgs p) {
-  using C = FCfg<BS>;
+                    const __grid_constant__ CUtensorMap tm_y, const FPairArgs p) {
+  using C = FCfg<GATED, BS>;
   using B = FpBlock<BS>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -75,8 +82,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
   const uint32_t accf_bar0 = bars + 8u * (2 * S);       // x 2, one per accumulator
-  const uint32_t acce_bar = bars + 8u * (2 * S + 2);    // the next tile may start
-  const uint32_t done_bar = bars + 8u * (2 * S + 3);
+  const uint32_t acce_bar0 = bars + 8u * (2 * S + 2);   // x 2: drained, as far as the next tile needs it
+  const uint32_t done_bar = bars + 8u * (2 * S + 4);
   const uint32_t tmem_slot = bars + 8u * C::kNumBars;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + C::kBars + 8 * C::kNumBars + 4);
 
@@ -91,7 +98,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     }
     mbar_init(accf_bar0, 1);
     mbar_init(accf_bar0 + 8, 1);
-    mbar_init(acce_bar, 8);   // 4 warps x 2 CTAs
+    mbar_init(acce_bar0, 8);   // 4 warps x 2 CTAs
+    mbar_init(acce_bar0 + 8, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -131,15 +139,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             else
               tma_load_2d_pair(at + kFOperand, &tm_u, bar, kb * 128, nt * 128);
           } else {
-            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
+            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * C::kTileN + rank * C::kRowsW);
           }
           tma_load_2d_pair(at + C::kSfx, &tm_sx, bar, sk, mt * 2 + rank);
           if (GATED) {
             tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt);
             tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_su, bar, sk, nt);
           } else {
-            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt * 2);
-            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, nt * 2 + 1);
+            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, (nt * C::kTileN) >> 7);
+            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, ((nt * C::kTileN) >> 7) + 1);
           }
         }
         __syncwarp();
@@ -158,60 +166,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (rank == 0) {
+    // One elected lane runs the whole loop: a vote and an election per stage cost it 150 cycles of a
+    // stage's 512.
+    if (rank == 0 && elect_one()) {
       int n = 0, s = 0;
       uint32_t phase = 0;
       bool go = true;
       for (int tile = cid; tile < p.tiles && go; tile += pairs, ++n) {
         const uint32_t d = tmem + ((n & 1) ? C::kAcc1 : 0);
-        // the tile before has given up the columns that its accumulator shares with this one's
-        // (and, earlier, everything of the tile before that)
-        if (n > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)))
+        // scales of weight rows that start in the middle of a tile of 128 (every other tile of 192)
+        const uint32_t sfw = tmem + C::kColW + (GATED ? 0 : ((tile / p.m_tiles) & 1) * 2);
+        // the accumulator is free: its last tile is drained; sharing columns, those of the tile before
+        // are (and, before them, everything of its own last tile)
+        const int before = C::kShared ? n - 1 : n - 2;
+        if (before >= 0 &&
+            !mbar_wait_bounded(acce_bar0 + 8u * (before & 1), (before >> 1) & 1, abort_flag, p.err, kFpWaitNs))
           break;
         for (int kb = 0; kb < p.nkb; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs))) {
+          if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) {
             go = false;
             break;
           }
           tc_fence_after();
           const int steps = min(kFpSteps, p.nsteps - kb * kFpSteps);
-          if (elect_one()) {
-            const uint32_t at = base + s * C::kStage;
-            const uint64_t dx = smem_desc_scales(at + C::kSfx), dw = smem_desc_scales(at + C::kSfw);
+          const uint32_t at = base + s * C::kStage;
+          const uint64_t dx = smem_desc_scales(at + C::kSfx), dw = smem_desc_scales(at + C::kSfw);
 #pragma unroll
-            for (int a = 0; a < B::kTiles; ++a) {
-              tc_cp_scales<2>(tmem + C::kColX + 4 * a, dx + a * (kFpTileBytes >> 4));
-              tc_cp_scales<2>(tmem + C::kColW + 8 * a, dw + a * (kFpTileBytes >> 4));
-              tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
-            }
-            const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
-#pragma unroll
-            for (int j = 0; j < kFpSteps; ++j) {
-              if (j >= steps) break;
-              const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
-              tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, 256, id), tmem + C::kColX + 4 * a,
-                                tmem + C::kColW + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
-            }
-            tc_commit_pair_mc(empty_bar(s), 0x3);
-            if (kb == p.nkb - 1) tc_commit_pair_mc(accf_bar0 + 8u * (n & 1), 0x3);
+          for (int a = 0; a < B::kTiles; ++a) {
+            tc_cp_scales<2>(tmem + C::kColX + 4 * a, dx + a * (kFpTileBytes >> 4));
+            tc_cp_scales<2>(tmem + C::kColW + 8 * a, dw + a * (kFpTileBytes >> 4));
+            tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
           }
-          __syncwarp();
+          const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
+#pragma unroll
+          for (int j = 0; j < kFpSteps; ++j) {
+            if (j >= steps) break;
+            const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
+            tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, C::kTileN, id), tmem + C::kColX + 4 * a,
+                              sfw + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
+          }
+          tc_commit_pair_mc(empty_bar(s), 0x3);
           if (++s == S) {
             s = 0;
             phase ^= 1u;
           }
         }
+        if (go) tc_commit_pair_mc(accf_bar0 + 8u * (n & 1), 0x3);
       }
-      if (elect_one()) tc_commit_pair_mc(done_bar, 0x3);
-      __syncwarp();
+      tc_commit_pair_mc(done_bar, 0x3);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, row = q * 32 + lane, e = threadIdx.x - 64;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t acce0 = mapa_shared(acce_bar, 0);
+    const uint32_t acce0 = mapa_shared(acce_bar0, 0);
     float* scale = reinterpret_cast<float*>(gbase + C::kRowScale);
-    constexpr int kCols = GATED ? 128 : 256;   // outputs of a tile's row
+    constexpr int kCols = C::kOutN, kTurns = kCols / 64;
     int n = 0;
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
@@ -231,11 +242,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
         break;
       tc_fence_after();
       const uint32_t d = tmem + lane_base + ((n & 1) ? C::kAcc1 : 0);
-      // 64 outputs a turn, first those whose columns the next tile's accumulator shares: the last
-      // ones of the first accumulator, the first ones of the second
+      // 64 outputs a turn; where accumulators share columns, those first: the last ones of the first
+      // accumulator, the first ones of the second
 #pragma unroll 1
-      for (int i = 0; i < kCols / 64; ++i) {
-        const int c = 64 * ((n & 1) ? i : kCols / 64 - 1 - i);
+      for (int i = 0; i < kTurns; ++i) {
+        const int c = 64 * (!C::kShared || (n & 1) ? i : kTurns - 1 - i);
         uint32_t v[64], u[GATED ? 64 : 1];
         tmem_ld32(d + c, *reinterpret_cast<uint32_t(*)[32]>(v));
         tmem_ld32(d + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
@@ -244,10 +255,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           tmem_ld32(d + 160 + c, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
         }
         tmem_wait_ld();
-        if (i == 0) {
+        if (i == (C::kShared ? 0 : kTurns - 1)) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(acce0);
+          if (lane == 0) mbar_arrive_remote(acce0 + 8u * (n & 1));
         }
         uint32_t h[32];
 #pragma unroll
@@ -261,21 +272,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           }
           h[j] = p.y_bf16 ? y_bits2<true>(a, b) : y_bits2<false>(a, b);
         }
-        if (m < p.M) {
-          uint16_t* out = p.y + static_cast<int64_t>(m) * p.N + n0 + c;
-          if (p.wide) {   // N % 16 == 0: sixteen outputs are all in or all out
+        // the last turn's store has read the buffer
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        const uint32_t out = base + C::kOut + q * 4096;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (n0 + c + 16 * j < p.N) st_global_v8(out + 16 * j, h + 8 * j);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (n0 + c + 8 * j < p.N)
-                *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x[4] = {h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]};
+          st_shared_v4(out + lane * 128 + ((j ^ (lane & 7)) << 4), x);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (m0 + q * 32 < p.M && n0 + c < p.N) tma_store_2d(&tm_y, out, n0 + c, m0 + q * 32);
+          bulk_commit_group();
         }
       }
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
   __syncwarp();
   if (warp == 1) {
@@ -297,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
 
 template <bool GATED, int BS>
 cudaError_t launch(const FpProduct& p) {
-  using C = FCfg<BS>;
+  using C = FCfg<GATED, BS>;
   using B = FpBlock<BS>;
   auto kern = fp4_pair_kernel<GATED, BS>;
   static std::atomic<uint64_t> done{0};
@@ -307,7 +321,7 @@ cudaError_t launch(const FpProduct& p) {
   a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
   a.m_tiles = static_cast<int>((p.M + 255) / 256);
-  const int64_t tiles = a.m_tiles * (GATED ? (p.N + 127) / 128 : (p.N + 255) / 256);
+  const int64_t tiles = a.m_tiles * ((p.N + C::kOutN - 1) / C::kOutN);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
   a.tiles = static_cast<int>(tiles);
   a.nkb = static_cast<int>((p.K + kFpStageK - 1) / kFpStageK);
@@ -315,15 +329,13 @@ cudaError_t launch(const FpProduct& p) {
   a.sx = p.x.row;
   a.sw = p.w.row;
   a.su = p.up.row;
-  a.y = static_cast<uint16_t*>(p.y);
-  a.wide = reinterpret_cast<uintptr_t>(p.y) % 32 == 0 && p.N % 16 == 0;
   a.y_bf16 = p.y_bf16;
   a.act = p.act;
   e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
-  CUtensorMap mx, mw, mu, msx, msw, msu;
-  auto codes = [&](CUtensorMap* m, const FpMat& q) {
-    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, 128,
+  CUtensorMap mx, mw, mu, msx, msw, msu, my;
+  auto codes = [&](CUtensorMap* m, const FpMat& q, int rows) {
+    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, rows,
                               CU_TENSOR_MAP_SWIZZLE_128B);
   };
   auto scales = [&](CUtensorMap* m, const FpMat& q) {
@@ -332,8 +344,10 @@ cudaError_t launch(const FpProduct& p) {
                               B::kBytes / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   };
   const FpMat& up = GATED ? p.up : p.w;
-  if (!codes(&mx, p.x) || !codes(&mw, p.w) || !codes(&mu, up) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
-      !scales(&msu, up))
+  if (!codes(&mx, p.x, 128) || !codes(&mw, p.w, C::kRowsW) || !codes(&mu, up, C::kRowsW) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
+      !scales(&msu, up) ||
+      !make_tensor_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.y, p.N, p.M, p.N * 2, 64, 32,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kFThreads, 1, 1);
@@ -362,7 +376,7 @@ cudaError_t launch(const FpProduct& p) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, mx, mw, mu, msx, msw, msu, a);
+  return cudaLaunchKernelEx(&cfg, kern, mx, mw, mu, msx, msw, msu, my, a);
 }
 
 }  // namespace
