@@ -166,8 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    // One elected lane runs the whole loop: a vote and an election per stage cost it 150 cycles of a
-    // stage's 512.
+    // One elected lane runs the whole loop: a vote and an election per stage would cost it 150 cycles
+    // of a stage's 512.
     if (rank == 0 && elect_one()) {
       int n = 0, s = 0;
       uint32_t phase = 0;
@@ -198,12 +198,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
           }
           const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
-#pragma unroll
-          for (int j = 0; j < kFpSteps; ++j) {
-            if (j >= steps) break;
+          auto step = [&](int j) {
             const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
             tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, C::kTileN, id), tmem + C::kColX + 4 * a,
                               sfw + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
+          };
+          if (steps == kFpSteps) {   // without a test per MMA, which would cost more than the MMA's issue
+#pragma unroll
+            for (int j = 0; j < kFpSteps; ++j) step(j);
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j) step(j);
           }
           tc_commit_pair_mc(empty_bar(s), 0x3);
           if (++s == S) {

@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(kRThreads, 1)
     // ------------------------------------------------------------ MMAs
     const uint32_t sfw = tmem + acc_cols, sfu = sfw + B::kCols, sft = sfw + (GATED ? 2 : 1) * B::kCols;
     const uint32_t tcols = 4 * p.tok_tiles;   // columns of the tokens' scales of one tile of K
-    int s = 0;
-    uint32_t phase = 0;
-    for (int i = 0; i < kb1 - kb0; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs))) break;
-      tc_fence_after();
-      const int steps = min(kFpSteps, p.nsteps - (kb0 + i) * kFpSteps);
-      if (elect_one()) {
+    if (elect_one()) {   // one lane runs the whole loop
+      int s = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) break;
+        tc_fence_after();
+        const int steps = min(kFpSteps, p.nsteps - (kb0 + i) * kFpSteps);
         const uint32_t at = base + s * p.stage_bytes;
         const uint64_t dw = smem_desc_scales(at + p.sfw_offset), du = smem_desc_scales(at + p.sfu_offset),
                        dt = smem_desc_scales(at + p.sft_offset);
@@ -147,28 +147,35 @@ __global__ void __launch_bounds__(kRThreads, 1)
           tc_cp_scales<1>(sfw + 4 * a, dw + a * (kFpTileBytes >> 4));
           if (GATED) tc_cp_scales<1>(sfu + 4 * a, du + a * (kFpTileBytes >> 4));
           tc_cp_scales<1>(sft + tcols * a, dt + a * (kFpTileBytes >> 4));
-          if (p.tok_tiles == 2) tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         }
+        if (p.tok_tiles == 2)
+#pragma unroll
+          for (int a = 0; a < B::kTiles; ++a)
+            tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         const uint64_t wd = smem_desc_k_sw128(at), ud = smem_desc_k_sw128(at + kROperand),
                        td = smem_desc_k_sw128(at + p.tok_offset);
-#pragma unroll
-        for (int j = 0; j < kFpSteps; ++j) {
-          if (j >= steps) break;
+        auto step = [&](int j) {
           const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
           const uint32_t idesc = idesc_fp4<BS>(128, p.tn, id);
           const uint32_t acc = (i > 0 || j > 0) ? 1u : 0u;
           tc_mma_fp4<1, BS>(tmem, wd + 2 * j, td + 2 * j, idesc, sfw + 4 * a, sft + tcols * a, acc);
           if (GATED) tc_mma_fp4<1, BS>(tmem + p.tn, ud + 2 * j, td + 2 * j, idesc, sfu + 4 * a, sft + tcols * a, acc);
+        };
+        if (steps == kFpSteps) {   // without a test per MMA, which would cost more than the MMA's issue
+#pragma unroll
+          for (int j = 0; j < kFpSteps; ++j) step(j);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < steps; ++j) step(j);
         }
         tc_commit(empty_bar(s));
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      __syncwarp();
-      if (++s == p.stages) {
-        s = 0;
-        phase ^= 1u;
-      }
+      tc_commit(acc_bar);
     }
-    if (elect_one()) tc_commit(acc_bar);
     __syncwarp();
   }
   // ---------------------------------------------------------------- sums
