@@ -19,6 +19,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "fp4_common.cuh"
 
@@ -30,30 +31,25 @@ constexpr int kFOperand = 128 * 128;             // bytes of a stage's codes of 
 constexpr int kFOut = 4 * 4096;                  // 4 warps x 32 rows x 128 bytes
 constexpr int kFTmemCols = 512;
 
-template <bool GATED, int BS>
+template <int BS>
 struct FCfg {
   using B = FpBlock<BS>;
-  static constexpr int kTileN = GATED ? 256 : 192;             // the MMA's N
-  static constexpr int kOutN = GATED ? 128 : 192;              // outputs of a token in a tile
-  static constexpr int kRowsW = kTileN / 2;                    // weight rows that a CTA loads
-  static constexpr int kSfx = kFOperand + kRowsW * 128;        // tokens' scales
+  static constexpr int kSfx = 2 * kFOperand;                   // tokens' scales
   static constexpr int kSfw = kSfx + B::kBytes;                // the weights', two tiles
-  static constexpr int kLoaded = kSfw + 2 * B::kBytes;         // bytes that a CTA loads a stage
-  static constexpr int kStage = (kLoaded + 1023) / 1024 * 1024;
+  static constexpr int kStage = kSfw + 2 * B::kBytes;          // bytes that a CTA loads a stage
   static constexpr int kStages = (232448 - 1024 - 512 - kFOut - 2 * 256 * 4) / kStage;
   static constexpr int kOut = kStages * kStage;
   static constexpr int kRowScale = kOut + kFOut;               // 2 tiles x 256 fp32
   static constexpr int kBars = kRowScale + 2 * 256 * 4;
-  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kNumBars = 2 * kStages + 4;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;
-  // tensor memory: two accumulators, at its end the scales.  Gated, the accumulators share columns.
+  // tensor memory: an accumulator, another one that shares its last columns, the scales
   static constexpr int kColX = kFTmemCols - 3 * B::kCols;
   static constexpr int kColW = kColX + B::kCols;
-  static constexpr bool kShared = 2 * kTileN > kColX;
-  static constexpr int kAcc1 = kShared ? kColX - kTileN : kTileN;
+  static constexpr int kAcc1 = kColX - 256;
+  static_assert(kStage % 1024 == 0, "stages must keep 1024-byte alignment for the swizzle");
   static_assert(kSmem <= 232448, "shared memory budget");
-  // the shared columns are among the first 64 outputs that are drained
-  static_assert(!kShared || kTileN - kAcc1 <= 64, "shared columns");
+  static_assert(256 - kAcc1 <= 64, "the shared columns are among the first 64 outputs that are drained");
 };
 
 struct FPairArgs {
@@ -71,7 +67,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
                     const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_sx,
                     const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_su,
                     const __grid_constant__ CUtensorMap tm_y, const FPairArgs p) {
-  using C = FCfg<GATED, BS>;
+  using C = FCfg<BS>;
   using B = FpBlock<BS>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -82,8 +78,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
   const uint32_t accf_bar0 = bars + 8u * (2 * S);       // x 2, one per accumulator
-  const uint32_t acce_bar0 = bars + 8u * (2 * S + 2);   // x 2: drained, as far as the next tile needs it
-  const uint32_t done_bar = bars + 8u * (2 * S + 4);
+  const uint32_t acce_bar = bars + 8u * (2 * S + 2);    // drained, as far as the next tile needs it
+  const uint32_t done_bar = bars + 8u * (2 * S + 3);
   const uint32_t tmem_slot = bars + 8u * C::kNumBars;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + C::kBars + 8 * C::kNumBars + 4);
 
@@ -98,8 +94,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     }
     mbar_init(accf_bar0, 1);
     mbar_init(accf_bar0 + 8, 1);
-    mbar_init(acce_bar0, 8);   // 4 warps x 2 CTAs
-    mbar_init(acce_bar0 + 8, 8);
+    mbar_init(acce_bar, 8);   // 4 warps x 2 CTAs
     mbar_init(done_bar, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -129,7 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           break;
         }
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kLoaded);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kStage);
           const uint32_t at = base + s * C::kStage, bar = full0 + 8u * s;
           const int sk = kb * (B::kBytes / 8);
           tma_load_2d_pair(at, &tm_x, bar, kb * 128, mt * 256 + rank * 128);
@@ -139,15 +134,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             else
               tma_load_2d_pair(at + kFOperand, &tm_u, bar, kb * 128, nt * 128);
           } else {
-            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * C::kTileN + rank * C::kRowsW);
+            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
           }
           tma_load_2d_pair(at + C::kSfx, &tm_sx, bar, sk, mt * 2 + rank);
           if (GATED) {
             tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt);
             tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_su, bar, sk, nt);
           } else {
-            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, (nt * C::kTileN) >> 7);
-            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, ((nt * C::kTileN) >> 7) + 1);
+            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt * 2);
+            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, nt * 2 + 1);
           }
         }
         __syncwarp();
@@ -174,21 +169,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
       bool go = true;
       for (int tile = cid; tile < p.tiles && go; tile += pairs, ++n) {
         const uint32_t d = tmem + ((n & 1) ? C::kAcc1 : 0);
-        // scales of weight rows that start in the middle of a tile of 128 (every other tile of 192)
-        const uint32_t sfw = tmem + C::kColW + (GATED ? 0 : ((tile / p.m_tiles) & 1) * 2);
-        // the accumulator is free: its last tile is drained; sharing columns, those of the tile before
-        // are (and, before them, everything of its own last tile)
-        const int before = C::kShared ? n - 1 : n - 2;
-        if (before >= 0 &&
-            !mbar_wait_bounded(acce_bar0 + 8u * (before & 1), (before >> 1) & 1, abort_flag, p.err, kFpWaitNs))
-          break;
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        // the tile before has given up the columns that its accumulator shares with this one's (and,
+        // earlier, everything of the tile before that)
+        if (n > 0 && !mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)) break;
+        // a stage: its scales, then `steps` MMAs
+        auto stage = [&](auto full, int steps, bool first) {
           if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) {
             go = false;
-            break;
+            return;
           }
           tc_fence_after();
-          const int steps = min(kFpSteps, p.nsteps - kb * kFpSteps);
           const uint32_t at = base + s * C::kStage;
           const uint64_t dx = smem_desc_scales(at + C::kSfx), dw = smem_desc_scales(at + C::kSfw);
 #pragma unroll
@@ -198,24 +188,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
           }
           const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
-          auto step = [&](int j) {
-            const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
-            tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, C::kTileN, id), tmem + C::kColX + 4 * a,
-                              sfw + 8 * a, (kb > 0 || j > 0) ? 1u : 0u);
-          };
-          if (steps == kFpSteps) {   // without a test per MMA, which would cost more than the MMA's issue
 #pragma unroll
-            for (int j = 0; j < kFpSteps; ++j) step(j);
-          } else {
-#pragma unroll 1
-            for (int j = 0; j < steps; ++j) step(j);
+          for (int j = 0; j < kFpSteps; ++j) {
+            if (!decltype(full)::value && j >= steps) break;
+            const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
+            tc_mma_fp4<2, BS>(d, ad + 2 * j, bd + 2 * j, idesc_fp4<BS>(256, 256, id), tmem + C::kColX + 4 * a,
+                              tmem + C::kColW + 8 * a, first && j == 0 ? 0u : 1u);
           }
           tc_commit_pair_mc(empty_bar(s), 0x3);
           if (++s == S) {
             s = 0;
             phase ^= 1u;
           }
-        }
+        };
+        // a test per MMA would cost more than its issue: only the last stage, when it is not full, has them
+        const int full_stages = p.nsteps / kFpSteps;
+        for (int kb = 0; kb < full_stages && go; ++kb) stage(std::true_type{}, kFpSteps, kb == 0);
+        if (full_stages < p.nkb && go) stage(std::false_type{}, p.nsteps - full_stages * kFpSteps, full_stages == 0);
         if (go) tc_commit_pair_mc(accf_bar0 + 8u * (n & 1), 0x3);
       }
       tc_commit_pair_mc(done_bar, 0x3);
@@ -225,9 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, row = q * 32 + lane, e = threadIdx.x - 64;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t acce0 = mapa_shared(acce_bar0, 0);
+    const uint32_t acce0 = mapa_shared(acce_bar, 0);
     float* scale = reinterpret_cast<float*>(gbase + C::kRowScale);
-    constexpr int kCols = C::kOutN, kTurns = kCols / 64;
+    constexpr int kCols = GATED ? 128 : 256, kTurns = kCols / 64;   // outputs of a token in a tile
     int n = 0;
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
@@ -247,11 +236,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
         break;
       tc_fence_after();
       const uint32_t d = tmem + lane_base + ((n & 1) ? C::kAcc1 : 0);
-      // 64 outputs a turn; where accumulators share columns, those first: the last ones of the first
-      // accumulator, the first ones of the second
+      // 64 outputs a turn, first those whose columns the next tile's accumulator shares: the last ones
+      // of the first accumulator, the first ones of the second
 #pragma unroll 1
       for (int i = 0; i < kTurns; ++i) {
-        const int c = 64 * (!C::kShared || (n & 1) ? i : kTurns - 1 - i);
+        const int c = 64 * ((n & 1) ? i : kTurns - 1 - i);
         uint32_t v[64], u[GATED ? 64 : 1];
         tmem_ld32(d + c, *reinterpret_cast<uint32_t(*)[32]>(v));
         tmem_ld32(d + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
@@ -260,10 +249,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           tmem_ld32(d + 160 + c, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
         }
         tmem_wait_ld();
-        if (i == (C::kShared ? 0 : kTurns - 1)) {
+        if (i == 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(acce0 + 8u * (n & 1));
+          if (lane == 0) mbar_arrive_remote(acce0);
         }
         uint32_t h[32];
 #pragma unroll
@@ -316,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
 
 template <bool GATED, int BS>
 cudaError_t launch(const FpProduct& p) {
-  using C = FCfg<GATED, BS>;
+  using C = FCfg<BS>;
   using B = FpBlock<BS>;
   auto kern = fp4_pair_kernel<GATED, BS>;
   static std::atomic<uint64_t> done{0};
@@ -326,7 +315,7 @@ cudaError_t launch(const FpProduct& p) {
   a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
   a.m_tiles = static_cast<int>((p.M + 255) / 256);
-  const int64_t tiles = a.m_tiles * ((p.N + C::kOutN - 1) / C::kOutN);
+  const int64_t tiles = a.m_tiles * (GATED ? (p.N + 127) / 128 : (p.N + 255) / 256);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
   a.tiles = static_cast<int>(tiles);
   a.nkb = static_cast<int>((p.K + kFpStageK - 1) / kFpStageK);
@@ -339,8 +328,8 @@ cudaError_t launch(const FpProduct& p) {
   e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
   CUtensorMap mx, mw, mu, msx, msw, msu, my;
-  auto codes = [&](CUtensorMap* m, const FpMat& q, int rows) {
-    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, rows,
+  auto codes = [&](CUtensorMap* m, const FpMat& q) {
+    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, 128,
                               CU_TENSOR_MAP_SWIZZLE_128B);
   };
   auto scales = [&](CUtensorMap* m, const FpMat& q) {
@@ -349,7 +338,7 @@ cudaError_t launch(const FpProduct& p) {
                               B::kBytes / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   };
   const FpMat& up = GATED ? p.up : p.w;
-  if (!codes(&mx, p.x, 128) || !codes(&mw, p.w, C::kRowsW) || !codes(&mu, up, C::kRowsW) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
+  if (!codes(&mx, p.x) || !codes(&mw, p.w) || !codes(&mu, up) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
       !scales(&msu, up) ||
       !make_tensor_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.y, p.N, p.M, p.N * 2, 64, 32,
                           CU_TENSOR_MAP_SWIZZLE_128B))

@@ -15,6 +15,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "fp4_common.cuh"
 
@@ -135,10 +136,14 @@ __global__ void __launch_bounds__(kRThreads, 1)
     if (elect_one()) {   // one lane runs the whole loop
       int s = 0;
       uint32_t phase = 0;
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) break;
+      bool go = true;
+      // a stage: its scales, then `steps` MMAs (a weight tile's each)
+      auto stage = [&](auto full, int steps, bool first) {
+        if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) {
+          go = false;
+          return;
+        }
         tc_fence_after();
-        const int steps = min(kFpSteps, p.nsteps - (kb0 + i) * kFpSteps);
         const uint32_t at = base + s * p.stage_bytes;
         const uint64_t dw = smem_desc_scales(at + p.sfw_offset), du = smem_desc_scales(at + p.sfu_offset),
                        dt = smem_desc_scales(at + p.sft_offset);
@@ -154,26 +159,24 @@ __global__ void __launch_bounds__(kRThreads, 1)
             tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         const uint64_t wd = smem_desc_k_sw128(at), ud = smem_desc_k_sw128(at + kROperand),
                        td = smem_desc_k_sw128(at + p.tok_offset);
-        auto step = [&](int j) {
+#pragma unroll
+        for (int j = 0; j < kFpSteps; ++j) {
+          if (!decltype(full)::value && j >= steps) break;
           const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
-          const uint32_t idesc = idesc_fp4<BS>(128, p.tn, id);
-          const uint32_t acc = (i > 0 || j > 0) ? 1u : 0u;
+          const uint32_t idesc = idesc_fp4<BS>(128, p.tn, id), acc = first && j == 0 ? 0u : 1u;
           tc_mma_fp4<1, BS>(tmem, wd + 2 * j, td + 2 * j, idesc, sfw + 4 * a, sft + tcols * a, acc);
           if (GATED) tc_mma_fp4<1, BS>(tmem + p.tn, ud + 2 * j, td + 2 * j, idesc, sfu + 4 * a, sft + tcols * a, acc);
-        };
-        if (steps == kFpSteps) {   // without a test per MMA, which would cost more than the MMA's issue
-#pragma unroll
-          for (int j = 0; j < kFpSteps; ++j) step(j);
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < steps; ++j) step(j);
         }
         tc_commit(empty_bar(s));
         if (++s == p.stages) {
           s = 0;
           phase ^= 1u;
         }
-      }
+      };
+      // a test per MMA would cost more than its issue: only the last stage, when it is not full, has them
+      const int full_end = min(kb1, p.nsteps / kFpSteps);
+      for (int kb = kb0; kb < full_end && go; ++kb) stage(std::true_type{}, kFpSteps, kb == kb0);
+      if (full_end < kb1 && go) stage(std::false_type{}, p.nsteps - full_end * kFpSteps, full_end == kb0);
       tc_commit(acc_bar);
     }
     __syncwarp();
