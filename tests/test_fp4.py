@@ -428,3 +428,23 @@ def test_binding_refusals():
     with pytest.raises(cider.CiderError):   # rows that start 8 bytes behind a 16-byte boundary
         cider.cider_quantize_fp4(torch.ones(4, 72, dtype=torch.float16, device="cuda")[:, 4:68])
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=str)
+@pytest.mark.parametrize("m,n,k", [(1, 128, 4096), (2, 264, 10240), (5, 2560, 10240), (13, 520, 1056), (16, 256, 4096), (16, 136, 4128),
+                                   (16, 2560, 10240), (3, 72, 36896), (1, 40, 131072)])
+def test_few_tokens_have_the_bits_of_quantized_ones(m, n, k, dtype, block):
+    """One launch that quantizes the rows itself, and two that do not: the same codes and sums."""
+    gen = generator(m, n, k, str(dtype), block)
+    x = activations(gen, m, k, dtype)
+    x[m // 2, : min(k, 96)] = 0
+    w, u = (cider.cider_quantize_fp4(0.05 * normal(gen, n, k), block) for _ in range(2))
+    qx = cider.cider_quantize_fp4(x, block)
+    assert torch.equal(cider.cider_w4a4_linear(x, w, block), cider.cider_w4a4_linear_prequant(qx, w, block, dtype))
+    assert torch.equal(cider.cider_w4a4_gated_linear(x, w, u, block), cider.cider_w4a4_gated_linear_prequant(qx, w, u, block, "silu", dtype))
+    a, b = ref.values(ref.matrix(x, block), block), ref.values(w, block)
+    y = cider.cider_w4a4_linear(x, w, block)
+    close(y, a @ b.T, ref.sum_bound(a, b) + ref.half_step(dtype, a @ b.T) * (1 + 2.0 ** -10))
+    clean()

@@ -13,7 +13,6 @@
 // one E8M0 scale.  Memory bounds it: 2 or 4 bytes read and 1/2 + 1/16 written a
 // value; each row is read once, the row's maximum is exchanged through shared
 // memory while the values stay in registers.
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include "fp4_common.cuh"
@@ -33,108 +32,6 @@ struct QuantArgs {
   uint8_t* scales;
   float* row;
 };
-
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-  return r;
-}
-
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 u = ld_stream_v4(p + 4 * i);
-    v[4 * i] = __uint_as_float(u.x);
-    v[4 * i + 1] = __uint_as_float(u.y);
-    v[4 * i + 2] = __uint_as_float(u.z);
-    v[4 * i + 3] = __uint_as_float(u.w);
-  }
-}
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = ld_stream_v4(p + 8 * i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
-        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[8 * i + 2 * j] = f.x;
-        v[8 * i + 2 * j + 1] = f.y;
-      }
-    }
-  }
-}
-
-// Eight values -> their E2M1 codes (nearest, ties to even, at most 6), the first in the low nibble.
-__device__ __forceinline__ uint32_t e2m1x8(const float* q) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  return r;
-}
-
-// A finite maximum a > 0 as mantissa and exponent: the smallest k with a <= m * 2^k, for m = f 2^w
-// given as the bits of f behind the leading one.  Subnormal a gives the exponent field's 0.
-__device__ __forceinline__ int power_for(float a, uint32_t f_bits, int w) {
-  const uint32_t u = __float_as_uint(a);
-  return static_cast<int>(u >> 23) - 127 - w + ((u & 0x7FFFFFu) > f_bits ? 1 : 0);
-}
-
-__device__ __forceinline__ bool not_finite(float a) { return __float_as_uint(a) >= 0x7F800000u; }
-
-// 2^k, k of -127 .. 127.
-__device__ __forceinline__ float pow2(int k) {
-  return k == -127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-}
-
-// The row's scale from its maximum: at least 2^-126, 1 for zeros, NaN where a value is not finite.
-__device__ __forceinline__ int row_power(float a) {
-  if (!(a > 0.0f)) return 0;
-  return max(power_for(a, 0x280000u, 11), -126);   // 2688 = 1.3125 * 2^11
-}
-
-// 16 values with their block's maximum (block 32: of both halves) -> two words of codes, the scale byte.
-template <int BS>
-__device__ __forceinline__ uint32_t encode16(const float (&v)[16], float top, float inv_row, uint32_t (&c)[2]) {
-  float q[16];
-  uint32_t byte;
-  if constexpr (BS == 32) {
-    if (not_finite(top)) {
-      c[0] = c[1] = 0u;
-      return 0xFFu;
-    }
-    const int e = top > 0.0f ? max(power_for(top, 0x400000u, 2), -127) : 0;   // 6 = 1.5 * 2^2
-    const float inv = pow2(-e);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = v[i] * inv;
-    byte = static_cast<uint32_t>(e + 127);
-  } else {
-    const float t = __fdiv_rn(top * inv_row, 6.0f);
-    byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-    if (byte == 0) {
-      c[0] = c[1] = 0u;
-      return 0u;
-    }
-    const float b = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
-    const float r = __frcp_rn(b);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = div_rn_by(v[i] * inv_row, b, r);
-  }
-  c[0] = e2m1x8(q);
-  c[1] = e2m1x8(q + 8);
-  return byte;
-}
 
 // Where the scale of block j of row r lies.
 __device__ __forceinline__ int64_t scale_at(int64_t r, int j, int tiles) {

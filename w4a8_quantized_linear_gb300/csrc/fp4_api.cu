@@ -62,16 +62,27 @@ struct Held {
   }
 };
 
-cudaError_t quantize(const void* x, int dtype, int64_t stride, int64_t K, int block, const cider::FpMat& q,
-                     cudaStream_t st) {
-  return cider::launch_quantize_fp4(x, dtype, stride, q.rows, K, block, const_cast<uint8_t*>(q.codes),
-                                    const_cast<uint8_t*>(q.scales), const_cast<float*>(q.row), false, st, true);
-}
-
 // Few tokens: all SMs read weights, 128 rows each.
 bool few_rows(const cider::FpProduct& p) { return p.M <= 128; }
 
-cudaError_t product(const cider::FpProduct& p) {
+// Few enough that the product's kernel quantizes the rows itself, each CTA its part of K: one launch
+// instead of two.  Block size 16 needs the rows' maxima, for which every CTA reads all of x.
+bool quantizes_itself(const cider::FpProduct& p) {
+  return few_rows(p) && p.M <= 16 && (p.block == 32 || p.M * p.K <= 65536) && cider::fp4_rows_quantizes_itself(p);
+}
+
+// A product of x in 16 bits: quantized into `held` (scratch) first, or by the product's kernel.
+cudaError_t product(cider::FpProduct& p, const cider::FpMat& held) {
+  if (p.wide_x) {
+    if (quantizes_itself(p)) return cider::launch_fp4_rows(p);
+    const cudaError_t e = cider::launch_quantize_fp4(
+        p.wide_x, p.x_bf16 ? CIDER_BF16 : CIDER_F16, p.x_stride, p.M, p.K, p.block, const_cast<uint8_t*>(held.codes),
+        const_cast<uint8_t*>(held.scales), const_cast<float*>(held.row), false, p.st, true);
+    if (e != cudaSuccess) return e;
+    p.x = held;
+    p.wide_x = nullptr;
+    p.after_launch = true;
+  }
   return few_rows(p) ? cider::launch_fp4_rows(p) : cider::launch_fp4_pair(p);
 }
 
@@ -128,26 +139,7 @@ cider_status_t run(const Call& c) {
     const cudaStream_t st = static_cast<cudaStream_t>(c.stream);
     const int64_t K = c.w->cols, F = c.w->rows;
     const int block = c.w->block_size;
-    // scratch: x's codes and scales; for a whole block the hidden values, then their codes and scales
-    const Held hx(c.qx ? 0 : M, K, block), hh(c.down ? M : 0, c.down ? F : 32, block);
-    const size_t wide = c.down ? round256(static_cast<size_t>(M) * F * 2) : 0;
-    cider::ScratchSource scratch = cider::ScratchSource::pooled(st);
-    uint8_t* base = nullptr;
-    if (hx.bytes() + wide + hh.bytes() > 0) {
-      void* p = nullptr;
-      s = scratch.get(hx.bytes() + wide + hh.bytes(), &p);
-      if (s != CIDER_OK) return s;
-      base = static_cast<uint8_t*>(p);
-    }
     cider::FpProduct p;
-    if (c.qx) {
-      p.x = mat(c.qx);
-    } else {
-      p.x = hx.at(base, M);
-      const cudaError_t e = quantize(c.x, c.x_dtype, c.x_stride, K, block, p.x, st);
-      if (e != cudaSuccess) return cuda_status(e);
-      p.after_launch = true;
-    }
     p.w = mat(c.w);
     if (c.gated) p.up = mat(c.up);
     p.is_gated = c.gated;
@@ -158,25 +150,45 @@ cider_status_t run(const Call& c) {
     p.block = block;
     p.num_sms = sms;
     p.st = st;
-    p.y = c.down ? base + hx.bytes() : c.y;
+    if (c.qx) p.x = mat(c.qx);
+    p.wide_x = c.qx ? nullptr : c.x;
+    p.x_stride = c.x_stride;
+    p.x_bf16 = c.x_dtype == CIDER_BF16;
     p.y_bf16 = (c.down ? c.x_dtype : c.y_dtype) == CIDER_BF16;
-    cudaError_t e = F == 0 ? cudaSuccess : product(p);
-    if (e != cudaSuccess || !c.down) return cuda_status(e);
     cider::FpProduct d;
-    d.x = hh.at(base + hx.bytes() + wide, M);
-    e = quantize(p.y, c.x_dtype, F, F, block, d.x, st);
-    if (e != cudaSuccess) return cuda_status(e);
-    d.after_launch = true;
-    d.w = mat(c.down);
-    d.M = M;
-    d.N = N;
-    d.K = F;
-    d.block = block;
-    d.num_sms = sms;
-    d.st = st;
-    d.y = c.y;
-    d.y_bf16 = c.y_dtype == CIDER_BF16;
-    return cuda_status(product(d));
+    if (c.down) {
+      d.w = mat(c.down);
+      d.M = M;
+      d.N = N;
+      d.K = F;
+      d.block = block;
+      d.num_sms = sms;
+      d.st = st;
+      d.x_stride = F;
+      d.x_bf16 = p.x_bf16;
+      d.y = c.y;
+      d.y_bf16 = c.y_dtype == CIDER_BF16;
+    }
+    // scratch: x's codes and scales; for a whole block the hidden values, then their codes and scales
+    const Held hx(p.wide_x && !quantizes_itself(p) ? M : 0, K, block),
+        hh(c.down && !quantizes_itself(d) ? M : 0, c.down ? F : 32, block);
+    const size_t wide = c.down ? round256(static_cast<size_t>(M) * F * 2) : 0;
+    cider::ScratchSource scratch = cider::ScratchSource::pooled(st);
+    uint8_t* base = nullptr;
+    if (hx.bytes() + wide + hh.bytes() > 0) {
+      void* ptr = nullptr;
+      s = scratch.get(hx.bytes() + wide + hh.bytes(), &ptr);
+      if (s != CIDER_OK) return s;
+      base = static_cast<uint8_t*>(ptr);
+    }
+    p.y = c.down ? base + hx.bytes() : c.y;
+    if (F > 0) {
+      const cudaError_t e = product(p, hx.at(base, M));
+      if (e != cudaSuccess || !c.down) return cuda_status(e);
+    }
+    d.wide_x = p.y;
+    d.after_launch = true;   // should its kernel quantize the hidden values itself
+    return cuda_status(product(d, hh.at(base + hx.bytes() + wide, M)));
   });
 }
 

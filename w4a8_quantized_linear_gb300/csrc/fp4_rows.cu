@@ -9,9 +9,14 @@
 // through distributed shared memory in the order of their ranks: no scratch in
 // global memory, no second launch, the same bits each time.
 //
-// Warp 0 copies (weights' stages before the quantization of x has ended: they
-// do not depend on it), warp 1 issues scale copies and MMAs, warps 2..5 drain
-// the accumulators; all warps add up and store.
+// FUSE: up to 16 tokens whose rows this kernel quantizes itself, each CTA the
+// part of K that it multiplies (block size 16 takes the row's maximum from the
+// whole row, which every CTA reads), into the operand's place in shared memory:
+// a decoding step's linear is one launch and needs no scratch.
+//
+// Warp 0 copies (weights' stages before x is there: they do not depend on it),
+// warp 1 issues scale copies and MMAs, the others quantize; warps 2..5 drain the
+// accumulators, all warps add up and store.
 #include <cuda.h>
 
 #include <atomic>
@@ -22,14 +27,16 @@
 namespace cider {
 namespace {
 
-constexpr int kRThreads = 192;
 constexpr int kRMaxStages = 12;
 constexpr int kROperand = 128 * 128;   // bytes of 128 rows of a stage's codes
-constexpr int kRBars = 2 * kRMaxStages + 1;
-constexpr int kRTail = kRBars * 8 + 16;
+constexpr int kRBars = 2 * kRMaxStages + 2;
+constexpr int kRTail = kRBars * 8 + 16 + 2 * 16 * 4;   // barriers, flags, the fused rows' maxima and scales
+constexpr int kRTokens = 16;                           // of the fused form
+constexpr int kRQuantWarps = 8;
+constexpr int kRMaxFusedStages = 16;                   // of a CTA's part of K, held whole
 
 struct RowsArgs {
-  int M, N;
+  int M, N, K;
   int tn;            // tokens of a tile: 16, 32, 64, 128 or 256
   int m_tiles;       // token tiles (one, unless tn is 128 or 256)
   int splits;        // CTAs of a cluster
@@ -38,31 +45,109 @@ struct RowsArgs {
   int stages;        // ring slots
   int stage_bytes, tok_offset, sfw_offset, sfu_offset, sft_offset;   // within a stage
   int tok_tiles;     // 128-row tiles of the tokens' scales in a stage: 1 or 2
+  int x_offset, xs_offset;   // FUSE: all of the part's codes, and scales, of x
+  int tail;          // barriers and what follows
+  int sc_tiles;      // tiles of scales along K
   uint32_t tmem_cols;
+  const uint8_t *scw, *scu, *scx;   // block scales
   const float *sx, *sw, *su;
+  const void* x;     // FUSE
+  int64_t x_stride;
+  int x_bf16;
   void* y;
   int y_bf16, act;
   int* err;
 };
 
-template <bool GATED, int BS>
-__global__ void __launch_bounds__(kRThreads, 1)
+// The part of the rows of x that this CTA multiplies, quantized into shared memory.
+template <int BS>
+__device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes, uint8_t* scales, uint32_t* most,
+                                              float* row, int kb0, int kb1, int thread) {
+  constexpr int kThreads = 32 * kRQuantWarps;
+  auto load = [&](int r, int k, float (&v)[16]) {
+    if (p.x_bf16)
+      load16(static_cast<const __nv_bfloat16*>(p.x) + r * p.x_stride + k, v);
+    else
+      load16(static_cast<const __half*>(p.x) + r * p.x_stride + k, v);
+  };
+  if constexpr (BS == 16) {
+    // the rows' maxima; |x| is ordered like its bits, and a NaN comes out on top
+    const int per = p.K >> 4, units = p.M * per;
+    for (int u0 = 0; u0 < units; u0 += kThreads) {
+      const int u = u0 + thread, r = min(u, units - 1) / per;
+      uint32_t top = 0;
+      if (u < units) {
+        float v[16];
+        load(r, (u - r * per) * 16, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      }
+      if (__match_any_sync(0xffffffffu, r) == 0xffffffffu) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((thread & 31) == 0) atomicMax(most + r, top);
+      } else {
+        atomicMax(most + r, top);
+      }
+    }
+    named_barrier_sync(1, kThreads);
+    if (thread < p.M) {
+      const float a = __uint_as_float(most[thread]);
+      row[thread] = not_finite(a) ? __uint_as_float(0x7FC00000u) : pow2(row_power(a));
+    }
+  }
+  // whole steps of 64: zeros behind the end of the row
+  const int k0 = kb0 * kFpStageK, k1 = min(kb1 * kFpStageK, p.nsteps * kFpStepK);
+  const int per = (k1 - k0) >> 4, units = p.M * per;   // a multiple of 4: a block's two threads stay together
+  for (int u0 = 0; u0 < units; u0 += kThreads) {
+    const int u = u0 + thread, r = min(u, units - 1) / per, i = u - r * per, k = k0 + 16 * i;
+    const bool have = u < units && k < p.K;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+    if (have) load(r, k, v);
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max_abs_nan(top, v[j]);
+    uint32_t c[2] = {0u, 0u}, byte = 0u;
+    if constexpr (BS == 32) {
+      top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      byte = encode16<BS>(v, top, 1.0f, c);
+    } else {
+      const float a = __uint_as_float(most[r]);
+      if (!not_finite(a)) byte = encode16<BS>(v, top, pow2(-row_power(a)), c);
+    }
+    if (u >= units) continue;
+    const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
+    // 128-byte rows, their 16-byte pieces swizzled within groups of 8 rows
+    uint8_t* at = codes + kb * (kRTokens * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
+                  (((kk >> 5) ^ (r & 7)) << 4) + ((kk >> 1) & 8);
+    *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
+    // tiles half as far apart as they are long: rows 16 .. 31 are not there
+    if (BS == 16 || (i & 1) == 0)
+      scales[(kb * FpBlock<BS>::kTiles + kk / (4 * BS)) * (kFpTileBytes / 2) + 16 * r + (kk / BS & 3)] =
+          static_cast<uint8_t>(byte);
+  }
+}
+
+template <bool GATED, int BS, bool FUSE>
+__global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
     fp4_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_u,
-                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_sw,
-                    const __grid_constant__ CUtensorMap tm_su, const __grid_constant__ CUtensorMap tm_sx,
-                    const RowsArgs p) {
+                    const __grid_constant__ CUtensorMap tm_x, const RowsArgs p) {
   using B = FpBlock<BS>;
+  constexpr int kThreads = FUSE ? 64 + 32 * kRQuantWarps : 192;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const int ring = p.stages * p.stage_bytes;
-  const uint32_t bars = base + ring;
+  const uint32_t bars = base + p.tail;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kRMaxStages + s); };
   const uint32_t acc_bar = bars + 8u * (2 * kRMaxStages);
+  const uint32_t x_bar = bars + 8u * (2 * kRMaxStages + 1);
   const uint32_t tmem_slot = bars + 8u * kRBars;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + ring + 8 * kRBars + 4);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + p.tail + 8 * kRBars + 4);
+  uint32_t* most = reinterpret_cast<uint32_t*>(gbase + p.tail + 8 * kRBars + 16);
+  float* row = reinterpret_cast<float*>(most + kRTokens);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the rank in the cluster; of blockIdx, so that the compiler knows it to be the same for all threads
@@ -79,9 +164,11 @@ __global__ void __launch_bounds__(kRThreads, 1)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(acc_bar, 1);
+    mbar_init(x_bar, kRQuantWarps);
     *abort_flag = 0u;
     fence_mbar_init();
   }
+  if (FUSE && threadIdx.x >= 32 && threadIdx.x < 32 + kRTokens) most[threadIdx.x - 32] = 0u;
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
@@ -89,39 +176,44 @@ __global__ void __launch_bounds__(kRThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + ring + 8 * kRBars);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + p.tail + 8 * kRBars);
   const int acc_cols = GATED ? 2 * p.tn : p.tn;
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint32_t bytes = (GATED ? 2u : 1u) * (kROperand + B::kBytes) + p.tn * 128 + p.tok_tiles * B::kBytes;
+    if (elect_one()) {
+      const int tok_tiles = FUSE ? 0 : min(p.tok_tiles, (p.M + 127) / 128 - (m0 >> 7));
+      // bytes of scales that a stage has (the last one may have fewer tiles)
+      auto scale_bytes = [&](int kb) { return min(B::kTiles, p.sc_tiles - kb * B::kTiles) * kFpTileBytes; };
       auto weights = [&](int kb, int s) {
-        const uint32_t at = base + s * p.stage_bytes;
-        mbar_arrive_expect_tx(full_bar(s), bytes);
+        const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
+        const int64_t from = (static_cast<int64_t>(nt) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes;
+        mbar_arrive_expect_tx(full_bar(s), (GATED ? 2u : 1u) * (kROperand + sb) + (FUSE ? 0u : p.tn * 128u) + tok_tiles * sb);
         tma_load_2d(at, &tm_w, full_bar(s), kb * 128, nt * 128);
-        tma_load_2d(at + p.sfw_offset, &tm_sw, full_bar(s), kb * (B::kBytes / 8), nt);
-        if (GATED) {
-          tma_load_2d(at + kROperand, &tm_u, full_bar(s), kb * 128, nt * 128);
-          tma_load_2d(at + p.sfu_offset, &tm_su, full_bar(s), kb * (B::kBytes / 8), nt);
-        }
+        if (GATED) tma_load_2d(at + kROperand, &tm_u, full_bar(s), kb * 128, nt * 128);
+        bulk_load(at + p.sfw_offset, p.scw + from, sb, full_bar(s));
+        if (GATED) bulk_load(at + p.sfu_offset, p.scu + from, sb, full_bar(s));
       };
       auto tokens = [&](int kb, int s) {
-        const uint32_t at = base + s * p.stage_bytes;
+        const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
         tma_load_2d(at + p.tok_offset, &tm_x, full_bar(s), kb * 128, m0);
-        for (int t = 0; t < p.tok_tiles; ++t)
-          tma_load_2d(at + p.sft_offset + t * B::kBytes, &tm_sx, full_bar(s), kb * (B::kBytes / 8), (m0 >> 7) + t);
+        for (int t = 0; t < tok_tiles; ++t)
+          bulk_load(at + p.sft_offset + t * B::kBytes,
+                    p.scx + (static_cast<int64_t>((m0 >> 7) + t) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes, sb,
+                    full_bar(s));
       };
       const int ahead = min(kb1 - kb0, p.stages);
       for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
-      pdl_wait();
-      for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
+      if (!FUSE) {
+        pdl_wait();
+        for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
+      }
       int i = ahead;
       for (; kb0 + i < kb1; ++i) {
         const int s = i % p.stages;
         if (!mbar_wait_bounded(empty_bar(s), ((i / p.stages) & 1) ^ 1u, abort_flag, p.err, kFpWaitNs)) break;
         weights(kb0 + i, s);
-        tokens(kb0 + i, s);
+        if (!FUSE) tokens(kb0 + i, s);
       }
       // what was issued has landed before the CTA leaves, also after a wait that gave up
       volatile uint32_t keep_waiting = 0u;
@@ -134,9 +226,9 @@ __global__ void __launch_bounds__(kRThreads, 1)
     const uint32_t sfw = tmem + acc_cols, sfu = sfw + B::kCols, sft = sfw + (GATED ? 2 : 1) * B::kCols;
     const uint32_t tcols = 4 * p.tok_tiles;   // columns of the tokens' scales of one tile of K
     if (elect_one()) {   // one lane runs the whole loop
-      int s = 0;
+      int s = 0, i = 0;
       uint32_t phase = 0;
-      bool go = true;
+      bool go = !FUSE || mbar_wait_bounded(x_bar, 0, abort_flag, p.err, kFpWaitNs);
       // a stage: its scales, then `steps` MMAs (a weight tile's each)
       auto stage = [&](auto full, int steps, bool first) {
         if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) {
@@ -145,29 +237,32 @@ __global__ void __launch_bounds__(kRThreads, 1)
         }
         tc_fence_after();
         const uint32_t at = base + s * p.stage_bytes;
-        const uint64_t dw = smem_desc_scales(at + p.sfw_offset), du = smem_desc_scales(at + p.sfu_offset),
-                       dt = smem_desc_scales(at + p.sft_offset);
+        const uint64_t dw = smem_desc_scales(at + p.sfw_offset), du = smem_desc_scales(at + p.sfu_offset);
+        // FUSE: tiles of scales half as far apart as they are long
+        constexpr int kPitch = FUSE ? kFpTileBytes / 2 : kFpTileBytes;
+        const uint64_t dt = smem_desc_scales(FUSE ? base + p.xs_offset + i * B::kTiles * kPitch : at + p.sft_offset);
 #pragma unroll
         for (int a = 0; a < B::kTiles; ++a) {
           tc_cp_scales<1>(sfw + 4 * a, dw + a * (kFpTileBytes >> 4));
           if (GATED) tc_cp_scales<1>(sfu + 4 * a, du + a * (kFpTileBytes >> 4));
-          tc_cp_scales<1>(sft + tcols * a, dt + a * (kFpTileBytes >> 4));
+          tc_cp_scales<1>(sft + tcols * a, dt + a * (kPitch >> 4));
         }
-        if (p.tok_tiles == 2)
+        if (!FUSE && p.tok_tiles == 2)
 #pragma unroll
           for (int a = 0; a < B::kTiles; ++a)
             tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         const uint64_t wd = smem_desc_k_sw128(at), ud = smem_desc_k_sw128(at + kROperand),
-                       td = smem_desc_k_sw128(at + p.tok_offset);
+                       td = smem_desc_k_sw128(FUSE ? base + p.x_offset + i * (kRTokens * 128) : at + p.tok_offset);
 #pragma unroll
         for (int j = 0; j < kFpSteps; ++j) {
           if (!decltype(full)::value && j >= steps) break;
           const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
-          const uint32_t idesc = idesc_fp4<BS>(128, p.tn, id), acc = first && j == 0 ? 0u : 1u;
+          const uint32_t idesc = idesc_fp4<BS>(128, FUSE ? kRTokens : p.tn, id), acc = first && j == 0 ? 0u : 1u;
           tc_mma_fp4<1, BS>(tmem, wd + 2 * j, td + 2 * j, idesc, sfw + 4 * a, sft + tcols * a, acc);
           if (GATED) tc_mma_fp4<1, BS>(tmem + p.tn, ud + 2 * j, td + 2 * j, idesc, sfu + 4 * a, sft + tcols * a, acc);
         }
         tc_commit(empty_bar(s));
+        ++i;
         if (++s == p.stages) {
           s = 0;
           phase ^= 1u;
@@ -180,6 +275,13 @@ __global__ void __launch_bounds__(kRThreads, 1)
       tc_commit(acc_bar);
     }
     __syncwarp();
+  } else if (FUSE) {
+    // ------------------------------------------------------------ quantization of x
+    pdl_wait();   // x may be what the launch just before wrote
+    quantize_part<BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x_bar);
   }
   // ---------------------------------------------------------------- sums
   // Every MMA that was issued has run (also after a wait that gave up); then the ring is free and
@@ -194,9 +296,9 @@ __global__ void __launch_bounds__(kRThreads, 1)
     ok = mbar_wait_bounded(acc_bar, 0, &keep_waiting, p.err, kFpWaitNs);
   }
   ok = __syncthreads_and(ok && *abort_flag == 0u);
-  if (ok && warp >= 2) {
+  if (ok && warp >= 2 && warp < 6) {
     tc_fence_after();
-    const int q = warp & 3, row = q * 32 + lane;
+    const int q = warp & 3, n = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     for (int c = 0; c < acc_cols; c += 32) {
       // columns of tokens behind the last one are not needed
@@ -206,7 +308,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
       tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (c + i < acc_cols) part[(c + i) * 128 + row] = __uint_as_float(v[i]);
+        if (c + i < acc_cols) part[(c + i) * 128 + n] = __uint_as_float(v[i]);
     }
     tc_fence_before();
   }
@@ -223,7 +325,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
     const int units = mv * 32;
     const int u0 = static_cast<int>(static_cast<int64_t>(rank) * units / p.splits);
     const int u1 = static_cast<int>(static_cast<int64_t>(rank + 1) * units / p.splits);
-    for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += kRThreads) {
+    for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += kThreads) {
       const int t = u >> 5, n = nt * 128 + 4 * (u & 31);
       if (n >= p.N) continue;   // N % 8 == 0: four rows are all in or all out
       float a[GATED ? 8 : 4];
@@ -244,7 +346,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
           a[4 * h + 3] += f.w;
         }
       }
-      const float sx = p.sx ? __ldg(p.sx + m0 + t) : 1.0f;
+      const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? __ldg(p.sx + m0 + t) : 1.0f;
       float out[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -261,74 +363,27 @@ __global__ void __launch_bounds__(kRThreads, 1)
     }
   }
   __syncwarp();
-  if (p.splits > 1) cluster_sync_all();   // the partial sums stay until every CTA has read them
+  // the partial sums stay until every CTA has read them (what was stored need not be seen by then)
+  if (p.splits > 1) cluster_sync_relaxed();
 }
 
-template <bool GATED, int BS>
-cudaError_t launch(const FpProduct& p) {
-  using B = FpBlock<BS>;
-  RowsArgs a{};
-  a.M = static_cast<int>(p.M);
-  a.N = static_cast<int>(p.N);
-  const int most = GATED ? 128 : 256;
-  a.tn = 16;
-  while (a.tn < most && a.tn < p.M) a.tn *= 2;
-  a.m_tiles = static_cast<int>((p.M + a.tn - 1) / a.tn);
-  a.nkb = static_cast<int>((p.K + kFpStageK - 1) / kFpStageK);
-  a.nsteps = static_cast<int>((p.K + kFpStepK - 1) / kFpStepK);
-  a.tok_tiles = a.tn > 128 ? 2 : 1;
-  a.tok_offset = (GATED ? 2 : 1) * kROperand;
-  a.sfw_offset = a.tok_offset + a.tn * 128;
-  a.sfu_offset = a.sfw_offset + B::kBytes;
-  a.sft_offset = a.sfw_offset + (GATED ? 2 : 1) * B::kBytes;
-  a.stage_bytes = (a.sft_offset + a.tok_tiles * B::kBytes + 1023) / 1024 * 1024;
-  const int acc = (GATED ? 2 : 1) * a.tn;
-  const int cols = acc + ((GATED ? 2 : 1) + a.tok_tiles) * B::kCols;
-  a.tmem_cols = 64;
-  while (static_cast<int>(a.tmem_cols) < cols) a.tmem_cols *= 2;
-  // CTAs that hold at most half of the tensor memory share an SM in pairs (their shared memory
-  // allows two and no third), the others have one to themselves: no CTA of a cluster waits for
-  // tensor memory that another cluster's holds.
-  const bool two = a.tmem_cols <= 256;
-  const int budget = two ? 110 * 1024 : 224 * 1024;
-  const int tiles = a.m_tiles * static_cast<int>((p.N + 127) / 128);
-  a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= p.num_sms * (two ? 2 : 1) && a.nkb >= a.splits * 2) a.splits *= 2;
-  a.stages = budget / a.stage_bytes;
-  if (a.stages > kRMaxStages) a.stages = kRMaxStages;
-  int smem = a.stages * a.stage_bytes + kRTail + 1024;
-  if (two && smem < 79 * 1024) smem = 79 * 1024;
-  a.sx = p.x.row;
-  a.sw = p.w.row;
-  a.su = p.up.row;
-  a.y = p.y;
-  a.y_bf16 = p.y_bf16;
-  a.act = p.act;
-  cudaError_t e = device_error_word(&a.err);
-  if (e != cudaSuccess) return e;
-
-  CUtensorMap mw, mu, mx, msw, msu, msx;
+template <bool GATED, int BS, bool FUSE>
+cudaError_t launch(const FpProduct& p, RowsArgs& a, int smem, int tiles) {
+  CUtensorMap mw, mu, mx;
   auto codes = [&](CUtensorMap* m, const FpMat& q, int rows) {
     return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, p.K / 2, q.rows, p.K / 2, 128, rows,
                               CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  auto scales = [&](CUtensorMap* m, const FpMat& q) {
-    const uint64_t words = static_cast<uint64_t>(fp4_tiles(p.K, BS)) * (kFpTileBytes / 8);
-    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_INT64, q.scales, words, (q.rows + 127) / 128, words * 8,
-                              B::kBytes / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
-  };
-  const FpMat& up = GATED ? p.up : p.w;
-  if (!codes(&mw, p.w, 128) || !codes(&mu, up, 128) || !codes(&mx, p.x, a.tn) || !scales(&msw, p.w) ||
-      !scales(&msu, up) || !scales(&msx, p.x))
-    return cudaErrorInvalidValue;
-
-  auto kern = fp4_rows_kernel<GATED, BS>;
+  if (!codes(&mw, p.w, 128)) return cudaErrorInvalidValue;
+  mu = mx = mw;
+  if ((GATED && !codes(&mu, p.up, 128)) || (!FUSE && !codes(&mx, p.x, a.tn))) return cudaErrorInvalidValue;
+  auto kern = fp4_rows_kernel<GATED, BS, FUSE>;
   static std::atomic<uint64_t> done{0};
-  e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), 232448, done);
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), 232448, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
-  cfg.blockDim = dim3(kRThreads, 1, 1);
+  cfg.blockDim = dim3(FUSE ? 64 + 32 * kRQuantWarps : 192, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = p.st;
   cudaLaunchAttribute attr[2];
@@ -345,14 +400,96 @@ cudaError_t launch(const FpProduct& p) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, mw, mu, mx, msw, msu, msx, a);
+  return cudaLaunchKernelEx(&cfg, kern, mw, mu, mx, a);
+}
+
+// The launch's sizes; false: a part of K that the fused form does not hold.
+bool plan(const FpProduct& p, bool fuse, RowsArgs& a, int* smem_out, int* tiles_out) {
+  const int sides = p.is_gated ? 2 : 1;
+  const int per_tiles = kFpStageK / (4 * p.block), bytes = per_tiles * kFpTileBytes, cols_side = per_tiles * 4;
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.K = static_cast<int>(p.K);
+  const int most = p.is_gated ? 128 : 256;
+  a.tn = 16;
+  while (a.tn < most && a.tn < p.M) a.tn *= 2;
+  a.m_tiles = static_cast<int>((p.M + a.tn - 1) / a.tn);
+  a.nkb = static_cast<int>((p.K + kFpStageK - 1) / kFpStageK);
+  a.nsteps = static_cast<int>((p.K + kFpStepK - 1) / kFpStepK);
+  a.sc_tiles = fp4_tiles(p.K, p.block);
+  a.tok_tiles = a.tn > 128 ? 2 : 1;
+  a.tok_offset = sides * kROperand;
+  a.sfw_offset = a.tok_offset + (fuse ? 0 : a.tn * 128);
+  a.sfu_offset = a.sfw_offset + bytes;
+  a.sft_offset = a.sfw_offset + sides * bytes;
+  a.stage_bytes = (a.sft_offset + (fuse ? 0 : a.tok_tiles * bytes) + 1023) / 1024 * 1024;
+  const int cols = sides * a.tn + (sides + a.tok_tiles) * cols_side;
+  a.tmem_cols = 64;
+  while (static_cast<int>(a.tmem_cols) < cols) a.tmem_cols *= 2;
+  // CTAs that hold at most half of the tensor memory share an SM in pairs (their shared memory
+  // allows two and no third), the others have one to themselves: no CTA of a cluster waits for
+  // tensor memory that another cluster's holds.
+  const bool two = a.tmem_cols <= 256;
+  int budget = two ? 110 * 1024 : 224 * 1024;
+  const int tiles = a.m_tiles * static_cast<int>((p.N + 127) / 128);
+  a.splits = 1;
+  while (a.splits < 8 && tiles * a.splits * 2 <= p.num_sms * (two ? 2 : 1) && a.nkb >= a.splits * 2) a.splits *= 2;
+  const int mine = (a.nkb + a.splits - 1) / a.splits;   // stages of a CTA, at most
+  int held = 0;
+  if (fuse) {
+    if (p.M > kRTokens || mine > kRMaxFusedStages) return false;
+    // the last tile of scales is read to its end, half a tile behind the next one's start
+    held = mine * (kRTokens * 128) + (mine * per_tiles + 1) * (kFpTileBytes / 2);
+    held = (held + 1023) / 1024 * 1024;
+  }
+  a.stages = (budget - held) / a.stage_bytes;
+  if (a.stages > kRMaxStages) a.stages = kRMaxStages;
+  a.x_offset = a.stages * a.stage_bytes;
+  a.xs_offset = a.x_offset + mine * (kRTokens * 128);
+  a.tail = a.x_offset + held;
+  int smem = a.tail + kRTail + 1024;
+  if (two && smem < 79 * 1024) smem = 79 * 1024;
+  a.scw = p.w.scales;
+  a.scu = p.up.scales;
+  a.scx = p.x.scales;
+  a.sx = p.x.row;
+  a.sw = p.w.row;
+  a.su = p.up.row;
+  a.x = p.wide_x;
+  a.x_stride = p.x_stride;
+  a.x_bf16 = p.x_bf16;
+  a.y = p.y;
+  a.y_bf16 = p.y_bf16;
+  a.act = p.act;
+  *smem_out = smem;
+  *tiles_out = tiles;
+  return true;
 }
 
 }  // namespace
 
+bool fp4_rows_quantizes_itself(const FpProduct& p) {
+  RowsArgs a{};
+  int smem, tiles;
+  return plan(p, true, a, &smem, &tiles);
+}
+
 cudaError_t launch_fp4_rows(const FpProduct& p) {
-  if (p.is_gated) return p.block == 16 ? launch<true, 16>(p) : launch<true, 32>(p);
-  return p.block == 16 ? launch<false, 16>(p) : launch<false, 32>(p);
+  RowsArgs a{};
+  int smem = 0, tiles = 0;
+  const bool fuse = p.wide_x != nullptr;
+  if (!plan(p, fuse, a, &smem, &tiles)) return cudaErrorInvalidValue;
+  const cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return e;
+  auto go = [&](auto gated_, auto block) {
+    constexpr bool G = decltype(gated_)::value;
+    constexpr int BS = decltype(block)::value;
+    return fuse ? launch<G, BS, true>(p, a, smem, tiles) : launch<G, BS, false>(p, a, smem, tiles);
+  };
+  using B16 = std::integral_constant<int, 16>;
+  using B32 = std::integral_constant<int, 32>;
+  if (p.is_gated) return p.block == 16 ? go(std::true_type{}, B16{}) : go(std::true_type{}, B32{});
+  return p.block == 16 ? go(std::false_type{}, B16{}) : go(std::false_type{}, B32{});
 }
 
 }  // namespace cider
