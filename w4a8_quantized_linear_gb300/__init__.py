@@ -658,6 +658,8 @@ _WIDE = {torch.float16: CIDER_F16, torch.bfloat16: CIDER_BF16, torch.float32: CI
 
 
 def _refuse_fp4(q, block_size, name):
+    if block_size not in (16, 32):
+        raise ValueError(f"block_size must be 16 or 32, got {block_size}")
     if not isinstance(q, (tuple, list)) or len(q) != 3:
         raise TypeError(f"{name} must be (codes, scales, row_scale)")
     codes, scales, row = q
@@ -684,55 +686,56 @@ def _scale_shape(rows, cols, block_size):
     return (rows + 127) // 128, -(-cols // (4 * block_size)), 512
 
 
-def _block(block_size):
-    if block_size not in (16, 32):
-        raise ValueError(f"block_size must be 16 or 32, got {block_size}")
-
-
 def _fp4_args(q, block_size, name, dev=None):
     """-> (cider_fp4_t as bytes, device index, rows, cols)."""
     try:
         codes, scales, row = q
-        half, place = codes.shape, codes.get_device()
-        rows, cols = half[0], 2 * half[1]
-        if not (len(half) == 2 and codes.dtype is _U8 and scales.dtype is _U8 and place >= 0
-                and scales.get_device() == place and codes.is_contiguous() and scales.is_contiguous()
-                and scales.shape == _scale_shape(rows, cols, block_size)
+        rows, half = codes.shape
+        place = codes.get_device()
+        if not (codes.dtype is _U8 and scales.dtype is _U8 and place >= 0 and scales.get_device() == place
+                and (block_size == 16 or block_size == 32)
+                and scales.shape == ((rows + 127) >> 7, -(-half // (2 * block_size)), 512)
+                and codes.is_contiguous() and scales.is_contiguous()
                 and (row is None or (row.dtype is _F32 and row.shape == (rows,) and row.get_device() == place
                                      and row.is_contiguous()))):
             _refuse_fp4(q, block_size, name)
-    except (AttributeError, TypeError, ValueError, IndexError):   # not a triple of tensors
+    except (AttributeError, TypeError, ValueError):   # not a triple of tensors
         _refuse_fp4(q, block_size, name)
     if dev is not None and place != dev:
         raise ValueError(f"{name} is on another device")
-    return (_FP4.pack(codes.data_ptr(), scales.data_ptr(), 0 if row is None else row.data_ptr(), rows, cols,
-                      block_size), place, rows, cols)
+    return (_FP4.pack(codes.data_ptr(), scales.data_ptr(), 0 if row is None else row.data_ptr(), rows, 2 * half,
+                      block_size), place, rows, 2 * half)
 
 
-def _wide_rows(x, cols, kinds, dev=None):
-    """Type, row stride and rows of a matrix [rows, cols] with dense rows."""
+def _wide_rows(x, cols, kinds, dev):
+    """Type, row stride and rows of a matrix [rows, cols] with dense rows on this device (None: any)."""
+    try:
+        kind, place = kinds[x.dtype], x.get_device()
+        n, k = x.shape
+        stride, one = x.stride()
+        if (one == 1 or k == 1) and (cols is None or k == cols) and place >= 0 and (dev is None or place == dev):
+            return kind, stride if n > 1 else k, n
+    except (AttributeError, KeyError, ValueError):
+        pass
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor")
     if x.dtype not in kinds:
-        raise TypeError(f"x must be one of {', '.join(str(k) for k in kinds)}, got {x.dtype}")
+        raise TypeError(f"x must be one of {', '.join(str(t) for t in kinds)}, got {x.dtype}")
     if x.dim() != 2 or (cols is not None and x.shape[1] != cols):
         raise ValueError(f"x must have shape [rows, {'cols' if cols is None else cols}], got {tuple(x.shape)}")
-    n, k = x.shape
-    stride, one = x.stride()
-    if one != 1 and k > 1:
+    if x.stride(1) != 1:
         raise ValueError("x must have contiguous rows")
-    if dev is not None and x.get_device() != dev:
-        raise ValueError("x is on another device")
-    return kinds[x.dtype], stride if n > 1 else k, n
+    raise ValueError("x is on another device")
 
 
-def _result(out, shape, dtype, dev, name):
+def _result(out, shape, dtype, like, name):
+    """The given output, or a new one on the device of `like`, and its pointer."""
     if dtype not in _DTYPES:
         raise TypeError(f"{name}'s type must be float16 or bfloat16")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        out = torch.empty(shape, dtype=dtype, device=like.device)
         return out, out.data_ptr()
-    return out, _flat(out, dtype, name, shape, dev)
+    return out, _flat(out, dtype, name, shape, like.get_device())
 
 
 def cider_quantize_fp4(x: torch.Tensor, block_size: int = 32):
@@ -740,8 +743,9 @@ def cider_quantize_fp4(x: torch.Tensor, block_size: int = 32):
     scales uint8 [ceil(rows / 128), ceil(cols / (4 block_size)), 512], row_scale):
     4-bit floating point (E2M1) with an E8M0 scale per 32 values (row_scale None),
     or an E4M3 scale per 16 values and row_scale fp32 [rows]."""
-    _block(block_size)
-    kind, stride, rows = _wide_rows(x, None, _WIDE)
+    if block_size not in (16, 32):
+        raise ValueError(f"block_size must be 16 or 32, got {block_size}")
+    kind, stride, rows = _wide_rows(x, None, _WIDE, None)
     cols, place = x.shape[1], x.device
     q = (torch.empty((rows, cols // 2), dtype=_U8, device=place),
          torch.empty(_scale_shape(rows, cols, block_size), dtype=_U8, device=place),
@@ -755,7 +759,6 @@ def cider_quantize_fp4(x: torch.Tensor, block_size: int = 32):
 def cider_dequantize_fp4(q, block_size: int = 32, dtype=torch.float16, out=None):
     """The values of a quantized matrix (codes, scales, row_scale) -> [rows, cols] of
     `dtype` (fp16, bf16 or fp32)."""
-    _block(block_size)
     c, dev, rows, cols = _fp4_args(q, block_size, "q")
     if dtype not in _WIDE:
         raise TypeError("dtype must be float16, bfloat16 or float32")
@@ -771,11 +774,10 @@ def cider_dequantize_fp4(q, block_size: int = 32, dtype=torch.float16, out=None)
 def cider_w4a4_linear(x, w, block_size: int = 32, y_dtype=None, out=None):
     """y [M, N] of y_dtype (None: x's) = x w^T for x fp16 or bf16 [M, K] (any row
     stride), quantized by the call, and w = cider_quantize_fp4(weights [N, K])."""
-    _block(block_size)
     c, dev, n, k = _fp4_args(w, block_size, "w")
     kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
     y_dtype = x.dtype if y_dtype is None else y_dtype
-    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    y, yp = _result(out, (m, n), y_dtype, w[0], "out")
     _launch((_lib or _load()).cider_w4a4_linear, dev, (x.data_ptr(), kind, stride, m, c, yp, _DTYPES[y_dtype],
             _raw_stream(dev)))
     return y
@@ -783,18 +785,16 @@ def cider_w4a4_linear(x, w, block_size: int = 32, y_dtype=None, out=None):
 
 def cider_w4a4_linear_prequant(qx, w, block_size: int = 32, y_dtype=torch.float16, out=None):
     """As cider_w4a4_linear for rows that cider_quantize_fp4 has quantized already."""
-    _block(block_size)
     c, dev, n, k = _fp4_args(w, block_size, "w")
     a, _, m, kx = _fp4_args(qx, block_size, "qx", dev)
     if kx != k:
         raise ValueError(f"qx has {kx} columns, w {k}")
-    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    y, yp = _result(out, (m, n), y_dtype, w[0], "out")
     _launch((_lib or _load()).cider_w4a4_linear_prequant, dev, (a, c, yp, _DTYPES[y_dtype], _raw_stream(dev)))
     return y
 
 
 def _gate_up(gate, up, block_size, activation):
-    _block(block_size)
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
     g, dev, f, k = _fp4_args(gate, block_size, "gate")
@@ -810,7 +810,7 @@ def cider_w4a4_gated_linear(x, gate, up, block_size: int = 32, activation="silu"
     g, u, dev, f, k, act = _gate_up(gate, up, block_size, activation)
     kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
     h_dtype = x.dtype if h_dtype is None else h_dtype
-    h, hp = _result(out, (m, f), h_dtype, dev, "out")
+    h, hp = _result(out, (m, f), h_dtype, gate[0], "out")
     _launch((_lib or _load()).cider_w4a4_gated_linear, dev, (x.data_ptr(), kind, stride, m, g, u, act, hp,
             _DTYPES[h_dtype], _raw_stream(dev)))
     return h
@@ -823,7 +823,7 @@ def cider_w4a4_gated_linear_prequant(qx, gate, up, block_size: int = 32, activat
     a, _, m, kx = _fp4_args(qx, block_size, "qx", dev)
     if kx != k:
         raise ValueError(f"qx has {kx} columns, gate {k}")
-    h, hp = _result(out, (m, f), h_dtype, dev, "out")
+    h, hp = _result(out, (m, f), h_dtype, gate[0], "out")
     _launch((_lib or _load()).cider_w4a4_gated_linear_prequant, dev, (a, g, u, act, hp, _DTYPES[h_dtype],
             _raw_stream(dev)))
     return h
@@ -838,7 +838,7 @@ def cider_w4a4_feed_forward(x, gate, up, down, block_size: int = 32, activation=
         raise ValueError(f"down has {fd} columns, gate {f} rows")
     kind, stride, m = _wide_rows(x, k, _DTYPES, dev)
     y_dtype = x.dtype if y_dtype is None else y_dtype
-    y, yp = _result(out, (m, n), y_dtype, dev, "out")
+    y, yp = _result(out, (m, n), y_dtype, gate[0], "out")
     _launch((_lib or _load()).cider_w4a4_feed_forward, dev, (x.data_ptr(), kind, stride, m, g, u, d, act, yp,
             _DTYPES[y_dtype], _raw_stream(dev)))
     return y

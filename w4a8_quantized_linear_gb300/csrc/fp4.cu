@@ -42,60 +42,65 @@ __device__ __forceinline__ int64_t scale_at(int64_t r, int j, int tiles) {
 template <int BS>
 __device__ __forceinline__ void store_scales(const QuantArgs& p, int64_t r, int first, uint32_t byte, int lane) {
   constexpr int kStep = BS / 16;   // lanes of a block
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, byte, (lane & ~(4 * kStep - 1)) + i * kStep) << (8 * i);
+  uint32_t word = byte << (8 * (lane / kStep & 3));
+  word |= __shfl_xor_sync(0xffffffffu, word, kStep);
+  word |= __shfl_xor_sync(0xffffffffu, word, 2 * kStep);
   if ((lane & (4 * kStep - 1)) == 0) {
     const int j = first / BS;      // `first`: the lane's first value of the row
     if (r < p.padded && j < 4 * p.tiles) *reinterpret_cast<uint32_t*>(p.scales + scale_at(r, j, p.tiles)) = word;
   }
 }
 
-// `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA.
+// `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA at a time.  The next
+// rows' values are on their way while these are encoded.
 template <typename T, int BS>
 __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) {
-  __shared__ float part[32];
+  __shared__ uint32_t part[2][32];
   if (release) pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / warps, w = warp - sub * warps;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (32 * warps)) + sub;
+  const int per = blockDim.x / (32 * warps);
   const int k = (w * 32 + lane) * 16;
-  const bool have = r < p.rows && k < p.K;   // K % 32 == 0: a thread's 16 values are all in or all out
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  if (have) load16(static_cast<const T*>(p.x) + r * p.x_stride + k, v);
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = max_abs_nan(top, v[i]);
-  float inv_row = 1.0f;
-  bool bad = false;
-  if constexpr (BS == 32) {
-    top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  } else {
-    float most = top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max_abs_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (warps > 1) {
-      if (lane == 0) part[warp] = most;
-      __syncthreads();
-      for (int i = 0; i < warps; ++i) most = max_abs_nan(most, part[sub * warps + i]);
+  const bool in = k < p.K;   // K % 32 == 0: a thread's 16 values are all in or all out
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * per + sub;
+  const T* x = static_cast<const T*>(p.x) + k;
+  Sixteen<T> next;
+  next.clear();
+  if (in && r < p.rows) next.load(x + r * p.x_stride);
+  // every thread of the CTA makes the same turns
+  for (int64_t turn = static_cast<int64_t>(blockIdx.x) * per, n = 0; turn < p.padded; turn += step, r += step, ++n) {
+    const Sixteen<T> v = next;
+    const bool have = in && r < p.rows;
+    next.clear();
+    if (in && r + step < p.rows) next.load(x + (r + step) * p.x_stride);
+    uint32_t top = v.top();
+    float inv_row = 1.0f;
+    bool bad = false;
+    if constexpr (BS == 32) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    } else {
+      uint32_t most = __reduce_max_sync(0xffffffffu, top);
+      if (warps > 1) {
+        if (lane == 0) part[n & 1][warp] = most;
+        __syncthreads();
+        for (int i = 0; i < warps; ++i) most = max(most, part[n & 1][sub * warps + i]);
+      }
+      bad = not_finite(most);
+      inv_row = pow2(-row_power(most));
+      if (w == 0 && lane == 0 && r < p.rows) p.row[r] = row_scale(most);
     }
-    bad = not_finite(most);
-    const int e = row_power(most);
-    inv_row = pow2(-e);
-    if (w == 0 && lane == 0 && r < p.rows) p.row[r] = bad ? __uint_as_float(0x7FC00000u) : pow2(e);
+    uint32_t c[2] = {0u, 0u}, byte = 0u;
+    if (have && !bad) byte = encode16<T, BS>(v, top, inv_row, c);
+    if (have) *reinterpret_cast<uint2*>(p.codes + r * (p.K >> 1) + (k >> 1)) = make_uint2(c[0], c[1]);
+    store_scales<BS>(p, r, k, byte, lane);
   }
-  uint32_t c[2] = {0u, 0u}, byte = 0u;
-  if (have && !bad) byte = encode16<BS>(v, top, inv_row, c);
-  if (have) *reinterpret_cast<uint2*>(p.codes + r * (p.K >> 1) + (k >> 1)) = make_uint2(c[0], c[1]);
-  store_scales<BS>(p, r, k, byte, lane);
 }
 
 // Rows of any length: one CTA a row, which is read twice for the row's scale.
 template <typename T, int BS>
 __global__ void __launch_bounds__(1024) quantize_fp4_long_kernel(const QuantArgs p, bool release) {
-  __shared__ float part[32];
+  __shared__ uint32_t part[32];
   if (release) pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t r = blockIdx.x;
@@ -104,53 +109,49 @@ __global__ void __launch_bounds__(1024) quantize_fp4_long_kernel(const QuantArgs
   float inv_row = 1.0f;
   bool bad = false;
   if constexpr (BS == 16) {
-    float most = 0.0f;
+    uint32_t most = 0u;
     if (row_here)
       for (int k = threadIdx.x * 16; k < p.K; k += 1024 * 16) {
-        float v[16];
-        load16(x + k, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) most = max_abs_nan(most, v[i]);
+        Sixteen<T> v;
+        v.load(x + k);
+        most = max(most, v.top());
       }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max_abs_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) part[threadIdx.x >> 5] = most;
     __syncthreads();
-    for (int i = 0; i < 32; ++i) most = max_abs_nan(most, part[i]);
+    for (int i = 0; i < 32; ++i) most = max(most, part[i]);
     bad = not_finite(most);
-    const int e = row_power(most);
-    inv_row = pow2(-e);
-    if (threadIdx.x == 0 && row_here) p.row[r] = bad ? __uint_as_float(0x7FC00000u) : pow2(e);
+    inv_row = pow2(-row_power(most));
+    if (threadIdx.x == 0 && row_here) p.row[r] = row_scale(most);
   }
   // whole warps together: the scales' bytes are gathered over the lanes
   const int span = 4 * BS * p.tiles;
   for (int k0 = (threadIdx.x & ~31) * 16; k0 < span; k0 += 1024 * 16) {
     const int k = k0 + lane * 16;
     const bool have = row_here && k < p.K;
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    if (have) load16(x + k, v);
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max_abs_nan(top, v[i]);
-    if constexpr (BS == 32) top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    Sixteen<T> v;
+    v.clear();
+    if (have) v.load(x + k);
+    uint32_t top = v.top();
+    if constexpr (BS == 32) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     uint32_t c[2] = {0u, 0u}, byte = 0u;
-    if (have && !bad) byte = encode16<BS>(v, top, inv_row, c);
+    if (have && !bad) byte = encode16<T, BS>(v, top, inv_row, c);
     if (have) *reinterpret_cast<uint2*>(p.codes + r * (p.K >> 1) + (k >> 1)) = make_uint2(c[0], c[1]);
     store_scales<BS>(p, r, k, byte, lane);
   }
 }
 
 template <typename T, int BS>
-cudaError_t launch_quantize(const QuantArgs& p, cudaStream_t st, bool release) {
+cudaError_t launch_quantize(const QuantArgs& p, int num_sms, cudaStream_t st, bool release) {
   if (p.K > kRowK) {
     quantize_fp4_long_kernel<T, BS><<<static_cast<unsigned>(p.padded), 1024, 0, st>>>(p, release);
     return cudaGetLastError();
   }
   const int warps = (p.K + 511) / 512;
-  const int per = warps >= 8 ? 1 : 8 / warps;
-  quantize_fp4_kernel<T, BS><<<static_cast<unsigned>((p.padded + per - 1) / per), 32 * warps * per, 0, st>>>(p, warps, release);
+  const int per = warps >= 8 ? 1 : 8 / warps, threads = 32 * warps * per;
+  // as many CTAs as run at once (registers hold 1280 threads an SM), so that rows follow each other in a CTA
+  const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * (1280 / threads);
+  quantize_fp4_kernel<T, BS><<<static_cast<unsigned>(groups < most ? groups : most), threads, 0, st>>>(p, warps, release);
   return cudaGetLastError();
 }
 
@@ -160,48 +161,70 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
-// The value of a code: 0, 1/2, 1, 3/2, 2, 3, 4, 6, twice each in four bits.
-__device__ __forceinline__ float e2m1(uint32_t c) {
-  const float m = static_cast<float>((0xC8643210u >> (4 * (c & 7u))) & 15u) * 0.5f;
-  return c & 8u ? -m : m;
+// Two codes of a byte -> their values in fp32.
+__device__ __forceinline__ float2 e2m1_pair(uint32_t word, int byte) {
+  uint32_t h;
+  switch (byte) {   // unrolled: one instruction each
+    case 0: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(word)); break;
+    case 1: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(word)); break;
+    case 2: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(h) : "r"(word)); break;
+    default: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(h) : "r"(word)); break;
+  }
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A thread reads 8 bytes of codes and writes 16 values; `threads` a row, rows by the CTA's second index.
 template <typename T, int BS>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                             const float* row, int64_t rows, int K, int tiles, T* x) {
-  const int per_row = K / 16;
-  const int64_t n = rows * per_row, step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
-    const int64_t r = i / per_row;
-    const int k = static_cast<int>(i - r * per_row) * 16;
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + r * (K >> 1) + (k >> 1));
-    const float b = scale_value<BS>(scales[scale_at(r, k / BS, tiles)]);
-    const float s = row ? row[r] : 1.0f;
-    float v[16];
+                                                             const float* row, int64_t rows, int K, int tiles,
+                                                             bool wide, T* x) {
+  const int per_row = K >> 4;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * blockDim.y) {
+    const float s = row ? __ldg(row + r) : 1.0f;
+    for (int i = threadIdx.x; i < per_row; i += blockDim.x) {
+      const int k = i * 16;
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + r * (K >> 1) + (k >> 1));
+      const float b = scale_value<BS>(scales[scale_at(r, k / BS, tiles)]);
+      float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = e2m1(((j < 8 ? c.x : c.y) >> (4 * (j & 7))) & 15u) * b * s;
-    T* d = x + r * K + k;
-    if constexpr (sizeof(T) == 4) {
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = e2m1_pair(j < 4 ? c.x : c.y, j & 3);
+        v[2 * j] = f.x * b * s;
+        v[2 * j + 1] = f.y * b * s;
+      }
+      constexpr int kWords = 4 * sizeof(T);
+      uint32_t o[kWords];
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        reinterpret_cast<float4*>(d)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-      constexpr bool kBf = __is_same(T, __nv_bfloat16);
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(v[j]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        reinterpret_cast<uint4*>(d)[j] =
-            make_uint4(y_bits2<kBf>(v[8 * j], v[8 * j + 1]), y_bits2<kBf>(v[8 * j + 2], v[8 * j + 3]),
-                       y_bits2<kBf>(v[8 * j + 4], v[8 * j + 5]), y_bits2<kBf>(v[8 * j + 6], v[8 * j + 7]));
+        for (int j = 0; j < 8; ++j) o[j] = y_bits2<__is_same(T, __nv_bfloat16)>(v[2 * j], v[2 * j + 1]);
+      }
+      uint32_t* d = reinterpret_cast<uint32_t*>(x + r * K + k);
+      if (wide) {   // 32-byte boundaries: whole sectors
+#pragma unroll
+        for (int j = 0; j < kWords / 8; ++j) st_global_v8(d + 8 * j, o + 8 * j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kWords / 4; ++j)
+          reinterpret_cast<uint4*>(d)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      }
     }
   }
 }
 
 template <typename T, int BS>
-cudaError_t launch_dequantize(const FpMat& q, int64_t K, T* x, cudaStream_t st) {
-  const int64_t n = q.rows * (K / 16);
-  const int64_t grid = (n + 255) / 256;
-  dequantize_fp4_kernel<T, BS><<<static_cast<unsigned>(grid < 1 << 20 ? grid : 1 << 20), 256, 0, st>>>(
-      q.codes, q.scales, q.row, q.rows, static_cast<int>(K), fp4_tiles(K, BS), x);
+cudaError_t launch_dequantize(const FpMat& q, int64_t K, T* x, int num_sms, cudaStream_t st) {
+  // threads along a row: the smallest power of two that covers it, up to a CTA
+  unsigned tx = 1;
+  while (tx < 256 && tx * 16 < K) tx *= 2;
+  const dim3 block(tx, 256 / tx);
+  const int64_t groups = (q.rows + block.y - 1) / block.y, most = static_cast<int64_t>(num_sms) * 16;
+  dequantize_fp4_kernel<T, BS><<<static_cast<unsigned>(groups < most ? groups : most), block, 0, st>>>(
+      q.codes, q.scales, q.row, q.rows, static_cast<int>(K), fp4_tiles(K, BS),
+      reinterpret_cast<uintptr_t>(x) % 32 == 0, x);
   return cudaGetLastError();
 }
 
@@ -209,27 +232,27 @@ cudaError_t launch_dequantize(const FpMat& q, int64_t K, T* x, cudaStream_t st) 
 
 cudaError_t launch_quantize_fp4(const void* x, int dtype, int64_t x_stride, int64_t rows, int64_t K,
                                 int block, uint8_t* codes, uint8_t* scales, float* row, bool pad,
-                                cudaStream_t st, bool release) {
+                                int num_sms, cudaStream_t st, bool release) {
   const int64_t padded = pad ? (rows + kFpTileRows - 1) / kFpTileRows * kFpTileRows : rows;
   const QuantArgs p{x, x_stride, rows, padded, static_cast<int>(K), fp4_tiles(K, block), codes, scales, row};
   if (block == 16)
-    return dtype == CIDER_F16    ? launch_quantize<__half, 16>(p, st, release)
-           : dtype == CIDER_BF16 ? launch_quantize<__nv_bfloat16, 16>(p, st, release)
-                                 : launch_quantize<float, 16>(p, st, release);
-  return dtype == CIDER_F16    ? launch_quantize<__half, 32>(p, st, release)
-         : dtype == CIDER_BF16 ? launch_quantize<__nv_bfloat16, 32>(p, st, release)
-                               : launch_quantize<float, 32>(p, st, release);
+    return dtype == CIDER_F16    ? launch_quantize<__half, 16>(p, num_sms, st, release)
+           : dtype == CIDER_BF16 ? launch_quantize<__nv_bfloat16, 16>(p, num_sms, st, release)
+                                 : launch_quantize<float, 16>(p, num_sms, st, release);
+  return dtype == CIDER_F16    ? launch_quantize<__half, 32>(p, num_sms, st, release)
+         : dtype == CIDER_BF16 ? launch_quantize<__nv_bfloat16, 32>(p, num_sms, st, release)
+                               : launch_quantize<float, 32>(p, num_sms, st, release);
 }
 
 cudaError_t launch_dequantize_fp4(const FpMat& q, int64_t K, int block, void* x, int dtype,
-                                  cudaStream_t st) {
+                                  int num_sms, cudaStream_t st) {
   if (block == 16)
-    return dtype == CIDER_F16    ? launch_dequantize<__half, 16>(q, K, static_cast<__half*>(x), st)
-           : dtype == CIDER_BF16 ? launch_dequantize<__nv_bfloat16, 16>(q, K, static_cast<__nv_bfloat16*>(x), st)
-                                 : launch_dequantize<float, 16>(q, K, static_cast<float*>(x), st);
-  return dtype == CIDER_F16    ? launch_dequantize<__half, 32>(q, K, static_cast<__half*>(x), st)
-         : dtype == CIDER_BF16 ? launch_dequantize<__nv_bfloat16, 32>(q, K, static_cast<__nv_bfloat16*>(x), st)
-                               : launch_dequantize<float, 32>(q, K, static_cast<float*>(x), st);
+    return dtype == CIDER_F16    ? launch_dequantize<__half, 16>(q, K, static_cast<__half*>(x), num_sms, st)
+           : dtype == CIDER_BF16 ? launch_dequantize<__nv_bfloat16, 16>(q, K, static_cast<__nv_bfloat16*>(x), num_sms, st)
+                                 : launch_dequantize<float, 16>(q, K, static_cast<float*>(x), num_sms, st);
+  return dtype == CIDER_F16    ? launch_dequantize<__half, 32>(q, K, static_cast<__half*>(x), num_sms, st)
+         : dtype == CIDER_BF16 ? launch_dequantize<__nv_bfloat16, 32>(q, K, static_cast<__nv_bfloat16*>(x), num_sms, st)
+                               : launch_dequantize<float, 32>(q, K, static_cast<float*>(x), num_sms, st);
 }
 
 }  // namespace cider

@@ -77,7 +77,7 @@ cudaError_t product(cider::FpProduct& p, const cider::FpMat& held) {
     if (quantizes_itself(p)) return cider::launch_fp4_rows(p);
     const cudaError_t e = cider::launch_quantize_fp4(
         p.wide_x, p.x_bf16 ? CIDER_BF16 : CIDER_F16, p.x_stride, p.M, p.K, p.block, const_cast<uint8_t*>(held.codes),
-        const_cast<uint8_t*>(held.scales), const_cast<float*>(held.row), false, p.st, true);
+        const_cast<uint8_t*>(held.scales), const_cast<float*>(held.row), false, p.num_sms, p.st, true);
     if (e != cudaSuccess) return e;
     p.x = held;
     p.wide_x = nullptr;
@@ -206,10 +206,11 @@ cider_status_t cider_quantize_fp4(const void* x, int x_dtype, int64_t x_stride, 
         !valid_stride(x_stride, q->cols, x_dtype == CIDER_F32 ? 4 : 2))
       return CIDER_ERR_INVALID_ARGUMENT;
     if (!aligned(x, 16) || !well_aligned(q)) return CIDER_ERR_MISALIGNED;
-    const cider_status_t s = cider::check_device(nullptr, nullptr);
+    int sms = 0;
+    const cider_status_t s = cider::check_device(nullptr, &sms);
     if (s != CIDER_OK) return s;
     return cuda_status(cider::launch_quantize_fp4(x, x_dtype, x_stride, q->rows, q->cols, q->block_size, q->codes,
-                                                  q->scales, q->row_scale, true,
+                                                  q->scales, q->row_scale, true, sms,
                                                   static_cast<cudaStream_t>(stream), false));
   });
 }
@@ -220,9 +221,10 @@ cider_status_t cider_dequantize_fp4(const cider_fp4_t* q, void* x, int x_dtype, 
     if (q->rows == 0) return CIDER_OK;
     if (!valid(q) || !x || (!valid16(x_dtype) && x_dtype != CIDER_F32)) return CIDER_ERR_INVALID_ARGUMENT;
     if (!aligned(x, 16) || !well_aligned(q)) return CIDER_ERR_MISALIGNED;
-    const cider_status_t s = cider::check_device(nullptr, nullptr);
+    int sms = 0;
+    const cider_status_t s = cider::check_device(nullptr, &sms);
     if (s != CIDER_OK) return s;
-    return cuda_status(cider::launch_dequantize_fp4(mat(q), q->cols, q->block_size, x, x_dtype,
+    return cuda_status(cider::launch_dequantize_fp4(mat(q), q->cols, q->block_size, x, x_dtype, sms,
                                                     static_cast<cudaStream_t>(stream)));
   });
 }

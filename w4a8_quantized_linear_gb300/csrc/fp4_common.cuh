@@ -91,106 +91,162 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return g * r * u;
 }
 // ------------------------------------------------------------ quantization of 16 values
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+// Two fp32 numbers, low and high half, and their packed arithmetic (each rounded as alone).
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 u = ld_stream_v4(p + 4 * i);
-    v[4 * i] = __uint_as_float(u.x);
-    v[4 * i + 1] = __uint_as_float(u.y);
-    v[4 * i + 2] = __uint_as_float(u.z);
-    v[4 * i + 3] = __uint_as_float(u.w);
-  }
-}
+// Sixteen values as they were loaded.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
+struct Sixteen {
+  static constexpr int kWords = 4 * sizeof(T);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = ld_stream_v4(p + 8 * i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
-        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[8 * i + 2 * j] = f.x;
-        v[8 * i + 2 * j + 1] = f.y;
-      }
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 u = ld_stream_v4(reinterpret_cast<const uint32_t*>(p) + 4 * i);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
     }
   }
-}
+  // The largest |x| as the bits of an fp32 number: these are ordered like |x|, infinity and NaN above
+  // all numbers.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      if constexpr (__is_same(T, __nv_bfloat16)) return m << 16;
+      return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    }
+  }
+  // Values 2 i and 2 i + 1 in fp32.
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(T) == 4) return pack2(w[2 * i], w[2 * i + 1]);
+    if constexpr (__is_same(T, __nv_bfloat16)) return pack2(w[i] << 16, w[i] & 0xFFFF0000u);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    return pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+  }
+};
 
-// Eight values -> their E2M1 codes (nearest, ties to even, at most 6), the first in the low nibble.
-__device__ __forceinline__ uint32_t e2m1x8(const float* q) {
+// Eight quotients -> their E2M1 codes (nearest, ties to even, at most 6), the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t* q) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 l, h;\n\t"
+      "mov.b64 {l, h}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 a, h, l;\n\t"
+      "mov.b64 {l, h}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, h, l;\n\t"
+      "mov.b64 {l, h}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, h, l;\n\t"
+      "mov.b64 {l, h}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 d, h, l;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+      : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
+  return r;
+}
+// The same through fp16.
+__device__ __forceinline__ uint32_t e2m1x8_f16(const uint64_t* q) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 l, h;\n\t.reg .b32 p;\n\t"
+      "mov.b64 {l, h}, %1;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 a, p;\n\t"
+      "mov.b64 {l, h}, %2;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b, p;\n\t"
+      "mov.b64 {l, h}, %3;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 c, p;\n\t"
+      "mov.b64 {l, h}, %4;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 d, p;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
   return r;
 }
 
-// A finite maximum a > 0 as mantissa and exponent: the smallest k with a <= m * 2^k, for m = f 2^w
-// given as the bits of f behind the leading one.  Subnormal a gives the exponent field's 0.
-__device__ __forceinline__ int power_for(float a, uint32_t f_bits, int w) {
-  const uint32_t u = __float_as_uint(a);
-  return static_cast<int>(u >> 23) - 127 - w + ((u & 0x7FFFFFu) > f_bits ? 1 : 0);
+// The smallest k with a <= m * 2^k for a finite a > 0 given by its bits and m = f 2^w, f given as the
+// bits behind its leading one (a subnormal a counts as the least normal number or less).
+__device__ __forceinline__ int power_for(uint32_t a, uint32_t f_bits, int w) {
+  return static_cast<int>(a >> 23) - 127 - w + ((a & 0x7FFFFFu) > f_bits ? 1 : 0);
 }
-
-__device__ __forceinline__ bool not_finite(float a) { return __float_as_uint(a) >= 0x7F800000u; }
-
+__device__ __forceinline__ bool not_finite(uint32_t a) { return a >= 0x7F800000u; }
 // 2^k, k of -127 .. 127.
 __device__ __forceinline__ float pow2(int k) {
   return k == -127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
-
-// The row's scale from its maximum: at least 2^-126, 1 for zeros, NaN where a value is not finite.
-__device__ __forceinline__ int row_power(float a) {
-  if (!(a > 0.0f)) return 0;
-  return max(power_for(a, 0x280000u, 11), -126);   // 2688 = 1.3125 * 2^11
+// The exponent of a row's scale from the bits of its maximum: at least -126, 0 for zeros.
+__device__ __forceinline__ int row_power(uint32_t a) {
+  return a == 0u ? 0 : max(power_for(a, 0x280000u, 11), -126);   // 2688 = 1.3125 * 2^11
+}
+// The row's scale: NaN where a value is not finite.
+__device__ __forceinline__ float row_scale(uint32_t a) {
+  return not_finite(a) ? __uint_as_float(0x7FC00000u) : pow2(row_power(a));
 }
 
-// 16 values with their block's maximum (block 32: of both halves) -> two words of codes, the scale byte.
-template <int BS>
-__device__ __forceinline__ uint32_t encode16(const float (&v)[16], float top, float inv_row, uint32_t (&c)[2]) {
-  float q[16];
-  uint32_t byte;
+// 16 values, their block's maximum (block 32: of both halves) and the inverse of the row's scale (a
+// power of two; 1 for block 32) -> two words of codes, the scale byte.
+//   Block 32 and fp32 rows: the quotient by the block's scale is correctly rounded (by a power of two:
+// exact; else Markstein's correction of a product with the reciprocal, as in div_rn_by).
+//   16-bit rows in blocks of 16: x has 11 bits and b 4, so x / b is one of the seven borders between
+// codes (3 bits) or at least 2^-11 of it away, and more than half a step of fp16.  The product with
+// the rounded reciprocal is off by 2^-23; rounded to fp16 it is the border itself in the one case, and
+// on the right side of it in the other, and a border goes to the even code.
+template <typename T, int BS>
+__device__ __forceinline__ uint32_t encode16(const Sixteen<T>& v, uint32_t top, float inv_row, uint32_t (&c)[2]) {
+  uint64_t q[8];
+  c[0] = c[1] = 0u;
   if constexpr (BS == 32) {
-    if (not_finite(top)) {
-      c[0] = c[1] = 0u;
-      return 0xFFu;
-    }
-    const int e = top > 0.0f ? max(power_for(top, 0x400000u, 2), -127) : 0;   // 6 = 1.5 * 2^2
-    const float inv = pow2(-e);
+    if (not_finite(top)) return 0xFFu;
+    const int e = top != 0u ? max(power_for(top, 0x400000u, 2), -127) : 0;   // 6 = 1.5 * 2^2
+    const uint64_t inv = both(pow2(-e));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = v[i] * inv;
-    byte = static_cast<uint32_t>(e + 127);
+    for (int i = 0; i < 8; ++i) q[i] = mul2(v.pair(i), inv);
+    c[0] = e2m1x8(q);
+    c[1] = e2m1x8(q + 4);
+    return static_cast<uint32_t>(e + 127);
   } else {
-    const float t = __fdiv_rn(top * inv_row, 6.0f);
-    byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-    if (byte == 0) {
-      c[0] = c[1] = 0u;
-      return 0u;
-    }
+    const float t = __fdiv_rn(__uint_as_float(top) * inv_row, 6.0f);
+    const uint32_t byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+    if (byte == 0u) return 0u;
     const float b = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
     const float r = __frcp_rn(b);
+    if constexpr (sizeof(T) == 4) {
+      const uint64_t inv = both(inv_row), bb = both(-b), rr = both(r);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = div_rn_by(v[i] * inv_row, b, r);
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t x = mul2(v.pair(i), inv), q0 = mul2(x, rr);
+        q[i] = fma2(fma2(q0, bb, x), rr, q0);
+      }
+      c[0] = e2m1x8(q);
+      c[1] = e2m1x8(q + 4);
+    } else {
+      // both factors at once, unless their product passes what fp32 holds
+      const float s = r * inv_row;
+      const bool one = s < 3.0e38f;
+      const uint64_t f = both(one ? s : r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = mul2(one ? v.pair(i) : mul2(v.pair(i), both(inv_row)), f);
+      c[0] = e2m1x8_f16(q);
+      c[1] = e2m1x8_f16(q + 4);
+    }
+    return byte;
   }
-  c[0] = e2m1x8(q);
-  c[1] = e2m1x8(q + 8);
-  return byte;
 }
 #endif
 
@@ -207,9 +263,9 @@ struct FpMat {
 // reach only outputs that it does not store).  release: as in quant.cu.
 cudaError_t launch_quantize_fp4(const void* x, int dtype, int64_t x_stride, int64_t rows, int64_t K,
                                 int block, uint8_t* codes, uint8_t* scales, float* row, bool pad,
-                                cudaStream_t st, bool release);
+                                int num_sms, cudaStream_t st, bool release);
 cudaError_t launch_dequantize_fp4(const FpMat& q, int64_t K, int block, void* x, int dtype,
-                                  cudaStream_t st);
+                                  int num_sms, cudaStream_t st);
 
 // One product: y = x w^T, or with `up` h = act(x w^T) (x up^T).
 struct FpProduct {

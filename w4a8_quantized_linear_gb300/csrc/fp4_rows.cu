@@ -60,27 +60,21 @@ struct RowsArgs {
 };
 
 // The part of the rows of x that this CTA multiplies, quantized into shared memory.
-template <int BS>
+template <typename T, int BS>
 __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes, uint8_t* scales, uint32_t* most,
                                               float* row, int kb0, int kb1, int thread) {
   constexpr int kThreads = 32 * kRQuantWarps;
-  auto load = [&](int r, int k, float (&v)[16]) {
-    if (p.x_bf16)
-      load16(static_cast<const __nv_bfloat16*>(p.x) + r * p.x_stride + k, v);
-    else
-      load16(static_cast<const __half*>(p.x) + r * p.x_stride + k, v);
-  };
+  const T* x = static_cast<const T*>(p.x);
   if constexpr (BS == 16) {
-    // the rows' maxima; |x| is ordered like its bits, and a NaN comes out on top
     const int per = p.K >> 4, units = p.M * per;
+#pragma unroll 2
     for (int u0 = 0; u0 < units; u0 += kThreads) {
       const int u = u0 + thread, r = min(u, units - 1) / per;
       uint32_t top = 0;
       if (u < units) {
-        float v[16];
-        load(r, (u - r * per) * 16, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        Sixteen<T> v;
+        v.load(x + r * p.x_stride + (u - r * per) * 16);
+        top = v.top();
       }
       if (__match_any_sync(0xffffffffu, r) == 0xffffffffu) {
         top = __reduce_max_sync(0xffffffffu, top);
@@ -90,31 +84,25 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
       }
     }
     named_barrier_sync(1, kThreads);
-    if (thread < p.M) {
-      const float a = __uint_as_float(most[thread]);
-      row[thread] = not_finite(a) ? __uint_as_float(0x7FC00000u) : pow2(row_power(a));
-    }
+    if (thread < p.M) row[thread] = row_scale(most[thread]);
   }
   // whole steps of 64: zeros behind the end of the row
   const int k0 = kb0 * kFpStageK, k1 = min(kb1 * kFpStageK, p.nsteps * kFpStepK);
   const int per = (k1 - k0) >> 4, units = p.M * per;   // a multiple of 4: a block's two threads stay together
+#pragma unroll 2
   for (int u0 = 0; u0 < units; u0 += kThreads) {
     const int u = u0 + thread, r = min(u, units - 1) / per, i = u - r * per, k = k0 + 16 * i;
     const bool have = u < units && k < p.K;
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-    if (have) load(r, k, v);
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = max_abs_nan(top, v[j]);
+    Sixteen<T> v;
+    v.clear();
+    if (have) v.load(x + r * p.x_stride + k);
+    uint32_t top = v.top();
     uint32_t c[2] = {0u, 0u}, byte = 0u;
     if constexpr (BS == 32) {
-      top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      byte = encode16<BS>(v, top, 1.0f, c);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      byte = encode16<T, BS>(v, top, 1.0f, c);
     } else {
-      const float a = __uint_as_float(most[r]);
-      if (!not_finite(a)) byte = encode16<BS>(v, top, pow2(-row_power(a)), c);
+      if (!not_finite(most[r])) byte = encode16<T, BS>(v, top, pow2(-row_power(most[r])), c);
     }
     if (u >= units) continue;
     const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
@@ -158,17 +146,35 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.nkb / p.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.nkb / p.splits);
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+  const int tok_tiles = FUSE ? 0 : min(p.tok_tiles, (p.M + 127) / 128 - (m0 >> 7));
+  // bytes of scales that a stage has (the last one may have fewer tiles)
+  auto scale_bytes = [&](int kb) { return min(B::kTiles, p.sc_tiles - kb * B::kTiles) * kFpTileBytes; };
+  auto weights = [&](int kb, int s) {
+    const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
+    const int64_t from = (static_cast<int64_t>(nt) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes;
+    mbar_arrive_expect_tx(full_bar(s), (GATED ? 2u : 1u) * (kROperand + sb) + (FUSE ? 0u : p.tn * 128u) + tok_tiles * sb);
+    tma_load_2d(at, &tm_w, full_bar(s), kb * 128, nt * 128);
+    if (GATED) tma_load_2d(at + kROperand, &tm_u, full_bar(s), kb * 128, nt * 128);
+    bulk_load(at + p.sfw_offset, p.scw + from, sb, full_bar(s));
+    if (GATED) bulk_load(at + p.sfu_offset, p.scu + from, sb, full_bar(s));
+  };
+  const int ahead = min(kb1 - kb0, p.stages);   // stages whose slots nothing has used before
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(full_bar(s), 1);
+        mbar_init(empty_bar(s), 1);
+      }
+      mbar_init(acc_bar, 1);
+      mbar_init(x_bar, kRQuantWarps);
+      *abort_flag = 0u;
+      fence_mbar_init();
+      // the weights are asked for before anything else is set up
+      for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
     }
-    mbar_init(acc_bar, 1);
-    mbar_init(x_bar, kRQuantWarps);
-    *abort_flag = 0u;
-    fence_mbar_init();
+    __syncwarp();
   }
-  if (FUSE && threadIdx.x >= 32 && threadIdx.x < 32 + kRTokens) most[threadIdx.x - 32] = 0u;
+  if (FUSE && threadIdx.x >= 64 && threadIdx.x < 64 + kRTokens) most[threadIdx.x - 64] = 0u;
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
@@ -182,18 +188,6 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     if (elect_one()) {
-      const int tok_tiles = FUSE ? 0 : min(p.tok_tiles, (p.M + 127) / 128 - (m0 >> 7));
-      // bytes of scales that a stage has (the last one may have fewer tiles)
-      auto scale_bytes = [&](int kb) { return min(B::kTiles, p.sc_tiles - kb * B::kTiles) * kFpTileBytes; };
-      auto weights = [&](int kb, int s) {
-        const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
-        const int64_t from = (static_cast<int64_t>(nt) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes;
-        mbar_arrive_expect_tx(full_bar(s), (GATED ? 2u : 1u) * (kROperand + sb) + (FUSE ? 0u : p.tn * 128u) + tok_tiles * sb);
-        tma_load_2d(at, &tm_w, full_bar(s), kb * 128, nt * 128);
-        if (GATED) tma_load_2d(at + kROperand, &tm_u, full_bar(s), kb * 128, nt * 128);
-        bulk_load(at + p.sfw_offset, p.scw + from, sb, full_bar(s));
-        if (GATED) bulk_load(at + p.sfu_offset, p.scu + from, sb, full_bar(s));
-      };
       auto tokens = [&](int kb, int s) {
         const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
         tma_load_2d(at + p.tok_offset, &tm_x, full_bar(s), kb * 128, m0);
@@ -202,8 +196,6 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
                     p.scx + (static_cast<int64_t>((m0 >> 7) + t) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes, sb,
                     full_bar(s));
       };
-      const int ahead = min(kb1 - kb0, p.stages);
-      for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
       if (!FUSE) {
         pdl_wait();
         for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
@@ -278,7 +270,10 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
   } else if (FUSE) {
     // ------------------------------------------------------------ quantization of x
     pdl_wait();   // x may be what the launch just before wrote
-    quantize_part<BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
+    if (p.x_bf16)
+      quantize_part<__nv_bfloat16, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
+    else
+      quantize_part<__half, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(x_bar);
@@ -331,21 +326,27 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
       float a[GATED ? 8 : 4];
 #pragma unroll
       for (int i = 0; i < (GATED ? 8 : 4); ++i) a[i] = 0.0f;
-      for (int r = 0; r < p.splits; ++r) {
+      // all ranks' partial sums are asked for before the first is added
+      float4 f[8][GATED ? 2 : 1];
 #pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-          const uint32_t local = base + static_cast<uint32_t>(((h * p.tn + t) * 128 + 4 * (u & 31)) * 4);
-          float4 f;
-          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                       : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                       : "r"(mapa_shared(local, p.splits > 1 ? r : 0))
-                       : "memory");
-          a[4 * h] += f.x;
-          a[4 * h + 1] += f.y;
-          a[4 * h + 2] += f.z;
-          a[4 * h + 3] += f.w;
+      for (int r = 0; r < 8; ++r)
+        if (r < p.splits) {
+#pragma unroll
+          for (int h = 0; h < (GATED ? 2 : 1); ++h)
+            f[r][h] = ld_cluster_v4(mapa_shared(
+                base + static_cast<uint32_t>(((h * p.tn + t) * 128 + 4 * (u & 31)) * 4), p.splits > 1 ? r : 0));
         }
-      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < p.splits) {
+#pragma unroll
+          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            a[4 * h] += f[r][h].x;
+            a[4 * h + 1] += f[r][h].y;
+            a[4 * h + 2] += f[r][h].z;
+            a[4 * h + 3] += f[r][h].w;
+          }
+        }
       const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? __ldg(p.sx + m0 + t) : 1.0f;
       float out[4];
 #pragma unroll
