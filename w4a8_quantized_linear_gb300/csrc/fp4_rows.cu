@@ -60,27 +60,33 @@ struct RowsArgs {
 };
 
 // The part of the rows of x that this CTA multiplies, quantized into shared memory.
+// A thread asks for four units of 16 values before it works on the first.
 template <typename T, int BS>
 __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes, uint8_t* scales, uint32_t* most,
                                               float* row, int kb0, int kb1, int thread) {
-  constexpr int kThreads = 32 * kRQuantWarps;
+  constexpr int kThreads = 32 * kRQuantWarps, kBatch = 4;
   const T* x = static_cast<const T*>(p.x);
   if constexpr (BS == 16) {
     const int per = p.K >> 4, units = p.M * per;
-#pragma unroll 2
-    for (int u0 = 0; u0 < units; u0 += kThreads) {
-      const int u = u0 + thread, r = min(u, units - 1) / per;
-      uint32_t top = 0;
-      if (u < units) {
-        Sixteen<T> v;
-        v.load(x + r * p.x_stride + (u - r * per) * 16);
-        top = v.top();
+    for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
+      Sixteen<T> v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int u = u0 + j * kThreads + thread, r = u / per;
+        v[j].clear();
+        if (u < units) v[j].load(x + r * p.x_stride + (u - r * per) * 16);
       }
-      if (__match_any_sync(0xffffffffu, r) == 0xffffffffu) {
-        top = __reduce_max_sync(0xffffffffu, top);
-        if ((thread & 31) == 0) atomicMax(most + r, top);
-      } else {
-        atomicMax(most + r, top);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (u0 + j * kThreads >= units) break;
+        const int r = min(u0 + j * kThreads + thread, units - 1) / per;
+        uint32_t top = v[j].top();
+        if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
+          top = __reduce_max_sync(0xffffffffu, top);
+          if ((thread & 31) == 0) atomicMax(most + r, top);
+        } else {
+          atomicMax(most + r, top);
+        }
       }
     }
     named_barrier_sync(1, kThreads);
@@ -89,31 +95,38 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
   // whole steps of 64: zeros behind the end of the row
   const int k0 = kb0 * kFpStageK, k1 = min(kb1 * kFpStageK, p.nsteps * kFpStepK);
   const int per = (k1 - k0) >> 4, units = p.M * per;   // a multiple of 4: a block's two threads stay together
-#pragma unroll 2
-  for (int u0 = 0; u0 < units; u0 += kThreads) {
-    const int u = u0 + thread, r = min(u, units - 1) / per, i = u - r * per, k = k0 + 16 * i;
-    const bool have = u < units && k < p.K;
-    Sixteen<T> v;
-    v.clear();
-    if (have) v.load(x + r * p.x_stride + k);
-    uint32_t top = v.top();
-    uint32_t c[2] = {0u, 0u}, byte = 0u;
-    if constexpr (BS == 32) {
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      byte = encode16<T, BS>(v, top, 1.0f, c);
-    } else {
-      if (!not_finite(most[r])) byte = encode16<T, BS>(v, top, pow2(-row_power(most[r])), c);
+  for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
+    Sixteen<T> v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int u = u0 + j * kThreads + thread, r = u / per, k = k0 + 16 * (u - r * per);
+      v[j].clear();
+      if (u < units && k < p.K) v[j].load(x + r * p.x_stride + k);
     }
-    if (u >= units) continue;
-    const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
-    // 128-byte rows, their 16-byte pieces swizzled within groups of 8 rows
-    uint8_t* at = codes + kb * (kRTokens * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
-                  (((kk >> 5) ^ (r & 7)) << 4) + ((kk >> 1) & 8);
-    *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
-    // tiles half as far apart as they are long: rows 16 .. 31 are not there
-    if (BS == 16 || (i & 1) == 0)
-      scales[(kb * FpBlock<BS>::kTiles + kk / (4 * BS)) * (kFpTileBytes / 2) + 16 * r + (kk / BS & 3)] =
-          static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (u0 + j * kThreads >= units) break;
+      const int u = u0 + j * kThreads + thread, r = min(u, units - 1) / per, i = u - r * per, k = k0 + 16 * i;
+      uint32_t top = v[j].top();
+      uint32_t c[2] = {0u, 0u}, byte = 0u;
+      if constexpr (BS == 32) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        byte = encode16<T, BS>(v[j], top, 1.0f, c);
+      } else {
+        if (!not_finite(most[r])) byte = encode16<T, BS>(v[j], top, pow2(-row_power(most[r])), c);
+      }
+      if (u < units) {
+        const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
+        // 128-byte rows, their 16-byte pieces swizzled within groups of 8 rows
+        uint8_t* at = codes + kb * (kRTokens * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
+                      (((kk >> 5) ^ (r & 7)) << 4) + ((kk >> 1) & 8);
+        *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
+        // tiles half as far apart as they are long: rows 16 .. 31 are not there
+        if (BS == 16 || (i & 1) == 0)
+          scales[(kb * FpBlock<BS>::kTiles + kk / (4 * BS)) * (kFpTileBytes / 2) + 16 * r + (kk / BS & 3)] =
+              static_cast<uint8_t>(byte);
+      }
+    }
   }
 }
 
@@ -169,19 +182,22 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
       mbar_init(x_bar, kRQuantWarps);
       *abort_flag = 0u;
       fence_mbar_init();
-      // the weights are asked for before anything else is set up
-      for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
     }
     __syncwarp();
+    named_barrier_arrive(2, kThreads);   // this warp needs nothing of what the others set up
+    if (elect_one())
+      for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
+    __syncwarp();
+  } else {
+    if (FUSE && threadIdx.x >= 64 && threadIdx.x < 64 + kRTokens) most[threadIdx.x - 64] = 0u;
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, p.tmem_cols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    named_barrier_sync(2, kThreads);
+    tc_fence_after();
   }
-  if (FUSE && threadIdx.x >= 64 && threadIdx.x < 64 + kRTokens) most[threadIdx.x - 64] = 0u;
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, p.tmem_cols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + p.tail + 8 * kRBars);
   const int acc_cols = GATED ? 2 * p.tn : p.tn;
 
