@@ -66,10 +66,8 @@ struct Held {
 bool few_rows(const cider::FpProduct& p) { return p.M <= 128; }
 
 // Few enough that the product's kernel quantizes the rows itself, each CTA its part of K: one launch
-// instead of two.  Block size 16 needs the rows' maxima, for which every CTA reads all of x.
-bool quantizes_itself(const cider::FpProduct& p) {
-  return few_rows(p) && p.M <= 16 && (p.block == 32 || p.M * p.K <= 65536) && cider::fp4_rows_quantizes_itself(p);
-}
+// instead of two.
+bool quantizes_itself(const cider::FpProduct& p) { return few_rows(p) && cider::fp4_rows_quantizes_itself(p); }
 
 // A product of x in 16 bits: quantized into `held` (scratch) first, or by the product's kernel.
 cudaError_t product(cider::FpProduct& p, const cider::FpMat& held) {

@@ -33,6 +33,7 @@ constexpr int kRBars = 2 * kRMaxStages + 2;
 constexpr int kRTail = kRBars * 8 + 16 + 2 * 16 * 4;   // barriers, flags, the fused rows' maxima and scales
 constexpr int kRTokens = 16;                           // of the fused form
 constexpr int kRQuantWarps = 8;
+constexpr int kRBatch = 4;
 constexpr int kRMaxFusedStages = 16;                   // of a CTA's part of K, held whole
 
 struct RowsArgs {
@@ -59,72 +60,85 @@ struct RowsArgs {
   int* err;
 };
 
-// The part of the rows of x that this CTA multiplies, quantized into shared memory.
-// A thread asks for four units of 16 values before it works on the first.
+// The part of the rows of x that this CTA multiplies, quantized into shared memory.  A thread asks for
+// four units of 16 values before it works on the first; block size 16, which needs the rows' maxima,
+// keeps all of x in registers until it has them.
 template <typename T, int BS>
 __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes, uint8_t* scales, uint32_t* most,
                                               float* row, int kb0, int kb1, int thread) {
-  constexpr int kThreads = 32 * kRQuantWarps, kBatch = 4;
+  constexpr int kThreads = 32 * kRQuantWarps, kBatch = kRBatch;
   const T* x = static_cast<const T*>(p.x);
+  const int k0 = kb0 * kFpStageK;
+  // 16 values' codes and (one of the threads that hold a block) their block's scale
+  auto put = [&](int r, int k, const uint32_t (&c)[2], uint32_t byte, bool first) {
+    const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
+    // 128-byte rows, their 16-byte pieces swizzled within groups of 8 rows
+    uint8_t* at = codes + kb * (kRTokens * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((kk >> 5) ^ (r & 7)) << 4) +
+                  ((kk >> 1) & 8);
+    *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
+    // tiles half as far apart as they are long: rows 16 .. 31 are not there
+    if (first)
+      scales[(kb * FpBlock<BS>::kTiles + kk / (4 * BS)) * (kFpTileBytes / 2) + 16 * r + (kk / BS & 3)] =
+          static_cast<uint8_t>(byte);
+  };
   if constexpr (BS == 16) {
-    const int per = p.K >> 4, units = p.M * per;
-    for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
-      Sixteen<T> v[kBatch];
+    const int per = p.K >> 4, units = p.M * per;   // at most kBatch * kThreads
+    const uint32_t magic = 0xFFFFFFFFu / per + 1u;   // u / per = the high half of u magic: u per < 2^32
+    Sixteen<T> v[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int u = u0 + j * kThreads + thread, r = u / per;
-        v[j].clear();
-        if (u < units) v[j].load(x + r * p.x_stride + (u - r * per) * 16);
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      const int u = j * kThreads + thread, r = per == 1 ? u : __umulhi(u, magic);
+      v[j].clear();
+      if (u < units) v[j].load(x + r * p.x_stride + (u - r * per) * 16);
+    }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (u0 + j * kThreads >= units) break;
-        const int r = min(u0 + j * kThreads + thread, units - 1) / per;
-        uint32_t top = v[j].top();
-        if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
-          top = __reduce_max_sync(0xffffffffu, top);
-          if ((thread & 31) == 0) atomicMax(most + r, top);
-        } else {
-          atomicMax(most + r, top);
-        }
+    for (int j = 0; j < kBatch; ++j) {
+      if (j * kThreads >= units) break;
+      const int u = min(j * kThreads + thread, units - 1), r = per == 1 ? u : __umulhi(u, magic);
+      uint32_t top = v[j].top();
+      if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((thread & 31) == 0) atomicMax(most + r, top);
+      } else {
+        atomicMax(most + r, top);
       }
     }
     named_barrier_sync(1, kThreads);
     if (thread < p.M) row[thread] = row_scale(most[thread]);
-  }
-  // whole steps of 64: zeros behind the end of the row
-  const int k0 = kb0 * kFpStageK, k1 = min(kb1 * kFpStageK, p.nsteps * kFpStepK);
-  const int per = (k1 - k0) >> 4, units = p.M * per;   // a multiple of 4: a block's two threads stay together
-  for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
-    Sixteen<T> v[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int u = u0 + j * kThreads + thread, r = u / per, k = k0 + 16 * (u - r * per);
-      v[j].clear();
-      if (u < units && k < p.K) v[j].load(x + r * p.x_stride + k);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (u0 + j * kThreads >= units) break;
-      const int u = u0 + j * kThreads + thread, r = min(u, units - 1) / per, i = u - r * per, k = k0 + 16 * i;
-      uint32_t top = v[j].top();
+      const int u = j * kThreads + thread, r = per == 1 ? u : __umulhi(u, magic), k = (u - r * per) * 16;
+      if (u >= units || k < k0 || k >= kb1 * kFpStageK) continue;
       uint32_t c[2] = {0u, 0u}, byte = 0u;
-      if constexpr (BS == 32) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        byte = encode16<T, BS>(v[j], top, 1.0f, c);
-      } else {
-        if (!not_finite(most[r])) byte = encode16<T, BS>(v[j], top, pow2(-row_power(most[r])), c);
+      if (!not_finite(most[r])) byte = encode16<T, BS>(v[j], v[j].top(), pow2(-row_power(most[r])), c);
+      put(r, k, c, byte, true);
+    }
+    // zeros up to a whole step of 64
+    if (kb1 == p.nkb && (p.K & 32) != 0 && thread < 2 * p.M) {
+      const uint32_t c[2] = {0u, 0u};
+      put(thread >> 1, p.K + 16 * (thread & 1), c, 0u, true);
+    }
+  } else {
+    // whole steps of 64: zeros behind the end of the row
+    const int k1 = min(kb1 * kFpStageK, p.nsteps * kFpStepK);
+    const int per = (k1 - k0) >> 4, units = p.M * per;   // a multiple of 4: a block's two threads stay together
+    const uint32_t magic = 0xFFFFFFFFu / per + 1u;
+    for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
+      Sixteen<T> v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int u = u0 + j * kThreads + thread, r = __umulhi(u, magic), k = k0 + 16 * (u - r * per);
+        v[j].clear();
+        if (u < units && k < p.K) v[j].load(x + r * p.x_stride + k);
       }
-      if (u < units) {
-        const int kk = k & (kFpStageK - 1), kb = (k - k0) / kFpStageK;
-        // 128-byte rows, their 16-byte pieces swizzled within groups of 8 rows
-        uint8_t* at = codes + kb * (kRTokens * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
-                      (((kk >> 5) ^ (r & 7)) << 4) + ((kk >> 1) & 8);
-        *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
-        // tiles half as far apart as they are long: rows 16 .. 31 are not there
-        if (BS == 16 || (i & 1) == 0)
-          scales[(kb * FpBlock<BS>::kTiles + kk / (4 * BS)) * (kFpTileBytes / 2) + 16 * r + (kk / BS & 3)] =
-              static_cast<uint8_t>(byte);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int u = u0 + j * kThreads + thread, r = __umulhi(u, magic), k = k0 + 16 * (u - r * per);
+        uint32_t top = v[j].top();
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        uint32_t c[2] = {0u, 0u};
+        const uint32_t byte = encode16<T, BS>(v[j], top, 1.0f, c);
+        if (u < units) put(r, k, c, byte, (u & 1) == 0);
       }
     }
   }
@@ -443,18 +457,28 @@ bool plan(const FpProduct& p, bool fuse, RowsArgs& a, int* smem_out, int* tiles_
   const int cols = sides * a.tn + (sides + a.tok_tiles) * cols_side;
   a.tmem_cols = 64;
   while (static_cast<int>(a.tmem_cols) < cols) a.tmem_cols *= 2;
-  // CTAs that hold at most half of the tensor memory share an SM in pairs (their shared memory
-  // allows two and no third), the others have one to themselves: no CTA of a cluster waits for
-  // tensor memory that another cluster's holds.
-  const bool two = a.tmem_cols <= 256;
-  int budget = two ? 110 * 1024 : 224 * 1024;
+  // As many CTAs as SMs, or a few more, K split in a power of two.  Measured (two more splits, a CTA
+  // or two on each SM): one token through 4096 x 4096, 32 tiles in 4 parts 5.7 us, in 8 parts 7.4; 16
+  // through 2560 x 10240, 20 tiles in 8 parts 10.6, in 4 parts 11.8; 128 through 10240 x 2560, 80 tiles
+  // in 2 parts 12.9, whole 14.3.  Other numbers of parts lose 5 us to the placing of their clusters.
+  // Where there are more CTAs than SMs they share SMs in pairs: they hold at most half of the tensor
+  // memory, and their shared memory allows two and no third.  All others have an SM to themselves.  So
+  // no CTA of a cluster waits for tensor memory that another cluster's holds.
   const int tiles = a.m_tiles * static_cast<int>((p.N + 127) / 128);
+  const int room = a.tmem_cols <= 256 ? p.num_sms + p.num_sms / 16 : p.num_sms;
   a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= p.num_sms * (two ? 2 : 1) && a.nkb >= a.splits * 2) a.splits *= 2;
+  while (a.splits < 8 && tiles * a.splits * 2 <= room && a.nkb >= a.splits * 4) a.splits *= 2;
+  const bool two = a.tmem_cols <= 256 && tiles * a.splits > p.num_sms;
+  const int budget = two ? 110 * 1024 : 224 * 1024;
   const int mine = (a.nkb + a.splits - 1) / a.splits;   // stages of a CTA, at most
   int held = 0;
   if (fuse) {
     if (p.M > kRTokens || mine > kRMaxFusedStages) return false;
+    // All of x in the threads' registers (block size 16), or a part that is soon done: 16 tokens' parts of
+    // 1280 values cost 3 us more than rows that are quantized already, of 4096 values 5 us; a launch of its
+    // own 1 us, and the caller 6 us of host time.
+    const int64_t values = p.block == 16 ? p.M * p.K : p.M * mine * kFpStageK;
+    if (values > (p.block == 16 ? 16 * kRBatch * 32 * kRQuantWarps : 32768)) return false;
     // the last tile of scales is read to its end, half a tile behind the next one's start
     held = mine * (kRTokens * 128) + (mine * per_tiles + 1) * (kFpTileBytes / 2);
     held = (held + 1023) / 1024 * 1024;
