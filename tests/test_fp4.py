@@ -448,3 +448,19 @@ def test_few_tokens_have_the_bits_of_quantized_ones(m, n, k, dtype, block):
     y = cider.cider_w4a4_linear(x, w, block)
     close(y, a @ b.T, ref.sum_bound(a, b) + ref.half_step(dtype, a @ b.T) * (1 + 2.0 ** -10))
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=str)
+@pytest.mark.parametrize("power", [-125, -112, -101, -99, 60, 99, 101, 112])
+def test_quantize_rows_far_from_one(dtype, power):
+    """Rows whose scales, or their products with the blocks', come near the ends of fp32."""
+    gen = generator(str(dtype), power)
+    x = (normal(gen, 40, 96) * torch.exp2(-20 * torch.rand(40, 96, generator=gen, device="cuda"))).double()
+    x = (x * 2.0 ** power).to(dtype)
+    for block in (16, 32):
+        q = cider.cider_quantize_fp4(x, block)
+        codes, held, row = ref.quantize(x, block)
+        assert torch.equal(q[1], ref.tiles(held)) and (row is None or torch.equal(q[2], row))
+        assert torch.equal(torch.stack((q[0] & 15, q[0] >> 4), -1).flatten(1).long(), codes)
+    clean()

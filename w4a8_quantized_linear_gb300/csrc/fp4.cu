@@ -38,17 +38,19 @@ __device__ __forceinline__ int64_t scale_at(int64_t r, int j, int tiles) {
   return ((r >> 7) * tiles + (j >> 2)) * kFpTileBytes + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (j & 3);
 }
 
-// Four neighbouring blocks' bytes, one word of a tile: gathered over the lanes that hold them.
+// Four neighbouring blocks' bytes, one word of a tile: gathered over the lanes that hold them.  `at`: the
+// row's place in its first tile, or null; `first`: the lane's first value of the row.
 template <int BS>
-__device__ __forceinline__ void store_scales(const QuantArgs& p, int64_t r, int first, uint32_t byte, int lane) {
+__device__ __forceinline__ void store_scales(uint8_t* at, int tiles, int first, uint32_t byte, int lane) {
   constexpr int kStep = BS / 16;   // lanes of a block
   uint32_t word = byte << (8 * (lane / kStep & 3));
   word |= __shfl_xor_sync(0xffffffffu, word, kStep);
   word |= __shfl_xor_sync(0xffffffffu, word, 2 * kStep);
-  if ((lane & (4 * kStep - 1)) == 0) {
-    const int j = first / BS;      // `first`: the lane's first value of the row
-    if (r < p.padded && j < 4 * p.tiles) *reinterpret_cast<uint32_t*>(p.scales + scale_at(r, j, p.tiles)) = word;
-  }
+  const int tile = first / (4 * BS);
+  if (at && (lane & (4 * kStep - 1)) == 0 && tile < tiles) *reinterpret_cast<uint32_t*>(at + tile * kFpTileBytes) = word;
+}
+__device__ __forceinline__ uint8_t* scale_row(const QuantArgs& p, int64_t r) {
+  return r < p.padded ? p.scales + scale_at(r, 0, p.tiles) : nullptr;
 }
 
 // `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA at a time.  The next
@@ -64,16 +66,20 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
   const bool in = k < p.K;   // K % 32 == 0: a thread's 16 values are all in or all out
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
   int64_t r = static_cast<int64_t>(blockIdx.x) * per + sub;
-  const T* x = static_cast<const T*>(p.x) + k;
+  const T* x = static_cast<const T*>(p.x) + r * p.x_stride + k;
+  const int64_t x_step = step * p.x_stride;
+  uint8_t* codes = p.codes + r * (p.K >> 1) + (k >> 1);
+  const int64_t codes_step = step * (p.K >> 1);
   Sixteen<T> next;
   next.clear();
-  if (in && r < p.rows) next.load(x + r * p.x_stride);
+  if (in && r < p.rows) next.load(x);
   // every thread of the CTA makes the same turns
   for (int64_t turn = static_cast<int64_t>(blockIdx.x) * per, n = 0; turn < p.padded; turn += step, r += step, ++n) {
     const Sixteen<T> v = next;
     const bool have = in && r < p.rows;
     next.clear();
-    if (in && r + step < p.rows) next.load(x + (r + step) * p.x_stride);
+    x += x_step;
+    if (in && r + step < p.rows) next.load(x);
     uint32_t top = v.top();
     float inv_row = 1.0f;
     bool bad = false;
@@ -84,7 +90,7 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
       if (warps > 1) {
         if (lane == 0) part[n & 1][warp] = most;
         __syncthreads();
-        for (int i = 0; i < warps; ++i) most = max(most, part[n & 1][sub * warps + i]);
+        most = __reduce_max_sync(0xffffffffu, lane < warps ? part[n & 1][sub * warps + lane] : 0u);
       }
       bad = not_finite(most);
       inv_row = pow2(-row_power(most));
@@ -92,8 +98,9 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
     }
     uint32_t c[2] = {0u, 0u}, byte = 0u;
     if (have && !bad) byte = encode16<T, BS>(v, top, inv_row, c);
-    if (have) *reinterpret_cast<uint2*>(p.codes + r * (p.K >> 1) + (k >> 1)) = make_uint2(c[0], c[1]);
-    store_scales<BS>(p, r, k, byte, lane);
+    if (have) *reinterpret_cast<uint2*>(codes) = make_uint2(c[0], c[1]);
+    codes += codes_step;
+    store_scales<BS>(scale_row(p, r), p.tiles, k, byte, lane);
   }
 }
 
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(1024) quantize_fp4_long_kernel(const QuantArgs
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) part[threadIdx.x >> 5] = most;
     __syncthreads();
-    for (int i = 0; i < 32; ++i) most = max(most, part[i]);
+    most = __reduce_max_sync(0xffffffffu, part[lane]);
     bad = not_finite(most);
     inv_row = pow2(-row_power(most));
     if (threadIdx.x == 0 && row_here) p.row[r] = row_scale(most);
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(1024) quantize_fp4_long_kernel(const QuantArgs
     uint32_t c[2] = {0u, 0u}, byte = 0u;
     if (have && !bad) byte = encode16<T, BS>(v, top, inv_row, c);
     if (have) *reinterpret_cast<uint2*>(p.codes + r * (p.K >> 1) + (k >> 1)) = make_uint2(c[0], c[1]);
-    store_scales<BS>(p, r, k, byte, lane);
+    store_scales<BS>(scale_row(p, r), p.tiles, k, byte, lane);
   }
 }
 

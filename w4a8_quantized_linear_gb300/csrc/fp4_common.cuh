@@ -109,6 +109,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Sixteen values as they were loaded.
 template <typename T>
 struct Sixteen {
@@ -138,7 +144,7 @@ struct Sixteen {
       return m;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      for (int i = 0; i < 8; ++i) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
       m = max(m & 0xFFFFu, m >> 16);
       if constexpr (__is_same(T, __nv_bfloat16)) return m << 16;
       return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
@@ -166,20 +172,6 @@ __device__ __forceinline__ uint32_t e2m1x8(const uint64_t* q) {
       : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
   return r;
 }
-// The same through fp16.
-__device__ __forceinline__ uint32_t e2m1x8_f16(const uint64_t* q) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 l, h;\n\t.reg .b32 p;\n\t"
-      "mov.b64 {l, h}, %1;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 a, p;\n\t"
-      "mov.b64 {l, h}, %2;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b, p;\n\t"
-      "mov.b64 {l, h}, %3;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 c, p;\n\t"
-      "mov.b64 {l, h}, %4;\n\tcvt.rn.f16x2.f32 p, h, l;\n\tcvt.rn.satfinite.e2m1x2.f16x2 d, p;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
-  return r;
-}
-
 // The smallest k with a <= m * 2^k for a finite a > 0 given by its bits and m = f 2^w, f given as the
 // bits behind its leading one (a subnormal a counts as the least normal number or less).
 __device__ __forceinline__ int power_for(uint32_t a, uint32_t f_bits, int w) {
@@ -201,12 +193,8 @@ __device__ __forceinline__ float row_scale(uint32_t a) {
 
 // 16 values, their block's maximum (block 32: of both halves) and the inverse of the row's scale (a
 // power of two; 1 for block 32) -> two words of codes, the scale byte.
-//   Block 32 and fp32 rows: the quotient by the block's scale is correctly rounded (by a power of two:
-// exact; else Markstein's correction of a product with the reciprocal, as in div_rn_by).
-//   16-bit rows in blocks of 16: x has 11 bits and b 4, so x / b is one of the seven borders between
-// codes (3 bits) or at least 2^-11 of it away, and more than half a step of fp16.  The product with
-// the rounded reciprocal is off by 2^-23; rounded to fp16 it is the border itself in the one case, and
-// on the right side of it in the other, and a border goes to the even code.
+// Quotients are correctly rounded: by a power of two exact, by b a product with the reciprocal and
+// Markstein's correction (as in div_rn_by).
 template <typename T, int BS>
 __device__ __forceinline__ uint32_t encode16(const Sixteen<T>& v, uint32_t top, float inv_row, uint32_t (&c)[2]) {
   uint64_t q[8];
@@ -221,30 +209,31 @@ __device__ __forceinline__ uint32_t encode16(const Sixteen<T>& v, uint32_t top, 
     c[1] = e2m1x8(q + 4);
     return static_cast<uint32_t>(e + 127);
   } else {
-    const float t = __fdiv_rn(__uint_as_float(top) * inv_row, 6.0f);
+    // a quotient so small that the correction underflows is a scale of 0 either way
+    const float t = div_rn_by(__uint_as_float(top) * inv_row, 6.0f, 1.0f / 6.0f);
     const uint32_t byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
     if (byte == 0u) return 0u;
     const float b = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
     const float r = __frcp_rn(b);
-    if constexpr (sizeof(T) == 4) {
-      const uint64_t inv = both(inv_row), bb = both(-b), rr = both(r);
+    // the quotients' negatives: so a zero keeps its sign through the correction
+    if (inv_row > 0x1p-100f && inv_row < 0x1p100f) {
+      // the row's scale goes into b and its reciprocal: the same quotients in one step less
+      const uint64_t bb = both(b * __uint_as_float(0x7F000000u - __float_as_uint(inv_row))), rr = both(-r * inv_row);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t x = v.pair(i), q0 = mul2(x, rr);
+        q[i] = fma2(fma2(q0, bb, x), rr, q0);
+      }
+    } else {
+      const uint64_t inv = both(inv_row), bb = both(b), rr = both(-r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint64_t x = mul2(v.pair(i), inv), q0 = mul2(x, rr);
         q[i] = fma2(fma2(q0, bb, x), rr, q0);
       }
-      c[0] = e2m1x8(q);
-      c[1] = e2m1x8(q + 4);
-    } else {
-      // both factors at once, unless their product passes what fp32 holds
-      const float s = r * inv_row;
-      const bool one = s < 3.0e38f;
-      const uint64_t f = both(one ? s : r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = mul2(one ? v.pair(i) : mul2(v.pair(i), both(inv_row)), f);
-      c[0] = e2m1x8_f16(q);
-      c[1] = e2m1x8_f16(q + 4);
     }
+    c[0] = e2m1x8(q) ^ 0x88888888u;
+    c[1] = e2m1x8(q + 4) ^ 0x88888888u;
     return byte;
   }
 }
