@@ -464,3 +464,26 @@ def test_quantize_rows_far_from_one(dtype, power):
         assert torch.equal(q[1], ref.tiles(held)) and (row is None or torch.equal(q[2], row))
         assert torch.equal(torch.stack((q[0] & 15, q[0] >> 4), -1).flatten(1).long(), codes)
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=str)
+@pytest.mark.parametrize("m", [1, 7, 16, 40, 128, 129, 515])
+@pytest.mark.parametrize("f", [32, 96, 160, 224, 416, 1056])
+def test_hidden_values_are_quantized_as_by_the_quantizer(m, f, dtype):
+    """Widths that end inside a step of 64, a tile of four blocks and a tile of 128 rows; a hidden value that is not
+    finite, blocks of zeros."""
+    gen = generator(m, f, str(dtype))
+    x = activations(gen, m, 128, dtype)
+    g, u = 0.05 * normal(gen, f, 128), 0.05 * normal(gen, f, 128)
+    u[: min(32, f - 1)] = 0
+    g[f - 1] = 1e6 if dtype == torch.float16 else 1e30   # h passes what the type holds, where x's sum is above zero
+    u[f - 1] = 1e6 if dtype == torch.float16 else 1e30
+    gate, up = cider.cider_quantize_fp4(g), cider.cider_quantize_fp4(u)
+    down = cider.cider_quantize_fp4(normal(gen, 40, f))
+    y = cider.cider_w4a4_feed_forward(x, gate, up, down)
+    h = cider.cider_w4a4_gated_linear(x, gate, up)
+    want = cider.cider_w4a4_linear(h, down)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(y.nan_to_num(), want.nan_to_num())
+    clean()

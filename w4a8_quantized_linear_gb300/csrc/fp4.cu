@@ -33,11 +33,6 @@ struct QuantArgs {
   float* row;
 };
 
-// Where the scale of block j of row r lies.
-__device__ __forceinline__ int64_t scale_at(int64_t r, int j, int tiles) {
-  return ((r >> 7) * tiles + (j >> 2)) * kFpTileBytes + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (j & 3);
-}
-
 // Four neighbouring blocks' bytes, one word of a tile: gathered over the lanes that hold them.  `at`: the
 // row's place in its first tile, or null; `first`: the lane's first value of the row.
 template <int BS>

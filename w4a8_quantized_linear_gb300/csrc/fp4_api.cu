@@ -167,10 +167,12 @@ cider_status_t run(const Call& c) {
       d.y = c.y;
       d.y_bf16 = c.y_dtype == CIDER_BF16;
     }
-    // scratch: x's codes and scales; for a whole block the hidden values, then their codes and scales
+    // scratch: x's codes and scales; for a whole block the hidden values, their codes and scales.  Block
+    // size 32: the first product writes the hidden values quantized.  Block size 16 needs their rows' maxima.
+    const bool straight = c.down && block == 32;
     const Held hx(p.wide_x && !quantizes_itself(p) ? M : 0, K, block),
-        hh(c.down && !quantizes_itself(d) ? M : 0, c.down ? F : 32, block);
-    const size_t wide = c.down ? round256(static_cast<size_t>(M) * F * 2) : 0;
+        hh(c.down && (straight || !quantizes_itself(d)) ? M : 0, c.down ? F : 32, block);
+    const size_t wide = c.down && !straight ? round256(static_cast<size_t>(M) * F * 2) : 0;
     cider::ScratchSource scratch = cider::ScratchSource::pooled(st);
     uint8_t* base = nullptr;
     if (hx.bytes() + wide + hh.bytes() > 0) {
@@ -179,14 +181,21 @@ cider_status_t run(const Call& c) {
       if (s != CIDER_OK) return s;
       base = static_cast<uint8_t*>(ptr);
     }
+    const cider::FpMat hidden = hh.at(base + hx.bytes() + wide, M);
     p.y = c.down ? base + hx.bytes() : c.y;
-    if (F > 0) {
-      const cudaError_t e = product(p, hx.at(base, M));
-      if (e != cudaSuccess || !c.down) return cuda_status(e);
+    if (straight) {
+      p.q_codes = const_cast<uint8_t*>(hidden.codes);
+      p.q_scales = const_cast<uint8_t*>(hidden.scales);
     }
-    d.wide_x = p.y;
-    d.after_launch = true;   // should its kernel quantize the hidden values itself
-    return cuda_status(product(d, hh.at(base + hx.bytes() + wide, M)));
+    const cudaError_t e = product(p, hx.at(base, M));
+    if (e != cudaSuccess || !c.down) return cuda_status(e);
+    // its weights do not depend on the launch before
+    d.after_launch = true;
+    if (straight)
+      d.x = hidden;
+    else
+      d.wide_x = p.y;
+    return cuda_status(product(d, hidden));
   });
 }
 

@@ -191,6 +191,15 @@ __device__ __forceinline__ float row_scale(uint32_t a) {
   return not_finite(a) ? __uint_as_float(0x7FC00000u) : pow2(row_power(a));
 }
 
+// The exponent of the scale of 32 values, from the bits of their finite maximum.
+__device__ __forceinline__ int block_power(uint32_t top) {
+  return top != 0u ? max(power_for(top, 0x400000u, 2), -127) : 0;   // 6 = 1.5 * 2^2
+}
+// Where the scale of block j of row r lies.
+__device__ __forceinline__ int64_t scale_at(int64_t r, int j, int tiles) {
+  return ((r >> 7) * tiles + (j >> 2)) * kFpTileBytes + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (j & 3);
+}
+
 // 16 values, their block's maximum (block 32: of both halves) and the inverse of the row's scale (a
 // power of two; 1 for block 32) -> two words of codes, the scale byte.
 // Quotients are correctly rounded: by a power of two exact, by b a product with the reciprocal and
@@ -201,7 +210,7 @@ __device__ __forceinline__ uint32_t encode16(const Sixteen<T>& v, uint32_t top, 
   c[0] = c[1] = 0u;
   if constexpr (BS == 32) {
     if (not_finite(top)) return 0xFFu;
-    const int e = top != 0u ? max(power_for(top, 0x400000u, 2), -127) : 0;   // 6 = 1.5 * 2^2
+    const int e = block_power(top);
     const uint64_t inv = both(pow2(-e));
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = mul2(v.pair(i), inv);
@@ -268,6 +277,8 @@ struct FpProduct {
   int act = kActSilu;
   void* y = nullptr;
   bool y_bf16 = false;
+  // gated, block 32, N % 32 == 0: the rounded outputs are quantized again, to here in place of y
+  uint8_t *q_codes = nullptr, *q_scales = nullptr;
   bool after_launch = false;   // the launch just before is this call's own: overlap with its end
   int num_sms = 0;
   cudaStream_t st = nullptr;

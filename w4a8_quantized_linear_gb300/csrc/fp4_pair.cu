@@ -15,7 +15,8 @@
 // MMAs' own order.
 //
 // Roles (one CTA per SM, persistent over tiles): warp 0 copies, warp 1 issues
-// (even CTA only), warps 2..5 drain, scale, round, and store by TMA.
+// (even CTA only), warps 2..5 drain, scale, round, and store by TMA (or quantize
+// what they rounded and store codes and scales).
 #include <cuda.h>
 
 #include <atomic>
@@ -49,7 +50,7 @@ struct FCfg {
   static constexpr int kAcc1 = kColX - 256;
   static_assert(kStage % 1024 == 0, "stages must keep 1024-byte alignment for the swizzle");
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(256 - kAcc1 <= 64, "the shared columns are among the first 64 outputs that are drained");
+  static_assert(256 - kAcc1 <= 64, "the shared columns are among those that are drained first");
 };
 
 struct FPairArgs {
@@ -58,8 +59,40 @@ struct FPairArgs {
   int nkb, nsteps;
   const float *sx, *sw, *su;
   int y_bf16, act;
+  uint8_t *q_codes, *q_scales;   // or null
+  int q_tiles;                   // tiles of scales along the outputs
   int* err;
 };
+
+// 32 rounded outputs from n on of token m, as a block of the quantized matrix.
+template <typename T>
+__device__ __forceinline__ uint32_t encode_block(const uint32_t* h, uint32_t (&c)[4]) {
+  Sixteen<T> a, b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a.w[i] = h[i];
+    b.w[i] = h[8 + i];
+  }
+  const uint32_t top = max(a.top(), b.top());
+  uint32_t lo[2], hi[2];
+  const uint32_t byte = encode16<T, 32>(a, top, 1.0f, lo);
+  encode16<T, 32>(b, top, 1.0f, hi);
+  c[0] = lo[0];
+  c[1] = lo[1];
+  c[2] = hi[0];
+  c[3] = hi[1];
+  return byte;
+}
+__device__ __forceinline__ void store_block(const FPairArgs& p, int m, int n, const uint32_t* h) {
+  uint32_t c[4];
+  const uint32_t byte = p.y_bf16 ? encode_block<__nv_bfloat16>(h, c) : encode_block<__half>(h, c);
+  *reinterpret_cast<uint4*>(p.q_codes + static_cast<int64_t>(m) * (p.N >> 1) + (n >> 1)) =
+      make_uint4(c[0], c[1], c[2], c[3]);
+  uint8_t* at = p.q_scales + scale_at(m, n >> 5, p.q_tiles);
+  *at = static_cast<uint8_t>(byte);
+  // the other block of a step of 64 that the row ends in
+  if (n + 32 == p.N && (p.N & 32) != 0) at[1] = 0;
+}
 
 template <bool GATED, int BS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
@@ -107,7 +140,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  pdl_wait();   // codes and scales of x come from the launch just before
   constexpr uint32_t tmem = 0;   // the CTA holds all columns
 
   if (warp == 0) {
@@ -116,6 +148,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     int s = 0, it = 0;
     uint32_t phase = 1;
     bool go = true;
+    auto weights = [&](int nt, int kb, int slot) {
+      if (rank == 0) mbar_arrive_expect_tx(full_bar(slot), 2 * C::kStage);
+      const uint32_t at = base + slot * C::kStage, bar = full0 + 8u * slot;
+      const int sk = kb * (B::kBytes / 8);
+      if (GATED) {
+        if (rank == 0)
+          tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 128);
+        else
+          tma_load_2d_pair(at + kFOperand, &tm_u, bar, kb * 128, nt * 128);
+        tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt);
+        tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_su, bar, sk, nt);
+      } else {
+        tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
+        tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt * 2);
+        tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, nt * 2 + 1);
+      }
+    };
+    auto tokens = [&](int mt, int kb, int slot) {
+      const uint32_t at = base + slot * C::kStage, bar = full0 + 8u * slot;
+      tma_load_2d_pair(at, &tm_x, bar, kb * 128, mt * 256 + rank * 128);
+      tma_load_2d_pair(at + C::kSfx, &tm_sx, bar, kb * (B::kBytes / 8), mt * 2 + rank);
+    };
+    // the first tile's first weights do not depend on the launch before, which makes x
+    const int ahead = min(S, p.nkb);
+    if (elect_one())
+      for (int kb = 0; kb < ahead; ++kb) weights(cid / p.m_tiles, kb, kb);
+    pdl_wait();
     for (int tile = cid; tile < p.tiles && go; tile += pairs) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
       for (int kb = 0; kb < p.nkb; ++kb, ++it) {
@@ -124,26 +183,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
           break;
         }
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kStage);
-          const uint32_t at = base + s * C::kStage, bar = full0 + 8u * s;
-          const int sk = kb * (B::kBytes / 8);
-          tma_load_2d_pair(at, &tm_x, bar, kb * 128, mt * 256 + rank * 128);
-          if (GATED) {
-            if (rank == 0)
-              tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 128);
-            else
-              tma_load_2d_pair(at + kFOperand, &tm_u, bar, kb * 128, nt * 128);
-          } else {
-            tma_load_2d_pair(at + kFOperand, &tm_w, bar, kb * 128, nt * 256 + rank * 128);
-          }
-          tma_load_2d_pair(at + C::kSfx, &tm_sx, bar, sk, mt * 2 + rank);
-          if (GATED) {
-            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt);
-            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_su, bar, sk, nt);
-          } else {
-            tma_load_2d_pair(at + C::kSfw, &tm_sw, bar, sk, nt * 2);
-            tma_load_2d_pair(at + C::kSfw + B::kBytes, &tm_sw, bar, sk, nt * 2 + 1);
-          }
+          if (it >= ahead) weights(nt, kb, s);
+          tokens(mt, kb, s);
         }
         __syncwarp();
         if (++s == S) {
@@ -216,8 +257,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t acce0 = mapa_shared(acce_bar, 0);
     float* scale = reinterpret_cast<float*>(gbase + C::kRowScale);
-    constexpr int kCols = GATED ? 128 : 256, kTurns = kCols / 64;   // outputs of a token in a tile
+    constexpr int kCols = GATED ? 128 : 256;   // outputs of a token in a tile
     int n = 0;
+    pdl_wait();   // row scales of x come from the launch before
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
       const int m0 = mt * 256 + static_cast<int>(rank) * 128, m = m0 + row, n0 = nt * kCols;
@@ -239,8 +281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
       // 64 outputs a turn, first those whose columns the next tile's accumulator shares: the last ones
       // of the first accumulator, the first ones of the second
 #pragma unroll 1
-      for (int i = 0; i < kTurns; ++i) {
-        const int c = 64 * ((n & 1) ? i : kTurns - 1 - i);
+      for (int i = 0; i < kCols / 64; ++i) {
+        const int c = 64 * ((n & 1) ? i : kCols / 64 - 1 - i);
         uint32_t v[64], u[GATED ? 64 : 1];
         tmem_ld32(d + c, *reinterpret_cast<uint32_t(*)[32]>(v));
         tmem_ld32(d + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
@@ -265,6 +307,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             b = gated(b, __uint_as_float(u[2 * j + 1]) * sx * t.y, p.act);
           }
           h[j] = p.y_bf16 ? y_bits2<true>(a, b) : y_bits2<false>(a, b);
+        }
+        if constexpr (GATED && BS == 32) {
+          if (p.q_codes) {
+            // a thread's outputs are two blocks of the quantized matrix
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (m < p.M && n0 + c + 32 * k < p.N) store_block(p, m, n0 + c + 32 * k, h + 16 * k);
+            continue;
+          }
         }
         // the last turn's store has read the buffer
         if (lane == 0) bulk_wait_group_read<0>();
@@ -325,6 +376,9 @@ cudaError_t launch(const FpProduct& p) {
   a.su = p.up.row;
   a.y_bf16 = p.y_bf16;
   a.act = p.act;
+  a.q_codes = p.q_codes;
+  a.q_scales = p.q_scales;
+  a.q_tiles = fp4_tiles(p.N, 32);
   e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
   CUtensorMap mx, mw, mu, msx, msw, msu, my;
@@ -339,7 +393,10 @@ cudaError_t launch(const FpProduct& p) {
   };
   const FpMat& up = GATED ? p.up : p.w;
   if (!codes(&mx, p.x) || !codes(&mw, p.w) || !codes(&mu, up) || !scales(&msx, p.x) || !scales(&msw, p.w) ||
-      !scales(&msu, up) ||
+      !scales(&msu, up))
+    return cudaErrorInvalidValue;
+  my = mx;
+  if (!p.q_codes &&
       !make_tensor_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.y, p.N, p.M, p.N * 2, 64, 32,
                           CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;

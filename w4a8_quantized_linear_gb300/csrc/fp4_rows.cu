@@ -57,6 +57,8 @@ struct RowsArgs {
   int x_bf16;
   void* y;
   int y_bf16, act;
+  uint8_t *q_codes, *q_scales;      // or null
+  int q_tiles;                      // tiles of scales along the outputs
   int* err;
 };
 
@@ -347,9 +349,8 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
   }
   if (ok) {
     // four weight rows of a token at a time; the cluster's CTAs take equal shares
-    const int units = mv * 32;
-    const int u0 = static_cast<int>(static_cast<int64_t>(rank) * units / p.splits);
-    const int u1 = static_cast<int>(static_cast<int64_t>(rank + 1) * units / p.splits);
+    // in blocks of 32 outputs (eight threads)
+    const int u0 = 8 * (rank * mv * 4 / p.splits), u1 = 8 * ((rank + 1) * mv * 4 / p.splits);
     for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += kThreads) {
       const int t = u >> 5, n = nt * 128 + 4 * (u & 31);
       if (n >= p.N) continue;   // N % 8 == 0: four rows are all in or all out
@@ -389,6 +390,40 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
         w = make_uint2(y_bits2<true>(out[0], out[1]), y_bits2<true>(out[2], out[3]));
       } else {
         w = make_uint2(y_bits2<false>(out[0], out[1]), y_bits2<false>(out[2], out[3]));
+      }
+      if (GATED && BS == 32 && p.q_codes) {
+        // eight neighbouring threads hold a block of the quantized matrix
+        const int64_t m = m0 + t;
+        const uint32_t group = 0xFFu << (lane & 24);
+        uint32_t top = max(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu) & 0xFFFFu,
+                           max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu) >> 16);
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(group, top, o));
+        float f[4];
+        if (p.y_bf16) {
+          top <<= 16;
+          f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xFFFF0000u);
+          f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+        } else {
+          top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+          const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x)),
+                       a1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+          f[0] = a0.x, f[1] = a0.y, f[2] = a1.x, f[3] = a1.y;
+        }
+        const bool bad = not_finite(top);
+        const int e = bad ? 0 : block_power(top);
+        const float inv = bad ? 0.0f : pow2(-e);
+        const uint64_t qp[4] = {pack2(__float_as_uint(f[0] * inv), __float_as_uint(f[1] * inv)),
+                                pack2(__float_as_uint(f[2] * inv), __float_as_uint(f[3] * inv)), 0ull, 0ull};
+        *reinterpret_cast<uint16_t*>(p.q_codes + m * (p.N >> 1) + (n >> 1)) =
+            bad ? uint16_t{0} : static_cast<uint16_t>(e2m1x8(qp));
+        if ((lane & 7) == 0) {
+          uint8_t* at = p.q_scales + scale_at(m, n >> 5, p.q_tiles);
+          *at = bad ? uint8_t{0xFF} : static_cast<uint8_t>(e + 127);
+          // the other block of a step of 64 that the row ends in
+          if (n + 32 == p.N && (p.N & 32) != 0) at[1] = 0;
+        }
+        continue;
       }
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + static_cast<int64_t>(m0 + t) * p.N + n) = w;
     }
@@ -502,6 +537,9 @@ bool plan(const FpProduct& p, bool fuse, RowsArgs& a, int* smem_out, int* tiles_
   a.y = p.y;
   a.y_bf16 = p.y_bf16;
   a.act = p.act;
+  a.q_codes = p.q_codes;
+  a.q_scales = p.q_scales;
+  a.q_tiles = fp4_tiles(p.N, 32);
   *smem_out = smem;
   *tiles_out = tiles;
   return true;
