@@ -224,13 +224,13 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// 16 bytes of shared memory anywhere in the cluster.
+// 16 bytes of shared memory anywhere in the cluster.  It stays behind the barrier that made them
+// visible (both are volatile); nothing else need wait for it.
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
   float4 f;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-               : "r"(cluster_addr)
-               : "memory");
+               : "r"(cluster_addr));
   return f;
 }
 // Arrive on an mbarrier anywhere in the cluster (address from mapa_shared),

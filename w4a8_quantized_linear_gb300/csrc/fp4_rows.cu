@@ -33,6 +33,7 @@ constexpr int kRBars = 2 * kRMaxStages + 2;
 constexpr int kRTail = kRBars * 8 + 16 + 2 * 16 * 4;   // barriers, flags, the fused rows' maxima and scales
 constexpr int kRTokens = 16;                           // of the fused form
 constexpr int kRQuantWarps = 8;
+constexpr int kRThreads = 64 + 32 * kRQuantWarps;
 constexpr int kRBatch = 4;
 constexpr int kRMaxFusedStages = 16;                   // of a CTA's part of K, held whole
 
@@ -147,11 +148,11 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
 }
 
 template <bool GATED, int BS, bool FUSE>
-__global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
+__global__ void __launch_bounds__(kRThreads, 2)
     fp4_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_u,
                     const __grid_constant__ CUtensorMap tm_x, const RowsArgs p) {
   using B = FpBlock<BS>;
-  constexpr int kThreads = FUSE ? 64 + 32 * kRQuantWarps : 192;
+  constexpr int kThreads = kRThreads;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -357,27 +358,32 @@ __global__ void __launch_bounds__(FUSE ? 64 + 32 * kRQuantWarps : 192, 2)
       float a[GATED ? 8 : 4];
 #pragma unroll
       for (int i = 0; i < (GATED ? 8 : 4); ++i) a[i] = 0.0f;
-      // all ranks' partial sums are asked for before the first is added
-      float4 f[8][GATED ? 2 : 1];
+      // the partial sums of several ranks are asked for before the first is added
+      constexpr int kAsk = GATED ? 4 : 8;
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < p.splits) {
+      for (int r0 = 0; r0 < 8; r0 += kAsk) {
+        if (r0 >= p.splits) break;
+        float4 f[kAsk][GATED ? 2 : 1];
 #pragma unroll
-          for (int h = 0; h < (GATED ? 2 : 1); ++h)
-            f[r][h] = ld_cluster_v4(mapa_shared(
-                base + static_cast<uint32_t>(((h * p.tn + t) * 128 + 4 * (u & 31)) * 4), p.splits > 1 ? r : 0));
-        }
+        for (int r = 0; r < kAsk; ++r)
+          if (r0 + r < p.splits) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < p.splits) {
-#pragma unroll
-          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            a[4 * h] += f[r][h].x;
-            a[4 * h + 1] += f[r][h].y;
-            a[4 * h + 2] += f[r][h].z;
-            a[4 * h + 3] += f[r][h].w;
+            for (int h = 0; h < (GATED ? 2 : 1); ++h)
+              f[r][h] = ld_cluster_v4(mapa_shared(
+                  base + static_cast<uint32_t>(((h * p.tn + t) * 128 + 4 * (u & 31)) * 4), p.splits > 1 ? r0 + r : 0));
           }
-        }
+#pragma unroll
+        for (int r = 0; r < kAsk; ++r)
+          if (r0 + r < p.splits) {
+#pragma unroll
+            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+              a[4 * h] += f[r][h].x;
+              a[4 * h + 1] += f[r][h].y;
+              a[4 * h + 2] += f[r][h].z;
+              a[4 * h + 3] += f[r][h].w;
+            }
+          }
+      }
       const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? __ldg(p.sx + m0 + t) : 1.0f;
       float out[4];
 #pragma unroll
@@ -449,7 +455,7 @@ cudaError_t launch(const FpProduct& p, RowsArgs& a, int smem, int tiles) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
-  cfg.blockDim = dim3(FUSE ? 64 + 32 * kRQuantWarps : 192, 1, 1);
+  cfg.blockDim = dim3(kRThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = p.st;
   cudaLaunchAttribute attr[2];
@@ -496,14 +502,18 @@ bool plan(const FpProduct& p, bool fuse, RowsArgs& a, int* smem_out, int* tiles_
   // or two on each SM): one token through 4096 x 4096, 32 tiles in 4 parts 5.7 us, in 8 parts 7.4; 16
   // through 2560 x 10240, 20 tiles in 8 parts 10.6, in 4 parts 11.8; 128 through 10240 x 2560, 80 tiles
   // in 2 parts 12.9, whole 14.3.  Other numbers of parts lose 5 us to the placing of their clusters.
-  // Where there are more CTAs than SMs they share SMs in pairs: they hold at most half of the tensor
+  // Where there are more CTAs than that they share SMs in pairs: they hold at most half of the tensor
   // memory, and their shared memory allows two and no third.  All others have an SM to themselves.  So
   // no CTA of a cluster waits for tensor memory that another cluster's holds.
   const int tiles = a.m_tiles * static_cast<int>((p.N + 127) / 128);
-  const int room = a.tmem_cols <= 256 ? p.num_sms + p.num_sms / 16 : p.num_sms;
+  // Clusters of 4 and of 8 do not reach every SM (144 and 120 of 152 with a CTA on each).
+  const bool small = a.tmem_cols <= 256;
+  auto reach = [&](int splits) { return splits == 8 ? p.num_sms * 3 / 4 : splits == 4 ? p.num_sms * 15 / 16 : p.num_sms; };
   a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= room && a.nkb >= a.splits * 4) a.splits *= 2;
-  const bool two = a.tmem_cols <= 256 && tiles * a.splits > p.num_sms;
+  while (a.splits < 8 && a.nkb >= a.splits * 4 &&
+         tiles * a.splits * 2 <= (small ? p.num_sms + p.num_sms / 16 : reach(a.splits * 2)))
+    a.splits *= 2;
+  const bool two = small && tiles * a.splits > reach(a.splits);
   const int budget = two ? 110 * 1024 : 224 * 1024;
   const int mine = (a.nkb + a.splits - 1) / a.splits;   // stages of a CTA, at most
   int held = 0;
