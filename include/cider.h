@@ -406,7 +406,9 @@ cider_status_t cider_verify_drafts(const void* logits, int64_t logits_stride, in
  *              (r / 128, j / 4).  Bytes of blocks behind the last one are zero;
  *              bytes of rows behind the last one reach no output
  *   row_scale  fp32 [rows], or NULL: 1.  A factor of the row's values
- * cols is a multiple of 32, at most 131072.
+ * cols is a multiple of 32, at most 131072.  E4M3 bytes have no sign; a product of
+ * two blocks' scales has to be within fp32's range.
+ * Outputs do not overlap inputs, but y or h may lie on a 16-bit x.
  *
  * Checks on the host, in this order: no rows or outputs returns CIDER_OK; null
  * pointers, sizes, strides, types that do not fit each other give
@@ -449,7 +451,9 @@ cider_status_t cider_dequantize_fp4(const cider_fp4_t* q, void* x, int x_dtype, 
  *      (as for cider_quantize_fp4);  w  [N, K], N % 8 == 0;  y  [M, N] of y_dtype
  * Products of codes and block scales are summed in fp32 in the tensor cores, the
  * sum is multiplied by x's row scale and then w's, and rounded once to y_dtype.
- * The same call gives the same bits. */
+ * The same call gives the same bits, and so does cider_w4a4_linear_prequant of rows
+ * that cider_quantize_fp4 quantized.  Scratch comes from the library's pool; the
+ * call is not one that cider_timing_begin counts. */
 cider_status_t cider_w4a4_linear(const void* x, int x_dtype, int64_t x_stride, int64_t M,
                                  const cider_fp4_t* w, void* y, int y_dtype, void* stream);
 

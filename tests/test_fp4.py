@@ -487,3 +487,44 @@ def test_hidden_values_are_quantized_as_by_the_quantizer(m, f, dtype):
     assert torch.equal(torch.isnan(y), torch.isnan(want))
     assert torch.equal(y.nan_to_num(), want.nan_to_num())
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("m", [1, 16, 50, 128, 300])
+def test_output_on_the_input(m, block):
+    gen = generator(m, block)
+    w, u = (cider.cider_quantize_fp4(0.05 * normal(gen, 2560, 2560), block) for _ in range(2))
+    for call in (lambda x, **kw: cider.cider_w4a4_linear(x, w, block, **kw),
+                 lambda x, **kw: cider.cider_w4a4_gated_linear(x, w, u, block, **kw),
+                 lambda x, **kw: cider.cider_w4a4_feed_forward(x, w, u, w, block, **kw)):
+        x = activations(gen, m, 2560, torch.bfloat16)
+        want = call(x)
+        for _ in range(3):
+            z = x.clone()
+            assert call(z, out=z) is z and torch.equal(z, want)
+    clean()
+
+
+@gpu
+def test_calls_on_three_streams_at_once():
+    """Kernels of every form beside each other: clusters that share SMs, pairs, quantization."""
+    gen = generator(3)
+    k, f = 1024, 2048
+    gate, up = (cider.cider_quantize_fp4(0.03 * normal(gen, f, k), 16) for _ in range(2))
+    down = cider.cider_quantize_fp4(0.03 * normal(gen, k, f), 16)
+    sizes = (1, 16, 33, 100, 200, 600)
+    xs = [activations(gen, m, k, torch.float16) for m in sizes]
+    call = lambda x: cider.cider_w4a4_feed_forward(x, gate, up, down, 16)
+    want = [call(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                n = (i * 5 + j * 2) % len(xs)
+                got.append((n, call(xs[n])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[n]) for n, y in got)
+    clean()

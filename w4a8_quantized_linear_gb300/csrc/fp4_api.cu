@@ -72,13 +72,17 @@ bool few_rows(const cider::FpProduct& p) {
 }
 
 // Few enough that the product's kernel quantizes the rows itself, each CTA its part of K: one launch
-// instead of two.
-bool quantizes_itself(const cider::FpProduct& p) { return few_rows(p) && cider::fp4_rows_quantizes_itself(p); }
+// instead of two.  Not where y lies on x: CTAs that are done would write what others still read.
+bool quantizes_itself(const cider::FpProduct& p, const void* x, const void* y) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t xn = 2 * ((p.M - 1) * p.x_stride + p.K), yn = 2 * p.M * p.N;
+  return few_rows(p) && !(x0 < y0 + yn && y0 < x0 + xn) && cider::fp4_rows_quantizes_itself(p);
+}
 
 // A product of x in 16 bits: quantized into `held` (scratch) first, or by the product's kernel.
 cudaError_t product(cider::FpProduct& p, const cider::FpMat& held) {
   if (p.wide_x) {
-    if (quantizes_itself(p)) return cider::launch_fp4_rows(p);
+    if (quantizes_itself(p, p.wide_x, p.y)) return cider::launch_fp4_rows(p);
     const cudaError_t e = cider::launch_quantize_fp4(
         p.wide_x, p.x_bf16 ? CIDER_BF16 : CIDER_F16, p.x_stride, p.M, p.K, p.block, const_cast<uint8_t*>(held.codes),
         const_cast<uint8_t*>(held.scales), const_cast<float*>(held.row), false, p.num_sms, p.st, true);
@@ -176,8 +180,9 @@ cider_status_t run(const Call& c) {
     // scratch: x's codes and scales; for a whole block the hidden values, their codes and scales.  Block
     // size 32: the first product writes the hidden values quantized.  Block size 16 needs their rows' maxima.
     const bool straight = c.down && block == 32;
-    const Held hx(p.wide_x && !quantizes_itself(p) ? M : 0, K, block),
-        hh(c.down && (straight || !quantizes_itself(d)) ? M : 0, c.down ? F : 32, block);
+    // (Scratch is not the caller's: neither h lies on x nor y on h.)
+    const Held hx(p.wide_x && !quantizes_itself(p, c.x, c.down ? nullptr : c.y) ? M : 0, K, block),
+        hh(c.down && (straight || !quantizes_itself(d, nullptr, c.y)) ? M : 0, c.down ? F : 32, block);
     const size_t wide = c.down && !straight ? round256(static_cast<size_t>(M) * F * 2) : 0;
     cider::ScratchSource scratch = cider::ScratchSource::pooled(st);
     uint8_t* base = nullptr;
