@@ -210,9 +210,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
       bool go = true;
       for (int tile = cid; tile < p.tiles && go; tile += pairs, ++n) {
         const uint32_t d = tmem + ((n & 1) ? C::kAcc1 : 0);
-        // the tile before has given up the columns that its accumulator shares with this one's (and,
-        // earlier, everything of the tile before that)
-        if (n > 0 && !mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)) break;
         // a stage: its scales, then `steps` MMAs
         auto stage = [&](auto full, int steps, bool first) {
           if (!mbar_wait_bounded(full_bar(s), phase, abort_flag, p.err, kFpWaitNs)) {
@@ -227,6 +224,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
             tc_cp_scales<2>(tmem + C::kColX + 4 * a, dx + a * (kFpTileBytes >> 4));
             tc_cp_scales<2>(tmem + C::kColW + 8 * a, dw + a * (kFpTileBytes >> 4));
             tc_cp_scales<2>(tmem + C::kColW + 8 * a + 4, dw + ((B::kBytes + a * kFpTileBytes) >> 4));
+          }
+          // the tile before has given up the columns that its accumulator shares with this one's (and,
+          // earlier, everything of the tile before that)
+          if (first && n > 0) {
+            if (!mbar_wait_bounded(acce_bar, (n - 1) & 1, abort_flag, p.err, kFpWaitNs)) {
+              go = false;
+              return;
+            }
+            tc_fence_after();
           }
           const uint64_t ad = smem_desc_k_sw128(at), bd = smem_desc_k_sw128(at + kFOperand);
 #pragma unroll
