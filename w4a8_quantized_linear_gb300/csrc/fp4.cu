@@ -48,8 +48,8 @@ __device__ __forceinline__ uint8_t* scale_row(const QuantArgs& p, int64_t r) {
   return r < p.padded ? p.scales + scale_at(r, 0, p.tiles) : nullptr;
 }
 
-// `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA at a time.  The next
-// rows' values are on their way while these are encoded.
+// `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA at a time.  (The next
+// rows' values asked for before these are encoded: 8.3 us for 7.4, in registers that other CTAs use better.)
 template <typename T, int BS>
 __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) {
   __shared__ uint32_t part[2][32];
@@ -65,16 +65,15 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
   const int64_t x_step = step * p.x_stride;
   uint8_t* codes = p.codes + r * (p.K >> 1) + (k >> 1);
   const int64_t codes_step = step * (p.K >> 1);
-  Sixteen<T> next;
-  next.clear();
-  if (in && r < p.rows) next.load(x);
   // every thread of the CTA makes the same turns
   for (int64_t turn = static_cast<int64_t>(blockIdx.x) * per, n = 0; turn < p.padded; turn += step, r += step, ++n) {
-    const Sixteen<T> v = next;
     const bool have = in && r < p.rows;
-    next.clear();
+    Sixteen<T> v;
+    if (have)
+      v.load(x);
+    else
+      v.clear();
     x += x_step;
-    if (in && r + step < p.rows) next.load(x);
     uint32_t top = v.top();
     float inv_row = 1.0f;
     bool bad = false;
@@ -151,9 +150,9 @@ cudaError_t launch_quantize(const QuantArgs& p, int num_sms, cudaStream_t st, bo
   }
   const int warps = (p.K + 511) / 512;
   const int per = warps >= 8 ? 1 : 8 / warps, threads = 32 * warps * per;
-  // about as many CTAs as run at once, so that rows follow each other in a CTA.  4096 x 4096 bf16: 8.5 us
-  // with 1280 threads an SM, 9.0 with 2048, 10.1 with a CTA a row; 10240 x 2560 fp32: 24.8, 21.8 and 27.0
-  const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * ((sizeof(T) == 4 ? 2048 : 1280) / threads);
+  // As many CTAs as run at once (their registers, 50 a thread, hold 1280 threads an SM).  4096 x 4096 bf16,
+  // block 32: 8.0 us, a CTA a row 10.1; 10240 x 2560 fp32 19.6, 27.0; equal rows in fewer CTAs 8.7 and 20.9.
+  const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * (1280 / threads);
   quantize_fp4_kernel<T, BS><<<static_cast<unsigned>(groups < most ? groups : most), threads, 0, st>>>(p, warps, release);
   return cudaGetLastError();
 }
