@@ -528,3 +528,42 @@ def test_calls_on_three_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[n]) for n, y in got)
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+def test_rows_whose_offsets_pass_32_bits(block):
+    """Rows of x 2^31 elements apart, matrices of more than 2^32 elements, outputs of more than 2^31."""
+    gen = generator(block)
+    far = torch.empty((2 << 31) + 4096, dtype=torch.float16, device="cuda")
+    w = cider.cider_quantize_fp4(0.05 * normal(gen, 24, 288), block)
+    x = far.as_strided((3, 288), (1 << 31, 1))
+    x.copy_(activations(gen, 3, 288, torch.float16))
+    near = x.contiguous()
+    a, b = cider.cider_quantize_fp4(x, block), cider.cider_quantize_fp4(near, block)
+    assert all(s is t or torch.equal(s, t) for s, t in zip(a, b))
+    assert torch.equal(cider.cider_w4a4_linear(x, w, block), cider.cider_w4a4_linear(near, w, block))
+    del far, x
+    rows, cols = 33000, 131072
+    big = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    big[-130:] = normal(gen, 130, cols).bfloat16()
+    q = cider.cider_quantize_fp4(big, block)
+    tail = big[-130:].clone()
+    codes, held, row = ref.quantize(tail, block)
+    assert torch.equal(torch.stack((q[0][-130:] & 15, q[0][-130:] >> 4), -1).flatten(1).long(), codes)
+    assert row is None or torch.equal(q[2][-130:], row)
+    back = cider.cider_dequantize_fp4(q, block, torch.bfloat16, out=big)
+    mine = ref.matrix(tail, block)
+    assert torch.equal(back[-130:].double(), ref.values(mine, block))
+    # the weights' last rows, through both kernels
+    for m in (2, 200):
+        x = activations(gen, m, cols, torch.bfloat16)
+        y = cider.cider_w4a4_linear(x, q, block)
+        v, u = ref.values(ref.matrix(x, block), block), ref.values(mine, block)
+        close(y[:, -130:], v @ u.T, ref.sum_bound(v, u) + ref.half_step(torch.bfloat16, v @ u.T) * (1 + 2.0 ** -10))
+    del big, back, q
+    x, w = activations(gen, 70000, 64, torch.float16), cider.cider_quantize_fp4(normal(gen, 32768, 64), block)
+    y = cider.cider_w4a4_linear(x, w, block)
+    assert y.numel() > 1 << 31
+    assert torch.equal(y[-300:], cider.cider_w4a4_linear(x[-300:], w, block))
+    clean()
