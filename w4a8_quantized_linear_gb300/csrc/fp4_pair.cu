@@ -6,7 +6,11 @@
 // of the tile (A) and weight rows [128 r, ..) (half of B), each CTA's tensor
 // memory its own 128 tokens x all 256 weight rows.  At 4 bits an MMA reads its
 // operands from shared memory as fast as it multiplies only when a pair shares
-// them: 8 KB per SM in the 64 cycles of 128 x 256 x 64 products.  Gated, the
+// them: 8 KB per SM in the 128 cycles of 128 x 256 x 64 products, where an SM
+// alone would take in 12.  The accumulators of two tiles share 24 or 48 columns,
+// because the scales need some too; the next tile starts once these are drained,
+// ~800 cycles behind the last one's end.  (Tiles of 192 weight rows, with nothing
+// shared, cost more in all: the issue of their MMAs is as long.)  Gated, the
 // even CTA's half of B is 128 rows of w, the odd one's the same rows of `up`:
 // columns j and 128 + j of an accumulator are the two sides of one output.
 //
@@ -265,6 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     float* scale = reinterpret_cast<float*>(gbase + C::kRowScale);
     constexpr int kCols = GATED ? 128 : 256;   // outputs of a token in a tile
     int n = 0;
+    bool ok = true;
     pdl_wait();   // row scales of x come from the launch before
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
@@ -278,10 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
         const int c = n0 + e + (GATED ? 0 : 128 * h);
         w[128 * h + e] = src && c < p.N ? __ldg(src + c) : 1.0f;
       }
-      named_barrier_sync(1, 128);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(accf_bar0 + 8u * (n & 1), (n >> 1) & 1, abort_flag, p.err,
-                                                     kFpWaitNs)))
-        break;
+      // warps whose waits gave up and warps whose did not leave together
+      if (!named_barrier_and(1, 128, ok)) break;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded(accf_bar0 + 8u * (n & 1), (n >> 1) & 1, abort_flag, p.err, kFpWaitNs));
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t d = tmem + lane_base + ((n & 1) ? C::kAcc1 : 0);
       // 64 outputs a turn, first those whose columns the next tile's accumulator shares: the last ones
