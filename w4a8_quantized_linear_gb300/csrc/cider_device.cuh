@@ -492,6 +492,13 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   return v;
 }
 
+// A load that stays behind pdl_wait(): what __ldg reads is taken to be constant for the whole kernel.
+__device__ __forceinline__ float ld_global_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- outputs
 // 32 bytes to a 32-byte boundary of global memory.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {

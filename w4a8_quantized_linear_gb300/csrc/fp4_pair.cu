@@ -274,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     for (int tile = cid; tile < p.tiles; tile += pairs, ++n) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
       const int m0 = mt * 256 + static_cast<int>(rank) * 128, m = m0 + row, n0 = nt * kCols;
-      const float sx = p.sx && m < p.M ? __ldg(p.sx + m) : 1.0f;
+      const float sx = p.sx && m < p.M ? ld_global_f32(p.sx + m) : 1.0f;
       float* w = scale + (n & 1) * 256;
       // weight rows' scales of the tile, in the order of the accumulator's columns
 #pragma unroll

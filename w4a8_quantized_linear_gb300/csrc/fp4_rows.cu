@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
             }
           }
       }
-      const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? __ldg(p.sx + m0 + t) : 1.0f;
+      const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? ld_global_f32(p.sx + m0 + t) : 1.0f;
       float out[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
