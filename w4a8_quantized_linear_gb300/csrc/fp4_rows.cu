@@ -65,10 +65,11 @@ struct RowsArgs {
 
 // The part of the rows of x that this CTA multiplies, quantized into shared memory.  A thread asks for
 // four units of 16 values before it works on the first; block size 16, which needs the rows' maxima,
-// keeps all of x in registers until it has them.
-template <typename T, int BS>
+// keeps all of x in registers until it has them.  `meet` is called when the first values are on their way:
+// shared memory is not used before it.
+template <typename T, int BS, typename F>
 __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes, uint8_t* scales, uint32_t* most,
-                                              float* row, int kb0, int kb1, int thread) {
+                                              float* row, int kb0, int kb1, int thread, F&& meet) {
   constexpr int kThreads = 32 * kRQuantWarps, kBatch = kRBatch;
   const T* x = static_cast<const T*>(p.x);
   const int k0 = kb0 * kFpStageK;
@@ -94,6 +95,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
       v[j].clear();
       if (u < units) v[j].load(x + r * p.x_stride + (u - r * per) * 16);
     }
+    meet();
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (j * kThreads >= units) break;
@@ -134,6 +136,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
         v[j].clear();
         if (u < units && k < p.K) v[j].load(x + r * p.x_stride + k);
       }
+      if (u0 == 0) meet();
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int u = u0 + j * kThreads + thread, r = __umulhi(u, magic), k = k0 + 16 * (u - r * per);
@@ -205,15 +208,30 @@ __global__ void __launch_bounds__(kRThreads, 2)
     if (elect_one())
       for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
     __syncwarp();
-  } else {
-    if (FUSE && threadIdx.x >= 64 && threadIdx.x < 64 + kRTokens) most[threadIdx.x - 64] = 0u;
-    if (warp == 1) {
-      tmem_alloc(tmem_slot, p.tmem_cols);
-      tmem_relinquish();
-    }
+  } else if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  // barriers initialised, tensor memory held
+  auto meet = [&] {
     tc_fence_before();
     named_barrier_sync(2, kThreads);
     tc_fence_after();
+  };
+  if (FUSE && warp >= 2) {
+    // ------------------------------------------------------------ quantization of x
+    const int thread = threadIdx.x - 64;
+    if (thread < kRTokens) most[thread] = 0u;
+    pdl_wait();   // x may be what the launch just before wrote
+    if (p.x_bf16)
+      quantize_part<__nv_bfloat16, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, thread, meet);
+    else
+      quantize_part<__half, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, thread, meet);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x_bar);
+  } else if (warp >= 1) {
+    meet();
   }
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + p.tail + 8 * kRBars);
   const int acc_cols = GATED ? 2 * p.tn : p.tn;
@@ -300,16 +318,6 @@ __global__ void __launch_bounds__(kRThreads, 2)
       tc_commit(acc_bar);
     }
     __syncwarp();
-  } else if (FUSE) {
-    // ------------------------------------------------------------ quantization of x
-    pdl_wait();   // x may be what the launch just before wrote
-    if (p.x_bf16)
-      quantize_part<__nv_bfloat16, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
-    else
-      quantize_part<__half, BS>(p, gbase + p.x_offset, gbase + p.xs_offset, most, row, kb0, kb1, threadIdx.x - 64);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x_bar);
   }
   // ---------------------------------------------------------------- sums
   // Every MMA that was issued has run (also after a wait that gave up); then the ring is free and
