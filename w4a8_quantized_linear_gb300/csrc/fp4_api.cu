@@ -63,10 +63,10 @@ struct Held {
 };
 
 // Few tokens: weights by 128 rows on all SMs, K split.  Measured (us, that against pairs of 256 x 256): 64
-// tokens through 10240 x 2560 8.6, 9.0, through 4096 x 4096 6.6, 10.0, gated 12288 x 4096 13.6, 17.1, gated
-// 1024 x 1024 7.0, 7.1; 128 tokens through 10240 x 2560 10.5, 9.0, gated 6144 x 2048 10.3, 8.6.  Where the
+// tokens through 10240 x 2560 8.3, 9.0, through 4096 x 4096 6.6, 10.0, gated 12288 x 4096 13.3, 17.1, gated
+// 1024 x 1024 7.1, 7.1; 128 tokens through 10240 x 2560 10.5, 9.0, gated 6144 x 2048 10.3, 8.7.  Where the
 // pairs' tiles fill few SMs it wins for longer: 192 tokens through 2560 x 10240 11.0, 17.3, through 1024 x
-// 4096 8.1, 10.3; 256 through 4096 x 4096 10.3, 10.3; 384 through 2560 x 10240 16.5, 17.7.
+// 4096 8.1, 10.3; 256 through 4096 x 4096 10.6, 10.3; 384 through 2560 x 10240 16.5, 17.7.
 bool few_rows(const cider::FpProduct& p) {
   return p.M <= 64 || (!p.is_gated && p.M <= 256 && (p.N + 255) / 256 <= p.num_sms / 8);
 }

@@ -150,6 +150,45 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
   }
 }
 
+// Four rounded outputs from n on of token m, of a block of the quantized matrix that eight neighbouring
+// threads hold.
+__device__ __forceinline__ void store_quantized(const RowsArgs& p, int64_t m, int n, uint2 w, int lane) {
+  const uint32_t group = 0xFFu << (lane & 24);
+  const uint32_t both_tops = max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+  uint32_t top = max(both_tops & 0xFFFFu, both_tops >> 16);
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(group, top, o));
+  float f[4];
+  if (p.y_bf16) {
+    top <<= 16;
+    f[0] = __uint_as_float(w.x << 16);
+    f[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(w.y << 16);
+    f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+  } else {
+    top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x)),
+                 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    f[0] = lo.x;
+    f[1] = lo.y;
+    f[2] = hi.x;
+    f[3] = hi.y;
+  }
+  const bool bad = not_finite(top);
+  const int e = bad ? 0 : block_power(top);
+  const float inv = pow2(-e);
+  const uint64_t q[4] = {pack2(__float_as_uint(f[0] * inv), __float_as_uint(f[1] * inv)),
+                         pack2(__float_as_uint(f[2] * inv), __float_as_uint(f[3] * inv)), 0ull, 0ull};
+  *reinterpret_cast<uint16_t*>(p.q_codes + m * (p.N >> 1) + (n >> 1)) =
+      bad ? uint16_t{0} : static_cast<uint16_t>(e2m1x8(q));
+  if ((lane & 7) == 0) {
+    uint8_t* at = p.q_scales + scale_at(m, n >> 5, p.q_tiles);
+    *at = bad ? uint8_t{0xFF} : static_cast<uint8_t>(e + 127);
+    // the other block of a step of 64 that the row ends in
+    if (n + 32 == p.N && (p.N & 32) != 0) at[1] = 0;
+  }
+}
+
 template <bool GATED, int BS, bool FUSE>
 __global__ void __launch_bounds__(kRThreads, 2)
     fp4_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_u,
@@ -324,6 +363,16 @@ __global__ void __launch_bounds__(kRThreads, 2)
   // takes the partial sums [accumulator column][weight row].
   const int mv = min(p.tn, p.M - m0);
   float* part = reinterpret_cast<float*>(gbase);
+  // four weight rows of a token at a time, the same four for a thread; the cluster's CTAs take equal shares
+  // in blocks of 32 outputs (eight threads)
+  const int u0 = 8 * (rank * mv * 4 / p.splits), u1 = 8 * ((rank + 1) * mv * 4 / p.splits);
+  const int row0 = nt * 128 + 4 * ((u0 + static_cast<int>(threadIdx.x)) & 31);
+  float sw[4], su[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sw[i] = p.sw && row0 < p.N ? __ldg(p.sw + row0 + i) : 1.0f;
+    su[i] = GATED && p.su && row0 < p.N ? __ldg(p.su + row0 + i) : 1.0f;
+  }
   pdl_wait();
   __syncthreads();   // the copies have landed: an abort leaves none in flight
   bool ok;
@@ -356,91 +405,77 @@ __global__ void __launch_bounds__(kRThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
-  if (ok) {
-    // four weight rows of a token at a time; the cluster's CTAs take equal shares
-    // in blocks of 32 outputs (eight threads)
-    const int u0 = 8 * (rank * mv * 4 / p.splits), u1 = 8 * ((rank + 1) * mv * 4 / p.splits);
-    for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += kThreads) {
-      const int t = u >> 5, n = nt * 128 + 4 * (u & 31);
-      if (n >= p.N) continue;   // N % 8 == 0: four rows are all in or all out
-      float a[GATED ? 8 : 4];
+  // U tokens' and kAsk ranks' partial sums are asked for before the first is added
+  auto finish = [&](auto tokens, auto ranks) {
+    constexpr int U = decltype(tokens)::value, kAsk = decltype(ranks)::value, kSides = GATED ? 2 : 1;
+    for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += U * kThreads) {
+      float a[U][4 * kSides], sx[U];
 #pragma unroll
-      for (int i = 0; i < (GATED ? 8 : 4); ++i) a[i] = 0.0f;
-      // the partial sums of several ranks are asked for before the first is added
-      constexpr int kAsk = GATED ? 4 : 8;
+      for (int k = 0; k < U; ++k) {
+        const int t = (u + k * kThreads) >> 5;
+        const bool have = u + k * kThreads < u1;
+        sx[k] = FUSE ? (BS == 16 && have ? row[t] : 1.0f) : p.sx && have ? ld_global_f32(p.sx + m0 + t) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * kSides; ++i) a[k][i] = 0.0f;
+      }
 #pragma unroll
       for (int r0 = 0; r0 < 8; r0 += kAsk) {
         if (r0 >= p.splits) break;
-        float4 f[kAsk][GATED ? 2 : 1];
+        float4 f[U][kAsk][kSides];
 #pragma unroll
-        for (int r = 0; r < kAsk; ++r)
-          if (r0 + r < p.splits) {
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h)
-              f[r][h] = ld_cluster_v4(mapa_shared(
-                  base + static_cast<uint32_t>(((h * p.tn + t) * 128 + 4 * (u & 31)) * 4), p.splits > 1 ? r0 + r : 0));
-          }
+          for (int r = 0; r < kAsk; ++r)
+            if (r0 + r < p.splits && u + k * kThreads < u1) {
 #pragma unroll
-        for (int r = 0; r < kAsk; ++r)
-          if (r0 + r < p.splits) {
-#pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-              a[4 * h] += f[r][h].x;
-              a[4 * h + 1] += f[r][h].y;
-              a[4 * h + 2] += f[r][h].z;
-              a[4 * h + 3] += f[r][h].w;
+              for (int h = 0; h < kSides; ++h) {
+                const int at = (h * p.tn + ((u + k * kThreads) >> 5)) * 128 + 4 * (u & 31);
+                f[k][r][h] = p.splits > 1 ? ld_cluster_v4(mapa_shared(base + 4u * at, r0 + r))
+                                          : *reinterpret_cast<const float4*>(part + at);
+              }
             }
-          }
-      }
-      const float sx = FUSE ? (BS == 16 ? row[t] : 1.0f) : p.sx ? ld_global_f32(p.sx + m0 + t) : 1.0f;
-      float out[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        out[i] = a[i] * sx * (p.sw ? __ldg(p.sw + n + i) : 1.0f);
-        if (GATED) out[i] = gated(out[i], a[(GATED ? 4 : 0) + i] * sx * (p.su ? __ldg(p.su + n + i) : 1.0f), p.act);
-      }
-      uint2 w;
-      if (p.y_bf16) {
-        w = make_uint2(y_bits2<true>(out[0], out[1]), y_bits2<true>(out[2], out[3]));
-      } else {
-        w = make_uint2(y_bits2<false>(out[0], out[1]), y_bits2<false>(out[2], out[3]));
-      }
-      if (GATED && BS == 32 && p.q_codes) {
-        // eight neighbouring threads hold a block of the quantized matrix
-        const int64_t m = m0 + t;
-        const uint32_t group = 0xFFu << (lane & 24);
-        uint32_t top = max(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu) & 0xFFFFu,
-                           max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu) >> 16);
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(group, top, o));
-        float f[4];
+          for (int r = 0; r < kAsk; ++r)
+            if (r0 + r < p.splits && u + k * kThreads < u1) {
+#pragma unroll
+              for (int h = 0; h < kSides; ++h) {
+                a[k][4 * h] += f[k][r][h].x;
+                a[k][4 * h + 1] += f[k][r][h].y;
+                a[k][4 * h + 2] += f[k][r][h].z;
+                a[k][4 * h + 3] += f[k][r][h].w;
+              }
+            }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (u + k * kThreads >= u1) break;
+        const int t = (u + k * kThreads) >> 5;
+        float out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          out[i] = a[k][i] * sx[k] * sw[i];
+          if constexpr (GATED) out[i] = gated(out[i], a[k][4 + i] * sx[k] * su[i], p.act);
+        }
+        uint2 w;
         if (p.y_bf16) {
-          top <<= 16;
-          f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xFFFF0000u);
-          f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+          w = make_uint2(y_bits2<true>(out[0], out[1]), y_bits2<true>(out[2], out[3]));
         } else {
-          top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
-          const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x)),
-                       a1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-          f[0] = a0.x, f[1] = a0.y, f[2] = a1.x, f[3] = a1.y;
+          w = make_uint2(y_bits2<false>(out[0], out[1]), y_bits2<false>(out[2], out[3]));
         }
-        const bool bad = not_finite(top);
-        const int e = bad ? 0 : block_power(top);
-        const float inv = bad ? 0.0f : pow2(-e);
-        const uint64_t qp[4] = {pack2(__float_as_uint(f[0] * inv), __float_as_uint(f[1] * inv)),
-                                pack2(__float_as_uint(f[2] * inv), __float_as_uint(f[3] * inv)), 0ull, 0ull};
-        *reinterpret_cast<uint16_t*>(p.q_codes + m * (p.N >> 1) + (n >> 1)) =
-            bad ? uint16_t{0} : static_cast<uint16_t>(e2m1x8(qp));
-        if ((lane & 7) == 0) {
-          uint8_t* at = p.q_scales + scale_at(m, n >> 5, p.q_tiles);
-          *at = bad ? uint8_t{0xFF} : static_cast<uint8_t>(e + 127);
-          // the other block of a step of 64 that the row ends in
-          if (n + 32 == p.N && (p.N & 32) != 0) at[1] = 0;
-        }
-        continue;
+        if (GATED && BS == 32 && p.q_codes)
+          store_quantized(p, m0 + t, row0, w, lane);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + static_cast<int64_t>(m0 + t) * p.N + row0) = w;
       }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + static_cast<int64_t>(m0 + t) * p.N + n) = w;
     }
+  };
+  if (ok && row0 < p.N) {   // N % 8 == 0: four weight rows are all in or all out
+    if (p.splits <= 2)
+      finish(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+    else
+      finish(std::integral_constant<int, 1>{}, std::integral_constant<int, GATED ? 4 : 8>{});
   }
   __syncwarp();
   // the partial sums stay until every CTA has read them (what was stored need not be seen by then)
