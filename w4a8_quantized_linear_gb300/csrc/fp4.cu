@@ -150,7 +150,7 @@ cudaError_t launch_quantize(const QuantArgs& p, int num_sms, cudaStream_t st, bo
   }
   const int warps = (p.K + 511) / 512;
   const int per = warps >= 8 ? 1 : 8 / warps, threads = 32 * warps * per;
-  // As many CTAs as run at once (their registers, 50 a thread, hold 1280 threads an SM).  4096 x 4096 bf16,
+  // As many CTAs as run at once (48 registers a thread as they are allocated: 1365 threads an SM).  4096 x 4096 bf16,
   // block 32: 8.0 us, a CTA a row 10.1; 10240 x 2560 fp32 19.6, 27.0; equal rows in fewer CTAs 8.7 and 20.9.
   const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * (1280 / threads);
   quantize_fp4_kernel<T, BS><<<static_cast<unsigned>(groups < most ? groups : most), threads, 0, st>>>(p, warps, release);
