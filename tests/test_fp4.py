@@ -567,3 +567,79 @@ def test_rows_whose_offsets_pass_32_bits(block):
     assert y.numel() > 1 << 31
     assert torch.equal(y[-300:], cider.cider_w4a4_linear(x[-300:], w, block))
     clean()
+
+
+# ------------------------------------------------------------ sizes that fill the GPU with pairs' tiles
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("m,n,k", [(257, 5000, 288), (300, 9800, 544), (1030, 2600, 2080), (700, 3208, 96), (513, 4808, 32),
+                                   (65, 12296, 736), (2100, 1272, 64)])
+def test_many_tokens(m, n, k, block):
+    gen = generator(m, n, k, block)
+    for dtype in TYPES[:2]:
+        x, w = activations(gen, m, k, dtype), ref.matrix(0.05 * normal(gen, n, k), block)
+        y = cider.cider_w4a4_linear(x, w, block)
+        a, b = ref.values(ref.matrix(x, block), block), ref.values(w, block)
+        want = a @ b.T
+        close(y, want, ref.sum_bound(a, b) + ref.half_step(dtype, want) * (1 + 2.0 ** -10))
+    # values that four bits hold: exact
+    pick = lambda r: ref.VALUES.float().cuda()[torch.randint(0, 8, (r, k), generator=gen, device="cuda")] * (
+        1 - 2 * torch.randint(0, 2, (r, k), generator=gen, device="cuda"))
+    x, w = pick(m), pick(n)
+    x[:, ::16], w[:, ::16] = 6.0, -6.0
+    y = cider.cider_w4a4_linear(x.half(), cider.cider_quantize_fp4(w, block), block, y_dtype=torch.bfloat16)
+    assert torch.equal(y, (x.double() @ w.double().T).float().bfloat16())
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("m,f,k,act", [(300, 2600, 1056, "silu"), (129, 9736, 160, "gelu"), (700, 1304, 2080, "silu"), (260, 5000, 64, "gelu")])
+def test_gated_linear_of_many_tokens(m, f, k, act, block):
+    gen = generator(m, f, k, act, block)
+    for dtype in TYPES[:2]:
+        x = activations(gen, m, k, dtype)
+        gate, up = (ref.matrix(0.03 * normal(gen, f, k), block) for _ in range(2))
+        h = cider.cider_w4a4_gated_linear(x, gate, up, block, act)
+        a, gv, uv = (ref.values(q, block) for q in (ref.matrix(x, block), gate, up))
+        g, u = a @ gv.T, a @ uv.T
+        eg, eu = ref.sum_bound(a, gv), ref.sum_bound(a, uv)
+        want = ref.activate(g, act) * u
+        bound = 1.13 * eg * (u.abs() + eu) + ref.activate(g.abs(), act).abs() * eu + want.abs() * 2.0 ** -14 + 2.0 ** -40
+        close(h, want, bound + ref.half_step(dtype, want) * (1 + 2.0 ** -10))
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+def test_many_tokens_edges(block):
+    """Neighbours of the output, rows that are not finite, row scales of the caller's, the whole block, twice the same bits."""
+    gen = generator(block)
+    m, n, k = 300, 5000, 96
+    x, w = activations(gen, m, k, torch.bfloat16), cider.cider_quantize_fp4(0.05 * normal(gen, n, k), block)
+    room = torch.full((m * n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = cider.cider_w4a4_linear(x, w, block, out=room[64 : 64 + m * n].view(m, n))
+    assert bool((room[:64] == 7).all()) and bool((room[64 + m * n :] == 7).all())
+    assert torch.equal(y, cider.cider_w4a4_linear(x, w, block))
+    h = cider.cider_w4a4_gated_linear(x, w, w, block, out=room[64 : 64 + m * n].view(m, n))
+    assert bool((room[:64] == 7).all()) and bool((room[64 + m * n :] == 7).all())
+    assert torch.equal(h, cider.cider_w4a4_gated_linear(x, w, w, block))
+    z = x.clone()
+    z[[5, 299], 40] = torch.tensor([float("nan"), float("inf")], device="cuda").bfloat16()
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    bad[[5, 299]] = True
+    for call in (lambda v: cider.cider_w4a4_linear(v, w, block), lambda v: cider.cider_w4a4_gated_linear(v, w, w, block)):
+        got, want = call(z), call(x)
+        assert bool(torch.isnan(got[bad]).all()) and torch.equal(got[~bad], want[~bad])
+    (xc, xs, _), (wc, ws, _) = cider.cider_quantize_fp4(x, block), w
+    rx, rw = torch.rand(m, generator=gen, device="cuda") + 0.3, torch.rand(n, generator=gen, device="cuda") + 0.3
+    for qx, qw in (((xc, xs, rx), (wc, ws, rw)), ((xc, xs, None), (wc, ws, rw)), ((xc, xs, None), (wc, ws, None))):
+        y = cider.cider_w4a4_linear_prequant(qx, qw, block, torch.bfloat16)
+        a, b = ref.values(qx, block), ref.values(qw, block)
+        close(y, a @ b.T, ref.sum_bound(a, b) + ref.half_step(torch.bfloat16, a @ b.T) * (1 + 2.0 ** -10))
+    f = 9760   # ends in the middle of a step of 64
+    gate, up = (cider.cider_quantize_fp4(0.03 * normal(gen, f, k), block) for _ in range(2))
+    down = cider.cider_quantize_fp4(0.03 * normal(gen, 264, f), block)
+    y = cider.cider_w4a4_feed_forward(x, gate, up, down, block)
+    assert torch.equal(y, cider.cider_w4a4_linear(cider.cider_w4a4_gated_linear(x, gate, up, block), down, block))
+    clean()

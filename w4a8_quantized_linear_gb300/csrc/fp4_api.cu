@@ -62,13 +62,15 @@ struct Held {
   }
 };
 
-// Few tokens: weights by 128 rows on all SMs, K split.  Measured (us, that against pairs of 256 x 256): 64
-// tokens through 10240 x 2560 8.3, 9.0, through 4096 x 4096 6.6, 10.0, gated 12288 x 4096 13.3, 17.1, gated
-// 1024 x 1024 7.1, 7.1; 128 tokens through 10240 x 2560 10.5, 9.0, gated 6144 x 2048 10.3, 8.7.  Where the
-// pairs' tiles fill few SMs it wins for longer: 192 tokens through 2560 x 10240 11.0, 17.3, through 1024 x
-// 4096 8.1, 10.3; 256 through 4096 x 4096 10.6, 10.3; 384 through 2560 x 10240 16.5, 17.7.
+// Few tokens: 128 rows of weights a CTA, K split.  Up to 64 tokens, or where its tiles of 64 (128, if not
+// gated) tokens are at most half as many as the SMs.  Measured (us, that against pairs of 256 x 256), weights
+// from memory: 64 tokens through 10240 x 2560 8.6, 9.3, gated 12288 x 4096 16.0, 19.0, gated 6144 x 2048 9.1,
+// 9.5; 96 through 10240 x 2560 9.7, 9.5, gated 6144 x 2048 9.9, 9.8; 128 through 4096 x 4096 8.8, 10.9; 256
+// through 1024 x 4096 6.8, 10.2, through 2560 x 10240 13.0, 17.7; 512 through 2048 x 6144 11.0, 13.0, gated
+// 1024 x 1024 6.8, 7.2; 768 through 2048 x 6144 13.8, 12.9, gated 1024 x 1024 7.7, 7.2.
 bool few_rows(const cider::FpProduct& p) {
-  return p.M <= 64 || (!p.is_gated && p.M <= 256 && (p.N + 255) / 256 <= p.num_sms / 8);
+  const int64_t rows = (p.N + 127) / 128, half = p.num_sms / 2;
+  return p.M <= 64 || (p.M + 63) / 64 * rows <= half || (!p.is_gated && (p.M + 127) / 128 * rows <= half);
 }
 
 // Few enough that the product's kernel quantizes the rows itself, each CTA its part of K: one launch

@@ -283,7 +283,7 @@ struct FpProduct {
   int num_sms = 0;
   cudaStream_t st = nullptr;
 };
-// fp4_rows.cu: 128 rows of weights against all (up to 256) tokens, K split over a cluster.
+// fp4_rows.cu: 128 rows of weights against up to 128 tokens, K split over a cluster.
 cudaError_t launch_fp4_rows(const FpProduct& p);
 // Whether it can quantize x itself (wide_x): few tokens, a part of K that fits beside the weights.
 bool fp4_rows_quantizes_itself(const FpProduct& p);

@@ -2,7 +2,7 @@
 // y[m, n] = sum_k x[m, k] w[n, k], both E2M1 with block scales, on the
 // block-scaled tensor cores.
 //
-// 128 rows of weights are the MMA's M, up to 256 tokens its N, so one token
+// 128 rows of weights are the MMA's M, up to 128 tokens its N, so one token
 // wastes tensor-core rows (which are free here) and no bytes: the weights are
 // read once, straight from HBM into shared memory by TMA, and nothing converts
 // them.  K is split over a cluster of CTAs, which add up their partial sums
@@ -39,14 +39,13 @@ constexpr int kRMaxFusedStages = 16;                   // of a CTA's part of K, 
 
 struct RowsArgs {
   int M, N, K;
-  int tn;            // tokens of a tile: 16, 32, 64, 128 or 256
-  int m_tiles;       // token tiles (one, unless tn is 128 or 256)
+  int tn;            // tokens of a tile: 16, 32, 64 or 128
+  int m_tiles;       // token tiles (one, unless tn is 64 or 128)
   int splits;        // CTAs of a cluster
   int nkb;           // stages of K in all
   int nsteps;        // MMAs of K in all
   int stages;        // ring slots
   int stage_bytes, tok_offset, sfw_offset, sfu_offset, sft_offset;   // within a stage
-  int tok_tiles;     // 128-row tiles of the tokens' scales in a stage: 1 or 2
   int x_offset, xs_offset;   // FUSE: all of the part's codes, and scales, of x
   int tail;          // barriers and what follows
   int sc_tiles;      // tiles of scales along K
@@ -218,13 +217,12 @@ __global__ void __launch_bounds__(kRThreads, 2)
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.nkb / p.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.nkb / p.splits);
 
-  const int tok_tiles = FUSE ? 0 : min(p.tok_tiles, (p.M + 127) / 128 - (m0 >> 7));
   // bytes of scales that a stage has (the last one may have fewer tiles)
   auto scale_bytes = [&](int kb) { return min(B::kTiles, p.sc_tiles - kb * B::kTiles) * kFpTileBytes; };
   auto weights = [&](int kb, int s) {
     const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
     const int64_t from = (static_cast<int64_t>(nt) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes;
-    mbar_arrive_expect_tx(full_bar(s), (GATED ? 2u : 1u) * (kROperand + sb) + (FUSE ? 0u : p.tn * 128u) + tok_tiles * sb);
+    mbar_arrive_expect_tx(full_bar(s), (GATED ? 2u : 1u) * (kROperand + sb) + (FUSE ? 0u : p.tn * 128u + sb));
     tma_load_2d(at, &tm_w, full_bar(s), kb * 128, nt * 128);
     if (GATED) tma_load_2d(at + kROperand, &tm_u, full_bar(s), kb * 128, nt * 128);
     bulk_load(at + p.sfw_offset, p.scw + from, sb, full_bar(s));
@@ -281,10 +279,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
       auto tokens = [&](int kb, int s) {
         const uint32_t at = base + s * p.stage_bytes, sb = scale_bytes(kb);
         tma_load_2d(at + p.tok_offset, &tm_x, full_bar(s), kb * 128, m0);
-        for (int t = 0; t < tok_tiles; ++t)
-          bulk_load(at + p.sft_offset + t * B::kBytes,
-                    p.scx + (static_cast<int64_t>((m0 >> 7) + t) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes, sb,
-                    full_bar(s));
+        bulk_load(at + p.sft_offset,
+                  p.scx + (static_cast<int64_t>(m0 >> 7) * p.sc_tiles + kb * B::kTiles) * kFpTileBytes, sb, full_bar(s));
       };
       if (!FUSE) {
         pdl_wait();
@@ -306,7 +302,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
     const uint32_t sfw = tmem + acc_cols, sfu = sfw + B::kCols, sft = sfw + (GATED ? 2 : 1) * B::kCols;
-    const uint32_t tcols = 4 * p.tok_tiles;   // columns of the tokens' scales of one tile of K
+    const uint32_t sfm = sft + ((m0 >> 5) & 3);   // 64 tokens may start in the middle of a tile of scales
     if (elect_one()) {   // one lane runs the whole loop
       int s = 0, i = 0;
       uint32_t phase = 0;
@@ -327,12 +323,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
         for (int a = 0; a < B::kTiles; ++a) {
           tc_cp_scales<1>(sfw + 4 * a, dw + a * (kFpTileBytes >> 4));
           if (GATED) tc_cp_scales<1>(sfu + 4 * a, du + a * (kFpTileBytes >> 4));
-          tc_cp_scales<1>(sft + tcols * a, dt + a * (kPitch >> 4));
+          tc_cp_scales<1>(sft + 4 * a, dt + a * (kPitch >> 4));
         }
-        if (!FUSE && p.tok_tiles == 2)
-#pragma unroll
-          for (int a = 0; a < B::kTiles; ++a)
-            tc_cp_scales<1>(sft + tcols * a + 4, dt + ((B::kBytes + a * kFpTileBytes) >> 4));
         const uint64_t wd = smem_desc_k_sw128(at), ud = smem_desc_k_sw128(at + kROperand),
                        td = smem_desc_k_sw128(FUSE ? base + p.x_offset + i * (kRTokens * 128) : at + p.tok_offset);
 #pragma unroll
@@ -340,8 +332,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
           if (!decltype(full)::value && j >= steps) break;
           const int a = BS == 16 ? j : j >> 1, id = BS == 16 ? 0 : 2 * (j & 1);
           const uint32_t idesc = idesc_fp4<BS>(128, FUSE ? kRTokens : p.tn, id), acc = first && j == 0 ? 0u : 1u;
-          tc_mma_fp4<1, BS>(tmem, wd + 2 * j, td + 2 * j, idesc, sfw + 4 * a, sft + tcols * a, acc);
-          if (GATED) tc_mma_fp4<1, BS>(tmem + p.tn, ud + 2 * j, td + 2 * j, idesc, sfu + 4 * a, sft + tcols * a, acc);
+          tc_mma_fp4<1, BS>(tmem, wd + 2 * j, td + 2 * j, idesc, sfw + 4 * a, sfm + 4 * a, acc);
+          if (GATED) tc_mma_fp4<1, BS>(tmem + p.tn, ud + 2 * j, td + 2 * j, idesc, sfu + 4 * a, sfm + 4 * a, acc);
         }
         tc_commit(empty_bar(s));
         ++i;
@@ -525,38 +517,37 @@ bool plan(const FpProduct& p, bool fuse, RowsArgs& a, int* smem_out, int* tiles_
   a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
   a.K = static_cast<int>(p.K);
-  const int most = p.is_gated ? 128 : 256;
+  // up to 64 tokens in one tile; more by 64 where that leaves two CTAs' worth of SMs to each tile, else by 128
+  const int n_tiles = static_cast<int>((p.N + 127) / 128);
   a.tn = 16;
-  while (a.tn < most && a.tn < p.M) a.tn *= 2;
+  while (a.tn < 64 && a.tn < p.M) a.tn *= 2;
+  if (p.M > 64 && (p.M + 63) / 64 * n_tiles > p.num_sms / 2) a.tn = 128;
   a.m_tiles = static_cast<int>((p.M + a.tn - 1) / a.tn);
   a.nkb = static_cast<int>((p.K + kFpStageK - 1) / kFpStageK);
   a.nsteps = static_cast<int>((p.K + kFpStepK - 1) / kFpStepK);
   a.sc_tiles = fp4_tiles(p.K, p.block);
-  a.tok_tiles = a.tn > 128 ? 2 : 1;
   a.tok_offset = sides * kROperand;
   a.sfw_offset = a.tok_offset + (fuse ? 0 : a.tn * 128);
   a.sfu_offset = a.sfw_offset + bytes;
   a.sft_offset = a.sfw_offset + sides * bytes;
-  a.stage_bytes = (a.sft_offset + (fuse ? 0 : a.tok_tiles * bytes) + 1023) / 1024 * 1024;
-  const int cols = sides * a.tn + (sides + a.tok_tiles) * cols_side;
+  a.stage_bytes = (a.sft_offset + (fuse ? 0 : bytes) + 1023) / 1024 * 1024;
+  const int cols = sides * a.tn + (sides + 1) * cols_side;   // at most 176
   a.tmem_cols = 64;
   while (static_cast<int>(a.tmem_cols) < cols) a.tmem_cols *= 2;
   // As many CTAs as SMs, or a few more, K split in a power of two.  Measured (two more splits, a CTA
   // or two on each SM): one token through 4096 x 4096, 32 tiles in 4 parts 5.7 us, in 8 parts 7.4; 16
   // through 2560 x 10240, 20 tiles in 8 parts 10.6, in 4 parts 11.8; 128 through 10240 x 2560, 80 tiles
   // in 2 parts 12.9, whole 14.3.  Other numbers of parts lose 5 us to the placing of their clusters.
-  // Where there are more CTAs than that they share SMs in pairs: they hold at most half of the tensor
-  // memory, and their shared memory allows two and no third.  All others have an SM to themselves.  So
-  // no CTA of a cluster waits for tensor memory that another cluster's holds.
-  const int tiles = a.m_tiles * static_cast<int>((p.N + 127) / 128);
-  // Clusters of 4 and of 8 do not reach every SM (144 and 120 of 152 with a CTA on each).
-  const bool small = a.tmem_cols <= 256;
-  auto reach = [&](int splits) { return splits == 8 ? p.num_sms * 3 / 4 : splits == 4 ? p.num_sms * 15 / 16 : p.num_sms; };
+  // Clusters of 4 and of 8 do not reach every SM (144 and 120 of 152 with a CTA on each).  Where there are
+  // more CTAs than that they share SMs in pairs: they hold at most half of the tensor memory, and their shared
+  // memory allows two and no third.  All others have an SM to themselves.  So no CTA of a cluster waits for
+  // tensor memory that another cluster's holds.
+  const int tiles = a.m_tiles * n_tiles;
   a.splits = 1;
-  while (a.splits < 8 && a.nkb >= a.splits * 4 &&
-         tiles * a.splits * 2 <= (small ? p.num_sms + p.num_sms / 16 : reach(a.splits * 2)))
-    a.splits *= 2;
-  const bool two = small && tiles * a.splits > reach(a.splits);
+  while (a.splits < 8 && a.nkb >= a.splits * 4 && tiles * a.splits * 2 <= p.num_sms + p.num_sms / 16) a.splits *= 2;
+  const bool two = tiles * a.splits > (a.splits == 8   ? p.num_sms * 3 / 4
+                                       : a.splits == 4 ? p.num_sms * 15 / 16
+                                                       : p.num_sms);
   const int budget = two ? 110 * 1024 : 224 * 1024;
   const int mine = (a.nkb + a.splits - 1) / a.splits;   // stages of a CTA, at most
   int held = 0;
