@@ -73,6 +73,26 @@ def test_quantize_bit_for_bit(rows, cols, dtype, block):
 @gpu
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,cols", [(5, 4064), (1300, 4128), (700, 8160), (350, 12320), (3, 16416), (200, 20512), (2, 32768),
+                                       (3, 32800)])
+def test_quantize_long_rows_bit_for_bit(rows, cols, dtype, block):
+    gen = generator(rows, cols, str(dtype), block)
+    wide = (normal(gen, rows, cols + 32) * torch.exp(normal(gen, rows, 1))).to(dtype)
+    x = wide[:, 16:16 + cols]
+    x[:, cols // 3] *= 50
+    x[rows // 2, cols // 2:] = 0
+    x[0, cols - 1] = 400   # the last unit holds the row's maximum
+    q = cider.cider_quantize_fp4(x, block)
+    codes, held, row = ref.quantize(x, block)
+    assert torch.equal(q[1], ref.tiles(held))
+    assert (q[2] is None) == (row is None) and (row is None or torch.equal(q[2], row))
+    assert torch.equal(torch.stack((q[0] & 15, q[0] >> 4), -1).flatten(1).long(), codes)
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_quantize_edges(dtype, block):
     """Ties of every code, the largest and the smallest numbers, borders of the scales, signed zeros."""
     big = torch.finfo(dtype).max

@@ -9,7 +9,7 @@
 // Divisions by powers of two are exact, so block 32 rounds once and block 16
 // rounds the scale's quotient, the scale, a value's quotient and the value.
 //
-// A thread holds 16 values: 8 bytes of codes, one E4M3 scale or (two threads)
+// A thread holds one unit of 16 values, or two: 8 bytes of codes, one E4M3 scale or (two threads)
 // one E8M0 scale.  Memory bounds it: 2 or 4 bytes read and 1/2 + 1/16 written a
 // value; each row is read once, the row's maximum is exchanged through shared
 // memory while the values stay in registers.
@@ -20,7 +20,10 @@
 namespace cider {
 namespace {
 
-constexpr int kRowK = 16384;   // longest row whose values stay in registers: 1024 threads x 16
+constexpr int kRowK = 32768;   // longest row whose values stay in registers: 1024 threads x 32
+// Threads an SM that quantize_fp4_kernel is compiled and launched for (48 or 40 registers a thread; 64 for two units).
+template <int BS, int U>
+constexpr int kResident = U == 2 ? 1024 : BS == 16 ? 1280 : 1536;
 
 struct QuantArgs {
   const void* x;
@@ -48,17 +51,17 @@ __device__ __forceinline__ uint8_t* scale_row(const QuantArgs& p, int64_t r) {
   return r < p.padded ? p.scales + scale_at(r, 0, p.tiles) : nullptr;
 }
 
-// `warps` warps take a row (K <= 512 warps), blockDim / (32 warps) rows a CTA at a time.  (The next
+// `warps` warps take a row (K <= 512 U warps), blockDim / (32 warps) rows a CTA at a time.  (The next
 // rows' values asked for before these are encoded: 8.3 us for 7.4, in registers that other CTAs use better.)
-template <typename T, int BS>
-__global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) {
+template <typename T, int BS, int U>
+__global__ void __launch_bounds__(U == 1 ? 256 : 1024, U == 1 ? kResident<BS, U> / 256 : 1)
+quantize_fp4_kernel(const QuantArgs p, int warps, bool release) {
   __shared__ uint32_t part[2][32];
   if (release) pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / warps, w = warp - sub * warps;
   const int per = blockDim.x / (32 * warps);
-  const int k = (w * 32 + lane) * 16;
-  const bool in = k < p.K;   // K % 32 == 0: a thread's 16 values are all in or all out
+  const int k = (w * 32 + lane) * 16, across = warps * 512;   // a thread's 16 values: k + u across
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
   int64_t r = static_cast<int64_t>(blockIdx.x) * per + sub;
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride + k;
@@ -67,20 +70,30 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
   const int64_t codes_step = step * (p.K >> 1);
   // every thread of the CTA makes the same turns
   for (int64_t turn = static_cast<int64_t>(blockIdx.x) * per, n = 0; turn < p.padded; turn += step, r += step, ++n) {
-    const bool have = in && r < p.rows;
-    Sixteen<T> v;
-    if (have)
-      v.load(x);
-    else
-      v.clear();
+    bool have[U];
+    Sixteen<T> v[U];
+    uint32_t top[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      have[u] = k + u * across < p.K && r < p.rows;   // K % 32 == 0: 16 values are all in or all out
+      if (have[u])
+        v[u].load(x + u * across);
+      else
+        v[u].clear();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top[u] = v[u].top();
     x += x_step;
-    uint32_t top = v.top();
     float inv_row = 1.0f;
     bool bad = false;
     if constexpr (BS == 32) {
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+#pragma unroll
+      for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], 1));
     } else {
-      uint32_t most = __reduce_max_sync(0xffffffffu, top);
+      uint32_t most = top[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) most = max(most, top[u]);
+      most = __reduce_max_sync(0xffffffffu, most);
       if (warps > 1) {
         if (lane == 0) part[n & 1][warp] = most;
         __syncthreads();
@@ -90,11 +103,14 @@ __global__ void quantize_fp4_kernel(const QuantArgs p, int warps, bool release) 
       inv_row = pow2(-row_power(most));
       if (w == 0 && lane == 0 && r < p.rows) p.row[r] = row_scale(most);
     }
-    uint32_t c[2] = {0u, 0u}, byte = 0u;
-    if (have && !bad) byte = encode16<T, BS>(v, top, inv_row, c);
-    if (have) *reinterpret_cast<uint2*>(codes) = make_uint2(c[0], c[1]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t c[2] = {0u, 0u}, byte = 0u;
+      if (have[u] && !bad) byte = encode16<T, BS>(v[u], top[u], inv_row, c);
+      if (have[u]) *reinterpret_cast<uint2*>(codes + u * (across >> 1)) = make_uint2(c[0], c[1]);
+      store_scales<BS>(scale_row(p, r), p.tiles, k + u * across, byte, lane);
+    }
     codes += codes_step;
-    store_scales<BS>(scale_row(p, r), p.tiles, k, byte, lane);
   }
 }
 
@@ -142,19 +158,27 @@ __global__ void __launch_bounds__(1024) quantize_fp4_long_kernel(const QuantArgs
   }
 }
 
+template <typename T, int BS, int U>
+cudaError_t launch_rows(const QuantArgs& p, int num_sms, cudaStream_t st, bool release) {
+  const int warps = (p.K + 512 * U - 1) / (512 * U);
+  const int per = warps >= 8 ? 1 : 8 / warps, threads = 32 * warps * per;
+  // As many CTAs as run at once.  4096 x 4096 bf16, block 32: 7.8 us, a CTA a row 10.1; 10240 x 2560 fp32 19.4, 27.0;
+  // equal rows in fewer CTAs 8.7 and 20.9.
+  const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * (kResident<BS, U> / threads);
+  quantize_fp4_kernel<T, BS, U><<<static_cast<unsigned>(groups < most ? groups : most), threads, 0, st>>>(p, warps, release);
+  return cudaGetLastError();
+}
+
 template <typename T, int BS>
 cudaError_t launch_quantize(const QuantArgs& p, int num_sms, cudaStream_t st, bool release) {
   if (p.K > kRowK) {
     quantize_fp4_long_kernel<T, BS><<<static_cast<unsigned>(p.padded), 1024, 0, st>>>(p, release);
     return cudaGetLastError();
   }
-  const int warps = (p.K + 511) / 512;
-  const int per = warps >= 8 ? 1 : 8 / warps, threads = 32 * warps * per;
-  // As many CTAs as run at once (48 registers a thread as they are allocated: 1365 threads an SM).  4096 x 4096 bf16,
-  // block 32: 8.0 us, a CTA a row 10.1; 10240 x 2560 fp32 19.6, 27.0; equal rows in fewer CTAs 8.7 and 20.9.
-  const int64_t groups = (p.padded + per - 1) / per, most = static_cast<int64_t>(num_sms) * (1280 / threads);
-  quantize_fp4_kernel<T, BS><<<static_cast<unsigned>(groups < most ? groups : most), threads, 0, st>>>(p, warps, release);
-  return cudaGetLastError();
+  // Long rows: two units a thread keep two CTAs or more on an SM, and half as many warps meet for a row's maximum.
+  // bf16, block 16, one unit against two: 4096 x 4096 11.1 us, 10.0; 8192 x 12288 94, 57 (block 32: 48, 38); but fp16
+  // 4096 x 2560 7.6, 8.1.
+  return p.K >= 4096 ? launch_rows<T, BS, 2>(p, num_sms, st, release) : launch_rows<T, BS, 1>(p, num_sms, st, release);
 }
 
 template <int BS>
