@@ -74,17 +74,21 @@ bool few_rows(const cider::FpProduct& p) {
 }
 
 // Few enough that the product's kernel quantizes the rows itself, each CTA its part of K: one launch
-// instead of two.  Not where y lies on x: CTAs that are done would write what others still read.
+// instead of two.  Not where y lies on x: CTAs that are done would write what others still read.  A null x
+// or y is scratch of the call, which neither the caller's matrices nor other scratch overlap.
 bool quantizes_itself(const cider::FpProduct& p, const void* x, const void* y) {
+  if (!few_rows(p) || !cider::fp4_rows_quantizes_itself(p)) return false;
+  if (!x || !y) return true;
   const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
   const uintptr_t xn = 2 * ((p.M - 1) * p.x_stride + p.K), yn = 2 * p.M * p.N;
-  return few_rows(p) && !(x0 < y0 + yn && y0 < x0 + xn) && cider::fp4_rows_quantizes_itself(p);
+  return !(x0 < y0 + yn && y0 < x0 + xn);
 }
 
-// A product of x in 16 bits: quantized into `held` (scratch) first, or by the product's kernel.
-cudaError_t product(cider::FpProduct& p, const cider::FpMat& held) {
+// A product of x in 16 bits: quantized by the product's kernel (`itself`: what quantizes_itself said when
+// the scratch was sized), or into `held` (scratch) first.
+cudaError_t product(cider::FpProduct& p, bool itself, const cider::FpMat& held) {
   if (p.wide_x) {
-    if (quantizes_itself(p, p.wide_x, p.y)) return cider::launch_fp4_rows(p);
+    if (itself) return cider::launch_fp4_rows(p);
     const cudaError_t e = cider::launch_quantize_fp4(
         p.wide_x, p.x_bf16 ? CIDER_BF16 : CIDER_F16, p.x_stride, p.M, p.K, p.block, const_cast<uint8_t*>(held.codes),
         const_cast<uint8_t*>(held.scales), const_cast<float*>(held.row), false, p.num_sms, p.st, true);
@@ -182,9 +186,10 @@ cider_status_t run(const Call& c) {
     // scratch: x's codes and scales; for a whole block the hidden values, their codes and scales.  Block
     // size 32: the first product writes the hidden values quantized.  Block size 16 needs their rows' maxima.
     const bool straight = c.down && block == 32;
-    // (Scratch is not the caller's: neither h lies on x nor y on h.)
-    const Held hx(p.wide_x && !quantizes_itself(p, c.x, c.down ? nullptr : c.y) ? M : 0, K, block),
-        hh(c.down && (straight || !quantizes_itself(d, nullptr, c.y)) ? M : 0, c.down ? F : 32, block);
+    // Who quantizes is decided here alone: the launches below follow it.
+    const bool first = p.wide_x && quantizes_itself(p, c.x, c.down ? nullptr : c.y),
+               second = c.down && !straight && quantizes_itself(d, nullptr, c.y);
+    const Held hx(p.wide_x && !first ? M : 0, K, block), hh(c.down && !second ? M : 0, c.down ? F : 32, block);
     const size_t wide = c.down && !straight ? round256(static_cast<size_t>(M) * F * 2) : 0;
     cider::ScratchSource scratch = cider::ScratchSource::pooled(st);
     uint8_t* base = nullptr;
@@ -200,7 +205,7 @@ cider_status_t run(const Call& c) {
       p.q_codes = const_cast<uint8_t*>(hidden.codes);
       p.q_scales = const_cast<uint8_t*>(hidden.scales);
     }
-    const cudaError_t e = product(p, hx.at(base, M));
+    const cudaError_t e = product(p, first, hx.at(base, M));
     if (e != cudaSuccess || !c.down) return cuda_status(e);
     // its weights do not depend on the launch before
     d.after_launch = true;
@@ -208,7 +213,7 @@ cider_status_t run(const Call& c) {
       d.x = hidden;
     else
       d.wide_x = p.y;
-    return cuda_status(product(d, hidden));
+    return cuda_status(product(d, second, hidden));
   });
 }
 
