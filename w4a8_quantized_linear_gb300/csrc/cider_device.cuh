@@ -499,6 +499,17 @@ __device__ __forceinline__ float ld_global_f32(const float* p) {
   return v;
 }
 
+// Sixteen bytes that the launch before may have written: behind pdl_wait(), and through the coherent path
+// (ld_stream_v4's is for what no one writes while the kernel is there).
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- outputs
 // 32 bytes to a 32-byte boundary of global memory.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {

@@ -124,10 +124,13 @@ struct Sixteen {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
+  // FRESH: the launch just before, with whose end this kernel overlaps, may have written them.
+  template <bool FRESH = false>
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 u = ld_stream_v4(reinterpret_cast<const uint32_t*>(p) + 4 * i);
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(p) + 4 * i;
+      const uint4 u = FRESH ? ld_global_v4(at) : ld_stream_v4(at);
       w[4 * i] = u.x;
       w[4 * i + 1] = u.y;
       w[4 * i + 2] = u.z;

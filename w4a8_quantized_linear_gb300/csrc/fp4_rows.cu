@@ -92,7 +92,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
     for (int j = 0; j < kBatch; ++j) {
       const int u = j * kThreads + thread, r = per == 1 ? u : __umulhi(u, magic);
       v[j].clear();
-      if (u < units) v[j].load(x + r * p.x_stride + (u - r * per) * 16);
+      if (u < units) v[j].template load<true>(x + r * p.x_stride + (u - r * per) * 16);
     }
     meet();
 #pragma unroll
@@ -133,7 +133,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
       for (int j = 0; j < kBatch; ++j) {
         const int u = u0 + j * kThreads + thread, r = __umulhi(u, magic), k = k0 + 16 * (u - r * per);
         v[j].clear();
-        if (u < units && k < p.K) v[j].load(x + r * p.x_stride + k);
+        if (u < units && k < p.K) v[j].template load<true>(x + r * p.x_stride + k);
       }
       if (u0 == 0) meet();
 #pragma unroll
