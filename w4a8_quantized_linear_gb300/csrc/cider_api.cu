@@ -35,9 +35,18 @@ bool force_unsupported() {
   return v != nullptr && v[0] == '1';
 }
 
+// While it lives, this thread may make calls that are otherwise refused (and end the capture) while a
+// stream is being captured.
+struct CaptureAllowsSetUp {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CaptureAllowsSetUp() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~CaptureAllowsSetUp() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 cudaError_t get_pool(int dev, cudaMemPool_t* pool) {
   std::lock_guard<std::mutex> lk(g_pool_mu);
   if (!g_pool[dev]) {
+    const CaptureAllowsSetUp set_up;   // a program's first call may be one that it captures
     cudaMemPoolProps props;
     memset(&props, 0, sizeof(props));
     props.allocType = cudaMemAllocationTypePinned;
