@@ -348,7 +348,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFThreads, 1)
     }
     if (lane == 0) bulk_wait_group<0>();
   }
+  // The odd CTA's warp 1 has nothing to do until here: it begins to wait when the last tile has been drained,
+  // not with the call, which may take longer than a wait does.
   __syncwarp();
+  __syncthreads();
   if (warp == 1) {
     // no MMA is in flight when the pair frees its tensor memory, also after a wait that gave up
     if (lane == 0) {

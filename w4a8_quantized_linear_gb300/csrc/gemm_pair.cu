@@ -719,7 +719,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
   }
 done:
+  // The odd CTA's issuers have nothing to do until here: the wait begins when
+  // the last tile has been drained, not with the call, which may take longer.
   __syncwarp();
+  __syncthreads();
   if (warp == 1) {
     // the even CTA's last commit reaches both CTAs; wait for it (bounded, and
     // also after an abort) so no MMA is in flight when the pair frees its

@@ -580,6 +580,10 @@ done:
   __syncwarp();
   cp_async_wait<0>();   // also after an abort: no copy into shared memory outlives the CTA
   if (EPI != kEpiAcc && warp == kGEpiWarp0 && lane == 0) bulk_wait_group<0>();   // y stores written
+  // The odd CTA's issuer has nothing to do until here: the wait begins when the
+  // last tile has been drained, not with the call, which may take longer.
+  __syncwarp();
+  __syncthreads();
   if (warp == kGMmaWarp) {
     // the even CTA's last commit reaches both CTAs; wait for it (bounded, and
     // also after an abort) so no MMA is in flight when the pair frees its
