@@ -469,7 +469,9 @@ cider_status_t cider_w4a4_linear_prequant(const cider_fp4_t* x, const cider_fp4_
  *               (g + 0.044715 g^3))) / 2
  *   h           [M, F] of h_dtype
  * Both sums are fp32 and are not rounded before the activation; e^x and the
- * reciprocal are the hardware's approximations (2 ulp); one rounding to h_dtype. */
+ * reciprocal are the hardware's approximations (2 ulp); one rounding to h_dtype.
+ * 1 / (1 + e^-t) (SiLU: t = g; GELU: t = 2 sqrt(2 / pi) (g + 0.044715 g^3)) counts
+ * as zero where it is below 2^-126, t below -87.3, whatever the other sum is. */
 cider_status_t cider_w4a4_gated_linear(const void* x, int x_dtype, int64_t x_stride, int64_t M,
                                        const cider_fp4_t* gate, const cider_fp4_t* up, int activation,
                                        void* h, int h_dtype, void* stream);

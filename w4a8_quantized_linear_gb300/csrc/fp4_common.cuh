@@ -82,7 +82,10 @@ __device__ __forceinline__ void tc_mma_fp4(uint32_t d, uint64_t a, uint64_t b, u
 
 // act(g) * u with act(g) = g / (1 + e^-t): t = g (SiLU), or t = 2 sqrt(2 / pi) (g + 0.044715 g^3),
 // for which g / (1 + e^-t) = g (1 + tanh(t / 2)) / 2 (GELU).  2^x and the reciprocal are the
-// hardware's approximations (2 ulp each), far below the 16-bit result's half step.
+// hardware's approximations (2 ulp each), far below the 16-bit result's half step, as long as the
+// reciprocal is a normal number: below t = -87 act(g), less than 2e-35, counts as zero, whatever u is.
+// (Giving e^(t / 2) to each factor there costs five operations an output, 2 us in 34 for 1334 tokens
+// through a block of 6144 x 2048; one test for 64 outputs and a second form of them 4 us and more.)
 __device__ __forceinline__ float gated(float g, float u, int act) {
   const float t = act == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
   float e, r;
