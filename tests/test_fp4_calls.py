@@ -2,52 +2,17 @@
 over launchers that only write down their arguments, so that no GPU is needed and every address can be made up."""
 import ctypes
 import itertools
-import os
-import subprocess
 
 import pytest
 
-from w4a8_quantized_linear_gb300 import _build
+from tests.fp4_calls import FEW, PAIRS, QUANTIZE, SCRATCH, first_on_pairs, library, made, product_kernels, weights
 
-HERE = os.path.dirname(os.path.abspath(__file__))
 BASE = 0x700000000000
-SCRATCH, QUANTIZE, FEW, PAIRS = range(4)
-NAMES = ("kind bytes wide codes scales row y to_codes to_scales to_row stride m n k gated dependent").split()
-
-
-class Record(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int64) for n in NAMES]
-
-
-class Fp4(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
-                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("block_size", ctypes.c_int32)]
 
 
 @pytest.fixture(scope="module")
-def lib(tmp_path_factory):
-    out = str(tmp_path_factory.mktemp("fp4") / "calls.so")
-    subprocess.run([_build._nvcc(), *_build.ARCH, *_build.NVCC_FLAGS, "-I", _build.CSRC, "-shared", "-o", out,
-                    os.path.join(HERE, "fp4_calls.cu")], check=True, capture_output=True)
-    loaded = ctypes.CDLL(out)
-    p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-    loaded.calls_begin.argtypes = [i64, i32, i32]
-    loaded.calls_records.restype = p
-    loaded.cider_w4a4_linear.argtypes = [p, i32, i64, i64, p, p, i32, p]
-    loaded.cider_w4a4_gated_linear.argtypes = [p, i32, i64, i64, p, p, i32, p, i32, p]
-    loaded.cider_w4a4_feed_forward.argtypes = [p, i32, i64, i64, p, p, p, i32, p, i32, p]
-    return loaded
-
-
-def weights(rows, cols, block):
-    """A matrix far away from everything else."""
-    far = 0x100000000000
-    return Fp4(far, far + (1 << 40), None, rows, cols, block)
-
-
-def made(lib):
-    n = lib.calls_made()
-    return [Record.from_buffer_copy(r) for r in (Record * n).from_address(lib.calls_records())] if n else []
+def lib():
+    return library()
 
 
 def up(v, unit):
@@ -139,3 +104,17 @@ def test_y_on_x(lib, m, k, n, block):
         launches = check(made(lib), block, x, k, m, y, n)
         clear = off + 2 * m * n <= 0 or off >= 2 * m * k
         assert launches[-1].kind == PAIRS or (len(launches) == 1) == clear
+
+
+@pytest.mark.parametrize("sms", [152, 148, 76])
+@pytest.mark.parametrize("gated", [False, True])
+def test_which_products_run_on_pairs(sms, gated):
+    """Never up to 64 tokens; always where there are more tiles of 128 weight rows and tokens than half of the SMs."""
+    for n in (8, 200, 1000, 2560, 10240, 128 * (sms // 2), 128 * (sms // 2) + 8):
+        first = first_on_pairs(n, 512, 32, gated, sms)
+        assert first > 64
+        assert product_kernels(first - 1, n, 512, 32, gated, sms) == FEW
+        half, rows = sms // 2, -(-n // 128)
+        assert -(-first // 64) * rows > half and (gated or -(-first // 128) * rows > half)
+        for m in (first + 1, 2 * first, 10 * first):
+            assert product_kernels(m, n, 512, 16, gated, sms) == PAIRS
