@@ -86,11 +86,11 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
   };
   if constexpr (BS == 16) {
     const int per = p.K >> 4, units = p.M * per;   // at most kBatch * kThreads
-    const uint32_t magic = 0xFFFFFFFFu / per + 1u;   // u / per = the high half of u magic: u per < 2^32
+    const uint32_t magic = 0xFFFFFFFFu / per + 1u;   // u / per = the high half of u magic: u per < 2^32, per >= 2
     Sixteen<T> v[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int u = j * kThreads + thread, r = per == 1 ? u : __umulhi(u, magic);
+      const int u = j * kThreads + thread, r = __umulhi(u, magic);
       v[j].clear();
       if (u < units) v[j].template load<true>(x + r * p.x_stride + (u - r * per) * 16);
     }
@@ -98,7 +98,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (j * kThreads >= units) break;
-      const int u = min(j * kThreads + thread, units - 1), r = per == 1 ? u : __umulhi(u, magic);
+      const int u = min(j * kThreads + thread, units - 1), r = __umulhi(u, magic);
       uint32_t top = v[j].top();
       if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
         top = __reduce_max_sync(0xffffffffu, top);
@@ -111,7 +111,7 @@ __device__ __forceinline__ void quantize_part(const RowsArgs& p, uint8_t* codes,
     if (thread < p.M) row[thread] = row_scale(most[thread]);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int u = j * kThreads + thread, r = per == 1 ? u : __umulhi(u, magic), k = (u - r * per) * 16;
+      const int u = j * kThreads + thread, r = __umulhi(u, magic), k = (u - r * per) * 16;
       if (u >= units || k < k0 || k >= kb1 * kFpStageK) continue;
       uint32_t c[2] = {0u, 0u}, byte = 0u;
       if (!not_finite(most[r])) byte = encode16<T, BS>(v[j], v[j].top(), pow2(-row_power(most[r])), c);
