@@ -499,6 +499,11 @@ __device__ __forceinline__ float ld_global_f32(const float* p) {
   return v;
 }
 
+__device__ __forceinline__ int ld_global_s32(const int* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 // Sixteen bytes that the launch before may have written: behind pdl_wait(), and through the coherent path
 // (ld_stream_v4's is for what no one writes while the kernel is there).
 __device__ __forceinline__ uint4 ld_global_v4(const void* p) {

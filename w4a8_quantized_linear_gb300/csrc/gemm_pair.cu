@@ -196,7 +196,7 @@ __device__ __forceinline__ bool pair_tile_fast(const PairArgs& a, int mt, int la
 #pragma unroll
   for (int i = 0; i < kPTileM / 32; ++i) {
     const int m = mt * kPTileM + i * 32 + lane;
-    if (m < a.M) mx = max(mx, __ldg(a.row_l1 + m));
+    if (m < a.M) mx = max(mx, ld_global_s32(a.row_l1 + m));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   return mx <= a.l1_limit;
@@ -528,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const int row = q * 32 + lane;   // token of this thread within the CTA's 128
       const int m = mt * kPTileM + static_cast<int>(rank) * kPHalf + row;
       const bool mvalid = m < p.M;
-      const float sam = (EPI != kEpiAcc && mvalid) ? __ldg(p.sa + m) : 0.0f;
+      const float sam = (EPI != kEpiAcc && mvalid) ? ld_global_f32(p.sa + m) : 0.0f;
       const int n_tile = nt * kPTileN;
       const bool piece = u.kind == kUnitPiece;
       // partial slot of a pair: 16-byte column group j of this thread's token

@@ -542,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         // c ^ (r & 7) (the TMA 128-byte swizzle)
         const int s_last = (tcount * p.nkb + p.nkb - 1) % S;
         const uint32_t ybuf = sA(s_last);
-        const float sam = mvalid ? __ldg(p.sa + m) : 0.0f;
+        const float sam = mvalid ? ld_global_f32(p.sa + m) : 0.0f;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {   // outputs 128 hcol + 8 c ... + 7 of the tile
           uint32_t hw[4];

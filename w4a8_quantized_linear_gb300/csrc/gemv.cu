@@ -609,13 +609,11 @@ int ring_slots(int64_t MB, int64_t K, bool mma = false) {
 // (acc * s_a) * s_w; per group the fp32 sum of the slices' partials, times
 // s_a unless the partials already carry it (tensor-core form).
 template <bool PG, bool PG_SCALED, bool BF16>
-__global__ void __launch_bounds__(256) gemv_combine_kernel(const uint32_t* __restrict__ part,
-                                                           int ks, int M, int64_t N,
-                                                           const float* __restrict__ sa,
-                                                           const float* __restrict__ sw,
-                                                           __half* __restrict__ y) {
+__global__ void __launch_bounds__(256) gemv_combine_kernel(const uint32_t* part, int ks, int M, int64_t N,
+                                                           const float* sa, const float* __restrict__ sw,
+                                                           __half* y) {
   const int64_t total = static_cast<int64_t>(M) * N;
-  pdl_wait();   // the partials are the GEMV's, launched just before
+  pdl_wait();   // the partials are the GEMV's, launched just before: nothing here but sw is constant for this kernel
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int m = static_cast<int>(i / N);
@@ -624,11 +622,11 @@ __global__ void __launch_bounds__(256) gemv_combine_kernel(const uint32_t* __res
       int v = 0;
       for (int s = 0; s < ks; ++s) v += static_cast<int>(part[s * total + i]);
       reinterpret_cast<uint16_t*>(y)[i] =
-          y_bits<BF16>(__fmul_rn(__fmul_rn(__int2float_rn(v), __ldg(sa + m)), __ldg(sw + n)));
+          y_bits<BF16>(__fmul_rn(__fmul_rn(__int2float_rn(v), ld_global_f32(sa + m)), __ldg(sw + n)));
     } else {
       float v = 0.0f;
       for (int s = 0; s < ks; ++s) v += __uint_as_float(part[s * total + i]);
-      reinterpret_cast<uint16_t*>(y)[i] = y_bits<BF16>(PG_SCALED ? v : __fmul_rn(v, __ldg(sa + m)));
+      reinterpret_cast<uint16_t*>(y)[i] = y_bits<BF16>(PG_SCALED ? v : __fmul_rn(v, ld_global_f32(sa + m)));
     }
   }
 }
