@@ -177,7 +177,8 @@ cudaError_t launch_quantize(const QuantArgs& p, int num_sms, cudaStream_t st, bo
   }
   // Long rows: two units a thread keep two CTAs or more on an SM, and half as many warps meet for a row's maximum.
   // bf16, block 16, one unit against two: 4096 x 4096 11.1 us, 10.0; 8192 x 12288 94, 57 (block 32: 48, 38); but fp16
-  // 4096 x 2560 7.6, 8.1.
+  // 4096 x 2560 7.6, 8.1.  Few rows, fp16, block 16: 64 x 4096 2.0, 2.2 (from 150 rows on no worse), 64 x 8192 2.4, 2.3,
+  // 64 x 12288 2.9, 2.7; block 32 1.7, 1.8 and 2.05, 1.9 and 2.4, 2.1.
   return p.K >= 4096 ? launch_rows<T, BS, 2>(p, num_sms, st, release) : launch_rows<T, BS, 1>(p, num_sms, st, release);
 }
 
@@ -199,8 +200,8 @@ __device__ __forceinline__ float2 e2m1_pair(uint32_t word, int byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// A thread reads 8 bytes of codes and writes 16 values, 32 bytes at a time (fp32 values 8 a thread, so that a
-// warp's store covers whole lines: 22.2 us for 10240 x 2560 in place of 20.1); rows by the CTA's second index.
+// A thread reads 8 bytes of codes and writes 16 values, 32 bytes at a time; rows by the CTA's second index.
+// (Eight values a thread for fp32, so that a warp's store covers whole lines: 22.2 us for 10240 x 2560, not 20.1.)
 template <typename T, int BS>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* codes, const uint8_t* scales,
                                                              const float* row, int64_t rows, int K, int tiles,

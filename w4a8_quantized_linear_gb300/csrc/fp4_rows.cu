@@ -12,7 +12,9 @@
 // FUSE: up to 16 tokens whose rows this kernel quantizes itself, each CTA the
 // part of K that it multiplies (block size 16 takes the row's maximum from the
 // whole row, which every CTA reads), into the operand's place in shared memory:
-// a decoding step's linear is one launch and needs no scratch.
+// a decoding step's linear is one launch and needs no scratch.  Block size 16
+// keeps all of x in registers, 16384 values at most: one token to K = 16384,
+// four to 4096; block size 32 parts of 32768 values.
 //
 // Warp 0 copies (weights' stages before x is there: they do not depend on it),
 // warp 1 issues scale copies and MMAs, the others quantize; warps 2..5 drain the
